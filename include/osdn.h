@@ -21,6 +21,14 @@
  * osdn_backward_kda (Phase 2 and the gradients with a decay per key channel,
  * the Kimi-Delta-Attention-style backbone of section 4).
  *
+ * Beside the delta rule, the plain layer with a decay per head, for models
+ * that mix the two: osdn_decay_attn, osdn_decay_attn_step and
+ * osdn_decay_attn_backward (linear attention: prompts, single tokens,
+ * gradients), osdn_group_norm and osdn_group_norm_backward (the norm with an
+ * activation behind either layer), and osdn_clip_grad_norm (the global
+ * gradient norm of a training step, and clipping by it).  These follow their
+ * formulas as stated at each call; the paper has no counterpart to them.
+ *
  * Conventions shared by every call
  * --------------------------------
  *  - All tensor pointers are DEVICE pointers owned by the caller; the
@@ -89,12 +97,18 @@ typedef enum {
     OSDN_ERR_TIMEOUT = -7,   /* device: a bounded wait ran out (status word)   */
     OSDN_ERR_DEVICE = -8,    /* device: an input checked on the device is invalid
                                 (osdn_chunk_fwd, bf16: a decay alpha that is not
-                                positive and finite, or a beta that is not finite) */
+                                positive and finite, or a beta that is not finite;
+                                osdn_decay_attn*: a decay outside [0, 1])      */
     OSDN_ERR_ALIAS = -9,     /* an output overlaps an input it must not alias  */
     OSDN_ERR_ARCH = -10,     /* the current device is not sm_103 (GB300)       */
-    OSDN_ERR_SCRATCH = -11   /* osdn_precond_scan_noalloc: shape needs more
+    OSDN_ERR_SCRATCH = -11,  /* osdn_precond_scan_noalloc: shape needs more
                                 scratch than its static buffer holds         */
+    OSDN_ERR_ARG = -12       /* a scalar argument is out of its range (eps, act,
+                                max_norm)                                     */
 } osdn_status;
+
+/* Activations of osdn_group_norm. */
+typedef enum { OSDN_ACT_NONE = 0, OSDN_ACT_SILU = 1, OSDN_ACT_SIGMOID = 2 } osdn_act;
 
 /* Bytes of workspace osdn_precond_scan needs for this shape (>= 256). */
 size_t osdn_precond_scan_workspace_bytes(int B, int H, int T, int K);
@@ -422,6 +436,125 @@ int osdn_decode_step_kda(int io, int B, int H, int K, int V, const void *q, cons
                          const void *v, const float *beta, const float *r, float eta,
                          const float *alpha_k, float *d, float *S, void *o, void *ktilde,
                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Bytes of workspace osdn_decay_attn needs for this shape (>= 256): where
+ * few sequences are cut into ranges of tokens that run side by side, one
+ * fp32 state (4 V K bytes) a range, at most a few hundred ranges.
+ */
+size_t osdn_decay_attn_workspace_bytes(int io, int B, int H, int T, int K, int V);
+
+/*
+ * Linear attention with a decay per head.  For each sequence (b,h), with
+ * a = decay[h] in [0, 1], from S_0 (S0, or zeros if S0 is NULL), for
+ * t = 1 .. T:
+ *     S_t = a S_{t-1} + v_t k_t^T,     o_t = S_t q_t
+ * that is, o_t = a^t S_0 q_t + sum_{s <= t} a^(t-s) (q_t . k_s) v_s.  The
+ * output is read from the state after token t and q is not scaled.
+ *
+ *   q, k  in  [B][H][T][K] io           v  in [B][H][T][V] io
+ *   decay in  [H] fp32, each in [0, 1]; anything else writes OSDN_ERR_DEVICE
+ *             into the status word and leaves the outputs undefined
+ *   S0    in  [B][H][V][K] fp32, or NULL (zeros)
+ *   o     out [B][H][T][V] io
+ *   ST    out [B][H][V][K] fp32, or NULL (not written)
+ * The state layout is that of osdn_chunk_fwd.  Inputs must be finite: inside
+ * a block of tokens a later token's infinity or NaN can reach earlier rows.
+ * With T == 0 the call writes ST = S0 and nothing else.  T may be at most
+ * 1,073,741,760.  Outputs must not overlap inputs, each other or the
+ * workspace (OSDN_ERR_ALIAS).  Results are the same on every run.
+ */
+int osdn_decay_attn(int io, int B, int H, int T, int K, int V, const void *q, const void *k,
+                    const void *v, const float *decay, const float *S0, void *o, float *ST,
+                    void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of osdn_decay_attn, in place: S <- a S + v k^T, o = S q.
+ *   q, k in [B][H][K] io     v in [B][H][V] io     decay in [H] fp32
+ *   S    in/out [B][H][V][K] fp32                  o out [B][H][V] io
+ * The workspace only carries the status word (>= 256 bytes).
+ */
+int osdn_decay_attn_step(int io, int B, int H, int K, int V, const void *q, const void *k,
+                         const void *v, const float *decay, float *S, void *o, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of L = <o, d_o> + <S_T, d_ST> through osdn_decay_attn with
+ * respect to q, k, v and S_0.  The decay is a constant of the model and has
+ * no gradient.  With X_T = d_ST, R_t = X_t + d_o_t q_t^T, X_{t-1} = a R_t:
+ *     dq_t = S_t^T d_o_t,   dk_t = R_t^T v_t,   dv_t = R_t k_t,   dS_0 = X_0
+ * (S_t is recomputed from k, v and S0).
+ *   d_o  in [B][H][T][V] io       d_ST in [B][H][V][K] fp32, or NULL (zeros)
+ *   dq, dk out [B][H][T][K] io    dv   out [B][H][T][V] io
+ *   dS0  out [B][H][V][K] fp32, or NULL (not written)
+ * The rest, and the limits, as osdn_decay_attn; with T == 0 the call writes
+ * dS0 = d_ST and nothing else.
+ */
+size_t osdn_decay_attn_backward_workspace_bytes(int io, int B, int H, int T, int K, int V);
+int osdn_decay_attn_backward(int io, int B, int H, int T, int K, int V, const void *q,
+                             const void *k, const void *v, const float *decay, const float *S0,
+                             const void *d_o, const float *d_ST, void *dq, void *dk, void *dv,
+                             float *dS0, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Group norm with an activation, channels last.  For every token (b,t) and
+ * group g of D channels, with m and s^2 the mean and (biased) variance of the
+ * group's D values,
+ *     z = weight (x - m) / sqrt(s^2 + eps) + bias
+ *     y = act(z)                 without a gate
+ *     y = z act(gate)            with one
+ * act: OSDN_ACT_NONE (u), OSDN_ACT_SILU (u sigmoid(u)) or OSDN_ACT_SIGMOID.
+ * Statistics belong to one token alone, so the norm is causal.
+ *
+ *   x      in  [B][T][G][D] io, or, with heads_first nonzero, [B][G][T][D]:
+ *              the layout in which the attention writes o
+ *   weight, bias in [G][D] fp32, each or both NULL (ones, zeros)
+ *   gate   in  [B][T][G][D] io, or NULL
+ *   y      out [B][T][G][D] io
+ * D is a multiple of 8 from 8 to 512; eps > 0 and finite.
+ */
+int osdn_group_norm(int io, int B, int G, int T, int D, int heads_first, const void *x,
+                    const float *weight, const float *bias, const void *gate, int act, float eps,
+                    void *y, void *stream);
+
+/*
+ * Gradients of osdn_group_norm given dy [B][T][G][D] io; x, weight, bias,
+ * gate, act and eps as in the forward call (its statistics are recomputed).
+ *   dx      out in x's layout, io       dgate out [B][T][G][D] io (required
+ *               with a gate, not written without one)
+ *   dweight, dbias out [G][D] fp32, each or both NULL (not written)
+ * The workspace holds each CTA's share of dweight and dbias, joined in a
+ * fixed order.  With B*T == 0 dweight and dbias are zeroed.
+ */
+size_t osdn_group_norm_backward_workspace_bytes(int B, int G, int T, int D);
+int osdn_group_norm_backward(int io, int B, int G, int T, int D, int heads_first, const void *x,
+                             const void *dy, const float *weight, const float *bias,
+                             const void *gate, int act, float eps, void *dx, void *dgate,
+                             float *dweight, float *dbias, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/*
+ * The global 2-norm of n tensors, and their clipping by it:
+ *     norm = sqrt(sum over all elements of g^2)
+ *     out_i = g_i min(1, max_norm / norm)
+ *
+ *   grads  host array of n device pointers; tensor i has sizes[i] elements
+ *          (up to 2^40, zero allowed) of type ios[i] (OSDN_F32 / OSDN_BF16)
+ *   outs   host array of n device pointers, of the same types; outs[i] may be
+ *          grads[i].  NULL: in place (nothing is written where norm <=
+ *          max_norm)
+ *   max_norm >= 0; infinity computes the norm alone (in place)
+ *   norm   out [1] fp32 on the device, or NULL
+ * A written tensor must not overlap any other tensor of the call; the call
+ * itself checks each outs[i] against its own grads[i], norm and the
+ * workspace.  An infinity or NaN in any gradient makes the norm infinite or
+ * NaN, and the scale 0 or NaN, as the formula says (0 times infinity is
+ * NaN).  The pointer arrays are read before the call returns.
+ */
+size_t osdn_clip_grad_norm_workspace_bytes(int n);
+int osdn_clip_grad_norm(int n, const void *const *grads, void *const *outs,
+                        const long long *sizes, const int *ios, float max_norm, float *norm,
+                        void *workspace, size_t workspace_bytes, void *stream);
 
 /* Zero the 256-byte status area at the start of a workspace (async). */
 int osdn_workspace_init(void *workspace, size_t workspace_bytes, void *stream);

@@ -1,0 +1,303 @@
+// decay_attn.cu -- linear attention with a decay per head, the token
+// recurrence in fp32 FFMA:
+//     S_t = a S_{t-1} + v_t k_t^T,   o_t = S_t q_t,   a = decay[h]
+// for fp32 I/O, where tensor-core operand rounding would not keep fp32
+// accuracy.
+//
+// The rows of S evolve independently, so a CTA of 128 threads takes 64 rows
+// of one range of the time axis: a thread holds two rows' columns 16m + 4p +
+// {0..3} (p = lane & 3), so that k and q come from shared memory as
+// broadcast 16-byte reads that serve two rows, and a row's dot product needs
+// two shuffles.  The decay costs no multiplication a token: over groups of
+// eight tokens the state is kept as S~ = a^-n S (v is scaled instead) and
+// multiplied by a^8 once a group; heads whose a^-8 would grow too large
+// (a < 1/16) decay token by token.
+#include "decay_attn.cuh"
+
+#include <algorithm>
+
+namespace osdn {
+namespace da {
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRows = 64;
+constexpr int kStage = 16;   // tokens staged at a time
+constexpr int kGroup = 8;    // tokens between rescalings
+constexpr int kUnit = 64;    // tokens a unit of the split
+
+struct Args {
+    Pass p;
+    Split s;
+    float *states;   // [G][V][K], see chain_states
+    int *status;
+};
+
+template <typename io_t, int K, bool STATE_ONLY>
+__global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
+    constexpr int M = K / 16;
+    __shared__ __align__(16) float ks[kStage][K], qs[STATE_ONLY ? 1 : kStage][K];
+    __shared__ __align__(8) float vs[kStage][kRows];
+    const Pass &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int pc = lane & 3, row = warp * 16 + (lane >> 2) * 2, row0 = blockIdx.x * kRows;
+    const int g = blockIdx.y + gridDim.y * blockIdx.z;
+    if (g >= a.s.G) return;
+    long long lo = a.s.lo(g, p.BH);
+    const long long hi = a.s.lo(g + 1, p.BH);
+    if (STATE_ONLY) {   // only the sequence that this range leaves unfinished
+        if (g + 1 >= a.s.G || hi % a.s.nch == 0) return;
+        lo = max(lo, hi / a.s.nch * a.s.nch);
+    }
+    const io_t *q = static_cast<const io_t *>(p.q), *k = static_cast<const io_t *>(p.k);
+    const io_t *v = static_cast<const io_t *>(p.v);
+    io_t *o = static_cast<io_t *>(p.o);
+
+    constexpr int NK = kStage * K / (kThreads * 4), NV = kStage * kRows / (kThreads * 4);
+    float rk[NK][4], rq[STATE_ONLY ? 1 : NK][4], rv[NV][4];
+    for (long long at = lo; at < hi;) {
+        const long long seq = at / a.s.nch;
+        const int u0 = (int)(at - seq * a.s.nch);
+        const int u1 = (int)min((long long)a.s.nch, u0 + (hi - at));
+        const int tbeg = u0 * kUnit, tend = min(p.T, u1 * kUnit);
+        at += u1 - u0;
+        const float dec = p.decay[seq % p.H];
+        if (!decay_ok(dec) && tid == 0) report_status(a.status, OSDN_ERR_DEVICE);
+        const float l2 = decay_log2(dec);
+        const bool grouped = dec >= 0.0625f;
+        const size_t kb = (size_t)seq * p.T * K, vb = (size_t)seq * p.T * p.V + row0;
+        auto fetch = [&](int t0) {   // the stage's tokens, in the pass's direction
+#pragma unroll
+            for (int n = 0; n < NK; ++n) {
+                const int idx = (tid + n * kThreads) * 4, t = t0 + idx / K;
+                const size_t r = kb + (size_t)(p.rev ? p.T - 1 - t : t) * K + idx % K;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) rk[n][e] = 0.0f;
+                if (t < tend) load4(k + r, rk[n]);
+                if (!STATE_ONLY) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) rq[n][e] = 0.0f;
+                    if (t < tend) load4(q + r, rq[n]);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+                const int idx = (tid + n * kThreads) * 4, t = t0 + idx / kRows;
+                const size_t r = vb + (size_t)(p.rev ? p.T - 1 - t : t) * p.V + idx % kRows;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) rv[n][e] = 0.0f;
+                if (t < tend) load4(v + r, rv[n]);
+            }
+        };
+        float2 S[2][M][2];
+        {
+            const size_t sb = (size_t)p.K * p.V;
+            const float *src = nullptr;
+            bool tr = false;
+            if (!STATE_ONLY && u0 > 0) {
+                src = a.states + (size_t)g * sb;
+            } else if (!STATE_ONLY && p.S0.p) {
+                src = p.S0.p + (size_t)seq * sb;
+                tr = p.S0.transposed;
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const int c = 16 * m + 4 * pc, i = row0 + row + r;
+                    if (src && !tr) load4(src + (size_t)i * K + c, x);
+                    if (src && tr) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = src[(size_t)(c + e) * p.V + i];
+                    }
+                    S[r][m][0] = make_float2(x[0], x[1]);
+                    S[r][m][1] = make_float2(x[2], x[3]);
+                }
+        }
+        auto scale = [&](float f) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) S[r][m][e] = __fmul2_rn(S[r][m][e], make_float2(f, f));
+        };
+        fetch(tbeg);
+        for (int t0 = tbeg; t0 < tend; t0 += kStage) {
+            __syncthreads();   // the last stage has been read
+#pragma unroll
+            for (int n = 0; n < NK; ++n) {
+                const int idx = (tid + n * kThreads) * 4;
+                store4(&ks[0][0] + idx, rk[n]);
+                if (!STATE_ONLY) store4(&qs[0][0] + idx, rq[n]);
+            }
+#pragma unroll
+            for (int n = 0; n < NV; ++n) store4(&vs[0][0] + (tid + n * kThreads) * 4, rv[n]);
+            __syncthreads();
+            if (t0 + kStage < tend) fetch(t0 + kStage);
+            const int tn = min(kStage, tend - t0);
+            for (int tt = 0; tt < tn; ++tt) {
+                // S_t = a^x S~ after this token, x counted from the group's start
+                const float x = (float)((tt & (kGroup - 1)) + (p.rev ? 0 : 1));
+                const float up = grouped ? decay_pow(l2, -x) : 1.0f;
+                if (!grouped && !p.rev) scale(dec);
+                const float2 vv = *reinterpret_cast<const float2 *>(&vs[tt][row]);
+                const float2 w0 = make_float2(up * vv.x, up * vv.x), w1 = make_float2(up * vv.y, up * vv.y);
+                float2 o0 = make_float2(0.0f, 0.0f), o1 = o0, o2 = o0, o3 = o0;
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const float4 kk = *reinterpret_cast<const float4 *>(&ks[tt][16 * m + 4 * pc]);
+                    const float2 ka = make_float2(kk.x, kk.y), kc = make_float2(kk.z, kk.w);
+                    S[0][m][0] = __ffma2_rn(w0, ka, S[0][m][0]);
+                    S[0][m][1] = __ffma2_rn(w0, kc, S[0][m][1]);
+                    S[1][m][0] = __ffma2_rn(w1, ka, S[1][m][0]);
+                    S[1][m][1] = __ffma2_rn(w1, kc, S[1][m][1]);
+                    if (!STATE_ONLY) {
+                        const float4 qq = *reinterpret_cast<const float4 *>(&qs[tt][16 * m + 4 * pc]);
+                        const float2 qa = make_float2(qq.x, qq.y), qc = make_float2(qq.z, qq.w);
+                        o0 = __ffma2_rn(S[0][m][0], qa, o0);
+                        o1 = __ffma2_rn(S[0][m][1], qc, o1);
+                        o2 = __ffma2_rn(S[1][m][0], qa, o2);
+                        o3 = __ffma2_rn(S[1][m][1], qc, o3);
+                    }
+                }
+                if (!STATE_ONLY) {
+                    float s0 = (o0.x + o0.y) + (o1.x + o1.y), s1 = (o2.x + o2.y) + (o3.x + o3.y);
+                    s0 += __shfl_xor_sync(kFullMask, s0, 1);
+                    s1 += __shfl_xor_sync(kFullMask, s1, 1);
+                    s0 += __shfl_xor_sync(kFullMask, s0, 2);
+                    s1 += __shfl_xor_sync(kFullMask, s1, 2);
+                    const float down = grouped ? decay_pow(l2, x) : 1.0f;
+                    const int t = t0 + tt;
+                    if (pc == 0) {
+                        const float y[2] = {down * s0, down * s1};
+                        store2(o + vb + (size_t)(p.rev ? p.T - 1 - t : t) * p.V + row, y);
+                    }
+                }
+                if (!grouped && p.rev) scale(dec);
+                if (grouped && ((tt & (kGroup - 1)) == kGroup - 1 || tt == tn - 1))
+                    scale(decay_pow(l2, (float)((tt & (kGroup - 1)) + 1)));
+            }
+        }
+        float *dst = nullptr;
+        bool tr = false;
+        const size_t sb = (size_t)p.K * p.V;
+        if (STATE_ONLY) {
+            dst = a.states + (size_t)(g + 1) * sb;
+        } else if (tend == p.T && p.ST.p) {
+            dst = p.ST.p + (size_t)seq * sb;
+            tr = p.ST.transposed;
+        }
+        if (dst) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const int c = 16 * m + 4 * pc, i = row0 + row + r;
+                    const float x[4] = {S[r][m][0].x, S[r][m][0].y, S[r][m][1].x, S[r][m][1].y};
+                    if (!tr) {
+                        store4(dst + (size_t)i * K + c, x);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) dst[(size_t)(c + e) * p.V + i] = x[e];
+                    }
+                }
+        }
+    }
+}
+
+// One thread per four state elements of a sequence: the states entering the
+// sequence's ranges, one after another.
+__global__ void __launch_bounds__(256) chain_states_kernel(Pass p, Split s, float *states) {
+    const size_t seq = grid_seq();
+    if (seq >= (size_t)p.BH) return;
+    const int n = p.K * p.V;
+    const int e = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
+    if (e >= n) return;
+    const long long beg = (long long)seq * s.nch, end = beg + s.nch;
+    // the first range that starts inside this sequence: the least g with lo(g) > beg
+    const long long N = (long long)p.BH * s.nch;
+    long long g = beg * s.G / N;
+    while (s.lo((int)g, p.BH) <= beg) ++g;
+    if (s.lo((int)g, p.BH) >= end) return;
+    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (p.S0.p) {
+        const float *src = p.S0.p + seq * n;
+        if (!p.S0.transposed) {
+            load4(src + e, c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = src[(size_t)(e % p.K + i) * p.V + e / p.K];
+        }
+    }
+    const float l2 = decay_log2(p.decay[seq % p.H]);
+    long long from = beg;
+    for (;;) {
+        const long long at = s.lo((int)g, p.BH);
+        if (at >= end) break;
+        // units are whole in the pass's direction except the sequence's last one, which no range
+        // that is followed by another holds
+        float *st = states + (size_t)g * n + e;
+        float x[4];
+        load4(st, x);
+        const float f = decay_pow(l2, (float)((at - from) * s.unit));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = fmaf(f, c[i], x[i]);
+        store4(st, c);
+        from = at;
+        ++g;
+    }
+}
+
+template <typename io_t, int K>
+cudaError_t launch_simt(const Args &a, cudaStream_t stream) {
+    const dim3 grid = seq_grid(a.p.V / kRows, a.s.G);
+    if (!unsplit(a.s, a.p.BH)) {
+        attend_simt_kernel<io_t, K, true><<<grid, kThreads, 0, stream>>>(a);
+        cudaError_t e = cudaGetLastError();
+        if (e == cudaSuccess) e = chain_states(a.p, a.s, a.states, stream);
+        if (e != cudaSuccess) return e;
+    }
+    attend_simt_kernel<io_t, K, false><<<grid, kThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t chain_states(const Pass &p, const Split &s, float *states, cudaStream_t stream) {
+    const dim3 grid = seq_grid((p.K * p.V / 4 + 255) / 256, p.BH);
+    chain_states_kernel<<<grid, 256, 0, stream>>>(p, s, states);
+    return cudaGetLastError();
+}
+
+Split simt_split(int BH, int T, int K, int V) {
+    Split s;
+    s.unit = kUnit;
+    s.nch = (T + kUnit - 1) / kUnit;
+    s.G = BH;
+    const long long slots = 152LL * 3 / (V / kRows);   // CTAs resident at once, in ranges
+    const long long N = (long long)BH * s.nch, G = std::min(N, slots);
+    // units in a row, one by one: a split pass costs about two thirds more, and two launches
+    // (about 16 units' time)
+    const long long whole = (BH + slots - 1) / slots * s.nch;
+    const long long split = (N + G - 1) / G * 5 / 3 + 16;
+    if (G > BH && split < whole) s.G = (int)G;
+    return s;
+}
+
+cudaError_t attend_simt(int io, const Pass &p, void *scratch, int *status, cudaStream_t stream) {
+    Args a;
+    a.p = p;
+    a.s = simt_split(p.BH, p.T, p.K, p.V);
+    a.states = static_cast<float *>(scratch);
+    a.status = status;
+    if (io == OSDN_F32)
+        return p.K == 128 ? launch_simt<float, 128>(a, stream) : launch_simt<float, 64>(a, stream);
+    return p.K == 128 ? launch_simt<__nv_bfloat16, 128>(a, stream)
+                      : launch_simt<__nv_bfloat16, 64>(a, stream);
+}
+
+}  // namespace da
+}  // namespace osdn

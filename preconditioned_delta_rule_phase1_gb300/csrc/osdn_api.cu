@@ -164,6 +164,7 @@ const char *osdn_status_string(int code) {
     case OSDN_ERR_ALIAS: return "output overlaps an input";
     case OSDN_ERR_ARCH: return "device is not sm_103 (GB300)";
     case OSDN_ERR_SCRATCH: return "problem needs more scratch than the static buffer holds";
+    case OSDN_ERR_ARG: return "a scalar argument is out of its range";
     default: return "unknown status";
     }
 }

@@ -22,6 +22,7 @@ import torch
 from . import build as _build
 
 OSDN_F32, OSDN_BF16 = 0, 1
+ACTS = {"none": 0, "silu": 1, "sigmoid": 2}
 STATUS_BYTES = 256
 _lock = threading.Lock()
 _lib = None
@@ -63,6 +64,24 @@ _SIGS = {
                      [ctypes.c_void_p] * 7 + [ctypes.c_size_t, ctypes.c_void_p]),
     "osdn_chunk_fwd_kda": (ctypes.c_int, [ctypes.c_int] * 6 + [ctypes.c_void_p] * 10 +
                            [ctypes.c_size_t, ctypes.c_void_p]),
+    "osdn_decay_attn_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 6),
+    "osdn_decay_attn": (ctypes.c_int, [ctypes.c_int] * 6 + [ctypes.c_void_p] * 8 +
+                        [ctypes.c_size_t, ctypes.c_void_p]),
+    "osdn_decay_attn_step": (ctypes.c_int, [ctypes.c_int] * 5 + [ctypes.c_void_p] * 7 +
+                             [ctypes.c_size_t, ctypes.c_void_p]),
+    "osdn_decay_attn_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 6),
+    "osdn_decay_attn_backward": (ctypes.c_int, [ctypes.c_int] * 6 + [ctypes.c_void_p] * 12 +
+                                 [ctypes.c_size_t, ctypes.c_void_p]),
+    "osdn_group_norm": (ctypes.c_int, [ctypes.c_int] * 6 + [ctypes.c_void_p] * 4 +
+                        [ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p]),
+    "osdn_group_norm_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 4),
+    "osdn_group_norm_backward": (ctypes.c_int, [ctypes.c_int] * 6 + [ctypes.c_void_p] * 5 +
+                                 [ctypes.c_int, ctypes.c_float] + [ctypes.c_void_p] * 5 +
+                                 [ctypes.c_size_t, ctypes.c_void_p]),
+    "osdn_clip_grad_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int]),
+    "osdn_clip_grad_norm": (ctypes.c_int, [ctypes.c_int] + [ctypes.c_void_p] * 4 +
+                            [ctypes.c_float] + [ctypes.c_void_p] * 2 +
+                            [ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 
@@ -488,3 +507,211 @@ def forward_kda(q, k, v, beta, r=None, eta=0.1, d0=None, alpha_k=None, S0=None, 
     ktilde, dT = precond_scan(k, beta, r, eta, d0, workspace=ws, stream=stream)
     o, ST = chunk_fwd_kda(q, k, ktilde, v, beta, alpha_k, S0, workspace=ws, stream=stream)
     return ktilde, dT, o, ST
+
+
+def decay_attn_workspace_bytes(io, B, H, T, K, V) -> int:
+    return int(lib().osdn_decay_attn_workspace_bytes(io, B, H, T, K, V))
+
+
+def decay_attn_backward_workspace_bytes(io, B, H, T, K, V) -> int:
+    return int(lib().osdn_decay_attn_backward_workspace_bytes(io, B, H, T, K, V))
+
+
+def group_norm_backward_workspace_bytes(B, G, T, D) -> int:
+    return int(lib().osdn_group_norm_backward_workspace_bytes(B, G, T, D))
+
+
+def clip_grad_norm_workspace_bytes(n) -> int:
+    return int(lib().osdn_clip_grad_norm_workspace_bytes(n))
+
+
+def decay_attn(q, k, v, decay, S0=None, o=None, ST=None, workspace=None, stream=None):
+    """Linear attention with a decay per head (osdn_decay_attn), q, k [B,H,T,K],
+    v [B,H,T,V] (io), decay [H] fp32 in [0, 1], S0 [B,H,V,K] fp32 or None:
+    returns (o, ST)."""
+    B, H, T, K = k.shape
+    V = v.shape[-1]
+    io, dev = _io(k), k.device
+    _expect("q", q, (B, H, T, K), k.dtype, dev)
+    _expect("k", k, (B, H, T, K), k.dtype, dev)
+    _expect("v", v, (B, H, T, V), k.dtype, dev)
+    _expect("decay", decay, (H,), F32, dev)
+    _expect("S0", S0, (B, H, V, K), F32, dev)
+    if o is None:
+        o = torch.empty(B, H, T, V, dtype=k.dtype, device=dev)
+    if ST is None:
+        ST = torch.empty(B, H, V, K, dtype=F32, device=dev)
+    _expect("o", o, (B, H, T, V), k.dtype, dev)
+    _expect("ST", ST, (B, H, V, K), F32, dev)
+    ws = _workspace(workspace, dev)
+    with _on(dev):
+        ws.ensure(decay_attn_workspace_bytes(io, B, H, T, K, V))
+        code = lib().osdn_decay_attn(io, B, H, T, K, V, _ptr(q), _ptr(k), _ptr(v), _ptr(decay),
+                                     _ptr(S0), _ptr(o), _ptr(ST), ws.ptr, ws.nbytes,
+                                     _stream(stream, dev))
+    _check(code, "osdn_decay_attn")
+    return o, ST
+
+
+def decay_attn_step(q, k, v, decay, S, o=None, workspace=None, stream=None):
+    """One token of ``decay_attn`` (osdn_decay_attn_step): updates S [B,H,V,K]
+    (fp32) in place for the token q, k [B,H,K], v [B,H,V] (io); returns o."""
+    B, H, K = k.shape
+    V = v.shape[-1]
+    io, dev = _io(k), k.device
+    _expect("q", q, (B, H, K), k.dtype, dev)
+    _expect("k", k, (B, H, K), k.dtype, dev)
+    _expect("v", v, (B, H, V), k.dtype, dev)
+    _expect("decay", decay, (H,), F32, dev)
+    _expect("S", S, (B, H, V, K), F32, dev)
+    if o is None:
+        o = torch.empty(B, H, V, dtype=k.dtype, device=dev)
+    _expect("o", o, (B, H, V), k.dtype, dev)
+    ws = _workspace(workspace, dev)
+    with _on(dev):
+        code = lib().osdn_decay_attn_step(io, B, H, K, V, _ptr(q), _ptr(k), _ptr(v), _ptr(decay),
+                                          _ptr(S), _ptr(o), ws.ptr, ws.nbytes,
+                                          _stream(stream, dev))
+    _check(code, "osdn_decay_attn_step")
+    return o
+
+
+def decay_attn_backward(q, k, v, decay, S0=None, *, do, dST=None, workspace=None, stream=None):
+    """Gradients through ``decay_attn`` (osdn_decay_attn_backward) given the
+    cotangents do [B,H,T,V] (io) of o and dST [B,H,V,K] fp32 of ST (None: zero).
+    Returns a dict with q, k, v (io) and, if S0 is given, S0 (fp32).  The decay
+    is a constant and has no gradient."""
+    B, H, T, K = k.shape
+    V = v.shape[-1]
+    io, dev = _io(k), k.device
+    _expect("q", q, (B, H, T, K), k.dtype, dev)
+    _expect("k", k, (B, H, T, K), k.dtype, dev)
+    _expect("v", v, (B, H, T, V), k.dtype, dev)
+    _expect("decay", decay, (H,), F32, dev)
+    _expect("S0", S0, (B, H, V, K), F32, dev)
+    _expect("do", do, (B, H, T, V), k.dtype, dev)
+    _expect("dST", dST, (B, H, V, K), F32, dev)
+    g = {"q": torch.empty_like(k), "k": torch.empty_like(k), "v": torch.empty_like(v)}
+    if S0 is not None:
+        g["S0"] = torch.empty_like(S0)
+    ws = _workspace(workspace, dev)
+    with _on(dev):
+        ws.ensure(decay_attn_backward_workspace_bytes(io, B, H, T, K, V))
+        code = lib().osdn_decay_attn_backward(
+            io, B, H, T, K, V, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0), _ptr(do),
+            _ptr(dST), _ptr(g["q"]), _ptr(g["k"]), _ptr(g["v"]), _ptr(g.get("S0")), ws.ptr,
+            ws.nbytes, _stream(stream, dev))
+    _check(code, "osdn_decay_attn_backward")
+    return g
+
+
+def _norm_shape(x, groups):
+    """(B, G, T, D, heads_first) of a group norm's input: [B,G,T,D] (four
+    dimensions), or [B,T,C] with `groups`."""
+    if x.dim() == 4:
+        B, G, T, D = x.shape
+        if groups is not None and groups != G:
+            raise ValueError("x has %d groups, groups is %s" % (G, groups))
+        return B, G, T, D, 1
+    if x.dim() != 3:
+        raise ValueError("x must be [B,G,T,D] or [B,T,C], got shape %s" % (tuple(x.shape),))
+    B, T, C = x.shape
+    if not groups or groups < 0 or C % groups:
+        raise ValueError("groups (%s) must divide the %d channels of x" % (groups, C))
+    return B, groups, T, C // groups, 0
+
+
+def _norm_inputs(x, weight, bias, gate, groups, act):
+    if act not in ACTS:
+        raise ValueError("act must be one of %s, got %r" % (sorted(ACTS), act))
+    B, G, T, D, first = _norm_shape(x, groups)
+    io, dev = _io(x), x.device
+    _expect("x", x, x.shape, x.dtype, dev)
+    _expect("weight", weight, (G * D,), F32, dev)
+    _expect("bias", bias, (G * D,), F32, dev)
+    _expect("gate", gate, (B, T, G * D), x.dtype, dev)
+    return io, B, G, T, D, first, dev
+
+
+def group_norm(x, weight=None, bias=None, gate=None, groups=None, act="none", eps=1e-5, y=None,
+               stream=None):
+    """Group norm of every token with an activation (osdn_group_norm).
+
+    x is the attention's output [B,H,T,D] (a group is a head) or channels last
+    [B,T,C] with `groups`; weight, bias [C] fp32; gate [B,T,C] (io).  Returns
+    y [B,T,C] = act(norm(x)), or norm(x) act(gate) with a gate; act is "none",
+    "silu" or "sigmoid"."""
+    io, B, G, T, D, first, dev = _norm_inputs(x, weight, bias, gate, groups, act)
+    if y is None:
+        y = torch.empty(B, T, G * D, dtype=x.dtype, device=dev)
+    _expect("y", y, (B, T, G * D), x.dtype, dev)
+    with _on(dev):
+        code = lib().osdn_group_norm(io, B, G, T, D, first, _ptr(x), _ptr(weight), _ptr(bias),
+                                     _ptr(gate), ACTS[act], float(eps), _ptr(y),
+                                     _stream(stream, dev))
+    _check(code, "osdn_group_norm")
+    return y
+
+
+def group_norm_backward(x, dy, weight=None, bias=None, gate=None, groups=None, act="none",
+                        eps=1e-5, workspace=None, stream=None):
+    """Gradients of ``group_norm`` (osdn_group_norm_backward) given dy [B,T,C]:
+    a dict with x (in x's layout) and weight, bias, gate for those given."""
+    io, B, G, T, D, first, dev = _norm_inputs(x, weight, bias, gate, groups, act)
+    _expect("dy", dy, (B, T, G * D), x.dtype, dev)
+    g = {"x": torch.empty_like(x)}
+    for name, t in (("weight", weight), ("bias", bias), ("gate", gate)):
+        if t is not None:
+            g[name] = torch.empty_like(t)
+    ws = _workspace(workspace, dev)
+    with _on(dev):
+        ws.ensure(group_norm_backward_workspace_bytes(B, G, T, D))
+        code = lib().osdn_group_norm_backward(
+            io, B, G, T, D, first, _ptr(x), _ptr(dy), _ptr(weight), _ptr(bias), _ptr(gate),
+            ACTS[act], float(eps), _ptr(g["x"]), _ptr(g.get("gate")), _ptr(g.get("weight")),
+            _ptr(g.get("bias")), ws.ptr, ws.nbytes, _stream(stream, dev))
+    _check(code, "osdn_group_norm_backward")
+    return g
+
+
+def clip_grad_norm(grads, max_norm, outs=None, norm=None, workspace=None, stream=None):
+    """Clip tensors by their global 2-norm (osdn_clip_grad_norm): every g becomes
+    g min(1, max_norm / norm), in place, or in `outs` (tensors like `grads`).
+    Returns norm [1] fp32 on the device.  max_norm = inf: the norm alone."""
+    grads = list(grads)
+    n = len(grads)
+    if n == 0 and norm is None:
+        raise ValueError("no gradients and no norm tensor: the device is unknown")
+    dev = grads[0].device if n else norm.device
+    ios, sizes = (ctypes.c_int * n)(), (ctypes.c_longlong * n)()
+    gp, op = (ctypes.c_void_p * n)(), None
+    for i, g in enumerate(grads):
+        if g.device != dev or not g.is_contiguous():
+            _expect("grads[%d]" % i, g, g.shape, g.dtype, dev)
+        ios[i], sizes[i], gp[i] = _io(g), g.numel(), g.data_ptr()
+    if outs is not None:
+        outs = list(outs)
+        if len(outs) != n:
+            raise ValueError("%d gradients, %d outputs" % (n, len(outs)))
+        op = (ctypes.c_void_p * n)()
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            _expect("outs[%d]" % i, o, g.shape, g.dtype, dev)
+            op[i] = o.data_ptr()
+    written = [p for p, s in zip(gp if op is None else op, sizes) if s]
+    if len(set(written)) != len(written):
+        raise ValueError("a tensor is written twice")
+    if norm is None:
+        norm = torch.empty(1, dtype=F32, device=dev)
+    _expect("norm", norm, (1,), F32, dev)
+    ws = _workspace(workspace, dev)
+    with _on(dev):
+        ws.ensure(clip_grad_norm_workspace_bytes(n))
+        code = lib().osdn_clip_grad_norm(n, gp, op, sizes, ios, float(max_norm), _ptr(norm),
+                                         ws.ptr, ws.nbytes, _stream(stream, dev))
+    _check(code, "osdn_clip_grad_norm")
+    return norm
+
+
+def grad_norm(grads, norm=None, workspace=None, stream=None):
+    """The global 2-norm of the tensors, [1] fp32 on the device."""
+    return clip_grad_norm(grads, float("inf"), norm=norm, workspace=workspace, stream=stream)
