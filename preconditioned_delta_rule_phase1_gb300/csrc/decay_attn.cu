@@ -34,11 +34,12 @@ struct Args {
     int *status;
 };
 
-template <typename io_t, int K, bool STATE_ONLY>
+template <int K, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
     constexpr int M = K / 16;
     __shared__ __align__(16) float ks[kStage][K], qs[STATE_ONLY ? 1 : kStage][K];
     __shared__ __align__(8) float vs[kStage][kRows];
+    __shared__ Pow pows[kGroup + 1];
     const Pass &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pc = lane & 3, row = warp * 16 + (lane >> 2) * 2, row0 = blockIdx.x * kRows;
@@ -50,9 +51,9 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
         if (g + 1 >= a.s.G || hi % a.s.nch == 0) return;
         lo = max(lo, hi / a.s.nch * a.s.nch);
     }
-    const io_t *q = static_cast<const io_t *>(p.q), *k = static_cast<const io_t *>(p.k);
-    const io_t *v = static_cast<const io_t *>(p.v);
-    io_t *o = static_cast<io_t *>(p.o);
+    const float *q = static_cast<const float *>(p.q), *k = static_cast<const float *>(p.k);
+    const float *v = static_cast<const float *>(p.v);
+    float *o = static_cast<float *>(p.o);
 
     constexpr int NK = kStage * K / (kThreads * 4), NV = kStage * kRows / (kThreads * 4);
     float rk[NK][4], rq[STATE_ONLY ? 1 : NK][4], rv[NV][4];
@@ -64,7 +65,6 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
         at += u1 - u0;
         const float dec = p.decay[seq % p.H];
         if (!decay_ok(dec) && tid == 0) report_status(a.status, OSDN_ERR_DEVICE);
-        const float l2 = decay_log2(dec);
         const bool grouped = dec >= 0.0625f;
         const size_t kb = (size_t)seq * p.T * K, vb = (size_t)seq * p.T * p.V + row0;
         auto fetch = [&](int t0) {   // the stage's tokens, in the pass's direction
@@ -116,14 +116,18 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
                     S[r][m][1] = make_float2(x[2], x[3]);
                 }
         }
-        auto scale = [&](float f) {
+        auto scale = [&](Pow f) {
+            const float2 h = make_float2(f.hi, f.hi), l = make_float2(f.lo, f.lo);
 #pragma unroll
             for (int r = 0; r < 2; ++r)
 #pragma unroll
                 for (int m = 0; m < M; ++m)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) S[r][m][e] = __fmul2_rn(S[r][m][e], make_float2(f, f));
+                    for (int e = 0; e < 2; ++e)
+                        S[r][m][e] = __ffma2_rn(h, S[r][m][e], __fmul2_rn(l, S[r][m][e]));
         };
+        __syncthreads();   // the last sequence's powers have been read
+        if (tid <= kGroup) pows[tid] = decay_pow(dec, tid);
         fetch(tbeg);
         for (int t0 = tbeg; t0 < tend; t0 += kStage) {
             __syncthreads();   // the last stage has been read
@@ -140,9 +144,9 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
             const int tn = min(kStage, tend - t0);
             for (int tt = 0; tt < tn; ++tt) {
                 // S_t = a^x S~ after this token, x counted from the group's start
-                const float x = (float)((tt & (kGroup - 1)) + (p.rev ? 0 : 1));
-                const float up = grouped ? decay_pow(l2, -x) : 1.0f;
-                if (!grouped && !p.rev) scale(dec);
+                const int in = tt & (kGroup - 1), x = in + (p.rev ? 0 : 1);
+                const float down = grouped ? pows[x].hi : 1.0f, up = 1.0f / down;
+                if (!grouped && !p.rev) scale(pows[1]);
                 const float2 vv = *reinterpret_cast<const float2 *>(&vs[tt][row]);
                 const float2 w0 = make_float2(up * vv.x, up * vv.x), w1 = make_float2(up * vv.y, up * vv.y);
                 float2 o0 = make_float2(0.0f, 0.0f), o1 = o0, o2 = o0, o3 = o0;
@@ -169,16 +173,14 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
                     s1 += __shfl_xor_sync(kFullMask, s1, 1);
                     s0 += __shfl_xor_sync(kFullMask, s0, 2);
                     s1 += __shfl_xor_sync(kFullMask, s1, 2);
-                    const float down = grouped ? decay_pow(l2, x) : 1.0f;
                     const int t = t0 + tt;
                     if (pc == 0) {
                         const float y[2] = {down * s0, down * s1};
                         store2(o + vb + (size_t)(p.rev ? p.T - 1 - t : t) * p.V + row, y);
                     }
                 }
-                if (!grouped && p.rev) scale(dec);
-                if (grouped && ((tt & (kGroup - 1)) == kGroup - 1 || tt == tn - 1))
-                    scale(decay_pow(l2, (float)((tt & (kGroup - 1)) + 1)));
+                if (!grouped && p.rev) scale(pows[1]);
+                if (grouped && (in == kGroup - 1 || tt == tn - 1)) scale(pows[in + 1]);
             }
         }
         float *dst = nullptr;
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(256) chain_states_kernel(Pass p, Split s, floa
             for (int i = 0; i < 4; ++i) c[i] = src[(size_t)(e % p.K + i) * p.V + e / p.K];
         }
     }
-    const float l2 = decay_log2(p.decay[seq % p.H]);
+    const float dec = p.decay[seq % p.H];
     long long from = beg;
     for (;;) {
         const long long at = s.lo((int)g, p.BH);
@@ -242,25 +244,25 @@ __global__ void __launch_bounds__(256) chain_states_kernel(Pass p, Split s, floa
         float *st = states + (size_t)g * n + e;
         float x[4];
         load4(st, x);
-        const float f = decay_pow(l2, (float)((at - from) * s.unit));
+        const Pow f = decay_pow(dec, (unsigned)((at - from) * s.unit));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = fmaf(f, c[i], x[i]);
+        for (int i = 0; i < 4; ++i) c[i] = fmaf(f.hi, c[i], fmaf(f.lo, c[i], x[i]));
         store4(st, c);
         from = at;
         ++g;
     }
 }
 
-template <typename io_t, int K>
+template <int K>
 cudaError_t launch_simt(const Args &a, cudaStream_t stream) {
     const dim3 grid = seq_grid(a.p.V / kRows, a.s.G);
     if (!unsplit(a.s, a.p.BH)) {
-        attend_simt_kernel<io_t, K, true><<<grid, kThreads, 0, stream>>>(a);
+        attend_simt_kernel<K, true><<<grid, kThreads, 0, stream>>>(a);
         cudaError_t e = cudaGetLastError();
         if (e == cudaSuccess) e = chain_states(a.p, a.s, a.states, stream);
         if (e != cudaSuccess) return e;
     }
-    attend_simt_kernel<io_t, K, false><<<grid, kThreads, 0, stream>>>(a);
+    attend_simt_kernel<K, false><<<grid, kThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -287,16 +289,13 @@ Split simt_split(int BH, int T, int K, int V) {
     return s;
 }
 
-cudaError_t attend_simt(int io, const Pass &p, void *scratch, int *status, cudaStream_t stream) {
+cudaError_t attend_simt(const Pass &p, void *scratch, int *status, cudaStream_t stream) {
     Args a;
     a.p = p;
     a.s = simt_split(p.BH, p.T, p.K, p.V);
     a.states = static_cast<float *>(scratch);
     a.status = status;
-    if (io == OSDN_F32)
-        return p.K == 128 ? launch_simt<float, 128>(a, stream) : launch_simt<float, 64>(a, stream);
-    return p.K == 128 ? launch_simt<__nv_bfloat16, 128>(a, stream)
-                      : launch_simt<__nv_bfloat16, 64>(a, stream);
+    return p.K == 128 ? launch_simt<128>(a, stream) : launch_simt<64>(a, stream);
 }
 
 }  // namespace da

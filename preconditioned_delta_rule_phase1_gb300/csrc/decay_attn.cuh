@@ -46,9 +46,26 @@ struct Split {
     }
 };
 
-// a^n for n >= 0 from log2(a) (a = 0: 0^0 = 1).
-__device__ __forceinline__ float decay_log2(float a) { return fmaxf(log2f(a), -1e30f); }
-__device__ __forceinline__ float decay_pow(float l2, float n) { return exp2f(n * l2); }
+// a^n to about 46 bits as an unevaluated sum of two fp32 (0^0 = 1), by
+// repeated squaring: a state that lives through thousands of decays would
+// otherwise carry their common rounding error thousands of times.
+struct Pow {
+    float hi, lo;
+};
+__device__ __forceinline__ Pow pow_mul(Pow x, Pow y) {
+    const float p = x.hi * y.hi;
+    const float e = fmaf(x.hi, y.hi, -p) + fmaf(x.hi, y.lo, x.lo * y.hi);
+    const float h = p + e;
+    return {h, e - (h - p)};
+}
+__device__ __forceinline__ Pow decay_pow(float a, unsigned n) {
+    Pow r = {1.0f, 0.0f}, b = {a, 0.0f};
+    for (; n; n >>= 1) {
+        if (n & 1) r = pow_mul(r, b);
+        b = pow_mul(b, b);
+    }
+    return r;
+}
 __device__ __forceinline__ bool decay_ok(float a) { return a >= 0.0f && a <= 1.0f; }
 
 // Bytes of the ranges' states ([G][V][K] fp32; none for a single range a sequence).
@@ -62,8 +79,11 @@ inline bool unsplit(const Split &s, int BH) { return s.G == BH; }
 // out, the state entering range g (ranges that start a sequence: untouched).
 cudaError_t chain_states(const Pass &p, const Split &s, float *states, cudaStream_t stream);
 
+// The token recurrence (fp32 I/O) and the chunked tensor-core form (bf16 I/O).
 Split simt_split(int BH, int T, int K, int V);
-cudaError_t attend_simt(int io, const Pass &p, void *scratch, int *status, cudaStream_t stream);
+cudaError_t attend_simt(const Pass &p, void *scratch, int *status, cudaStream_t stream);
+Split tc_split(int BH, int T, int K, int V);
+cudaError_t attend_tc(const Pass &p, void *scratch, int *status, cudaStream_t stream);
 
 }  // namespace da
 }  // namespace osdn

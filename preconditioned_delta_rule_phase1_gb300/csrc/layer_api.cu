@@ -96,11 +96,12 @@ osdn::da::State state(const float *p, int transposed = 0) {
 }
 
 size_t attend_bytes(int io, int BH, int T, int K, int V) {
-    (void)io;
-    return osdn::da::split_bytes(osdn::da::simt_split(BH, T, K, V), BH, K, V);
+    using namespace osdn::da;
+    return split_bytes(io == OSDN_F32 ? simt_split(BH, T, K, V) : tc_split(BH, T, K, V), BH, K, V);
 }
 cudaError_t attend(int io, const osdn::da::Pass &p, void *scratch, int *status, cudaStream_t stream) {
-    return osdn::da::attend_simt(io, p, scratch, status, stream);
+    return io == OSDN_F32 ? osdn::da::attend_simt(p, scratch, status, stream)
+                          : osdn::da::attend_tc(p, scratch, status, stream);
 }
 
 }  // namespace

@@ -195,9 +195,9 @@ __device__ __forceinline__ uint8_t *align1024(uint8_t *raw) {
 
 // ----------------------------------------------------------------------- host
 bool tensor_map_encoder_ready();
-// [BH][rows][width] bf16 in global memory, boxes of 64 columns x 64 rows,
-// 128-byte swizzle; rows past `rows` read as zero.
-bool make_map(CUtensorMap *m, const void *ptr, int BH, int rows, int width);
+// [BH][rows][width] bf16 in global memory, boxes of 64 columns x `box_rows`
+// rows, 128-byte swizzle; rows outside [0, rows) read as zero.
+bool make_map(CUtensorMap *m, const void *ptr, int BH, int rows, int width, int box_rows = C);
 // Streaming multiprocessors of the current device (152 if the query fails).
 int sm_count();
 // Extra inputs of the chunk preparation: the fused forward pass's

@@ -224,3 +224,18 @@ def test_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, -want[0]) and torch.equal(ST, -want[1])
+
+
+def test_a_wait_that_runs_out_is_reported():
+    # while the workspace's test word is nonzero the bf16 kernel loads nothing and its waits
+    # are shortened: they run out, the status says so and the device stays usable
+    x = inputs(1, 2, 300, 64, 64, "bf16", seed=3)
+    want = forward(x)
+    ws = ops.Workspace()
+    ws.ensure(ops.decay_attn_workspace_bytes(1, 1, 2, 300, 64, 64))
+    ws.buf[4] = 1
+    forward(x, ws)
+    assert ws.status() == -7
+    ws.reset()
+    o, ST = forward(x, ws)
+    assert ws.status() == 0 and torch.equal(o, want[0]) and torch.equal(ST, want[1])
