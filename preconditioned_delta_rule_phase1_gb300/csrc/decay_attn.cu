@@ -239,12 +239,11 @@ __global__ void __launch_bounds__(256) chain_states_kernel(Pass p, Split s, floa
     for (;;) {
         const long long at = s.lo((int)g, p.BH);
         if (at >= end) break;
-        // units are whole in the pass's direction except the sequence's last one, which no range
-        // that is followed by another holds
         float *st = states + (size_t)g * n + e;
         float x[4];
         load4(st, x);
-        const Pow f = decay_pow(dec, (unsigned)((at - from) * s.unit));
+        const Pow f = decay_pow(dec, (unsigned)(s.before((int)(at - beg), p.T, p.rev) -
+                                                s.before((int)(from - beg), p.T, p.rev)));
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[i] = fmaf(f.hi, c[i], fmaf(f.lo, c[i], x[i]));
         store4(st, c);

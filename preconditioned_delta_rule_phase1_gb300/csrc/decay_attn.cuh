@@ -39,10 +39,17 @@ struct Pass {
 // CTA.  A range that starts inside a sequence starts from the state that the
 // range before it leaves: a first pass forms what each range adds to that
 // state (its units of the sequence it ends in), a small kernel chains them.
+// Backwards in time the units start at the sequence's last token or, with
+// `natural`, are those of the forward direction in reverse order (the one
+// that may be short then comes first).
 struct Split {
-    int unit, nch, G;
+    int unit, nch, G, natural = 0;
     __host__ __device__ long long lo(int g, int BH) const {
         return (long long)BH * nch * g / G;
+    }
+    // tokens before unit u of a sequence, in the pass's direction
+    __device__ long long before(int u, int T, int rev) const {
+        return rev && natural && u > 0 ? T - (long long)(nch - u) * unit : (long long)u * unit;
     }
 };
 

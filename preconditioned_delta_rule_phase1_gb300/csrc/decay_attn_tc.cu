@@ -29,9 +29,16 @@
 // them, the second launch does the work.  That reads K and V once more, so
 // ranges that hold whole sequences are preferred where they fill the GPU.
 //
-// Roles (18 warps): 0 TMA; 1 MMA issue; 2-5 P out of TMEM, weighted, back as
-// a TMEM operand, and O to global memory; 6-9 K^ in halves of 64 tokens (the
-// first part over K, the others in two buffers of 16 KB); 10-17 the state.
+// Roles (15 warps): 0 TMA; 1 MMA issue for the outputs, 14 for the state;
+// 2-5 P out of TMEM, weighted, back as a TMEM operand, and O to global
+// memory; 6-13 the state: K^ in quarters of 32 tokens (the first part over K,
+// the others in buffers of their own), each multiplied while the next is
+// formed, then the update of S.  STATE_ONLY takes its chunks last to
+// first with weights up to the range's end, so that they add up in TMEM and
+// only the sum is read; it also leaves in L2 what the second launch reads
+// first.  The roles' loops are kept short (no unrolling beyond a quarter, a
+// block): each runs once a chunk, and unrolled they miss the instruction
+// cache (2x16x8192x128: 124 -> 80 us for the second launch).
 // Every wait is bounded: one that runs out records OSDN_ERR_TIMEOUT and all
 // roles leave their loops; no role waits for another in any other way.
 #include <algorithm>
@@ -53,23 +60,25 @@ using tc::wait_bar;
 using tc::wait_poll;
 
 constexpr int C = 128;          // tokens a chunk
-constexpr int kThreads = 576;
+constexpr int kThreads = 480;
+constexpr int kQ = 32;          // tokens of K^ formed at a time (a quarter)
 constexpr uint32_t kColP = 0;     // Q K^T, then P (bf16) over it
 constexpr uint32_t kColO1 = 128;  // Q S^T
 constexpr uint32_t kColO2 = 256;  // P V
 constexpr uint32_t kColD = 384;   // V^T K^
 constexpr uint32_t kTmemCols = 512;
 
-template <int K, int V>
+template <int K, int V, bool STATE_ONLY>
 struct Lay {
+    static constexpr int NV = STATE_ONLY ? 2 : 1;    // tiles of V (two do not fit beside Q and S)
     static constexpr int kK = C * K * 2, kV = C * V * 2;   // a tile of K (or Q), of V
     static constexpr int oK = 0;
     static constexpr int oV = oK + 2 * kK;
-    static constexpr int oQ = oV + 2 * kV;
-    static constexpr int oS = oQ + kK;               // bf16 S: V rows of K columns
-    static constexpr int oM = oS + V * K * 2;        // second and third parts of half a K^
-    static constexpr int oL = oM + kK / 2;
-    static constexpr int kBytes = oL + kK / 2;
+    static constexpr int oP = oV + NV * kV;          // second and third parts of K^
+    static constexpr int oQ = oP + 2 * kK;
+    // bf16 S (V rows of K columns); between its last use and the next S, O on its way out
+    static constexpr int oS = oQ + (STATE_ONLY ? 0 : kK);
+    static constexpr int kBytes = oS + (STATE_ONLY ? 0 : V * 2 * C);
     static constexpr int kAlloc = kBytes + 1024;
 };
 
@@ -81,9 +90,9 @@ struct Args {
 };
 
 struct Bars {
-    uint64_t fullK[2], fullV[2], emptyKV[2], fullQ, emptyQ;
-    uint64_t qk_full, p_ready, o_full, o_free;
-    uint64_t kh[2], h0_done, s_ready, ds_full, ds_free, done;
+    uint64_t fullK[2], emptyK[2], fullV[2], emptyV[2], fullQ, emptyQ;
+    uint64_t qk_full, p_ready, o_full, o_free, o_staged, o_stored;
+    uint64_t kq_full[4], kq_free[4], s_ready, ds_full, ds_free, done[2];
 };
 
 // The chunks of a range, one after another.
@@ -100,9 +109,10 @@ struct Walk {
             ++seq;
         }
     }
-    // first row of the chunk's tile (negative for the last chunk backwards), tokens in it
-    __device__ int row() const { return rev ? T - (u + 1) * C : u * C; }
-    __device__ int len() const { return min(C, T - u * C); }
+    __device__ void prev() { --u; }   // within a sequence
+    // the chunk's first token, and its length (a sequence's last tokens may be fewer than C)
+    __device__ int row() const { return (rev ? nch - 1 - u : u) * C; }
+    __device__ int len() const { return min(C, T - row()); }
 };
 
 __device__ __forceinline__ uint32_t top2(float a, float b) {   // the upper 16 bits of both
@@ -113,14 +123,14 @@ __device__ __forceinline__ float top(float a) { return __uint_as_float(__float_a
 template <int K, int V, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, Args a) {
-    using LY = Lay<K, V>;
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, Args a) {
+    using LY = Lay<K, V, STATE_ONLY>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = tc::align1024(smem_raw);
     __shared__ Bars bars;
     __shared__ uint32_t tmem_base_sh;
     __shared__ volatile int s_abort;
-    __shared__ float s_pow[4][32];
+    __shared__ __align__(16) float s_pow[4][96];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q4 = warp & 3;
     const int g = blockIdx.x;
@@ -139,6 +149,9 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     auto wait = [&](uint64_t &b, int parity) {   // by a whole warp
         return __all_sync(kFullMask, wait_bar(&b, parity & 1, &s_abort, st, bar_limit));
     };
+    auto poll = [&](uint64_t &b, int parity) {   // by one thread, on the critical path
+        return wait_poll(&b, parity & 1, &s_abort, st, poll_limit);
+    };
     auto arrive = [&](uint64_t &b) {
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&b);
@@ -148,14 +161,19 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bars.fullK[i], 1);
             ptx::mbar_init(&bars.fullV[i], 1);
-            ptx::mbar_init(&bars.emptyKV[i], 1);
-            ptx::mbar_init(&bars.kh[i], 4);
+            ptx::mbar_init(&bars.emptyK[i], 1);
+            ptx::mbar_init(&bars.emptyV[i], STATE_ONLY ? 1 : 2);   // one from either issuer
+            ptx::mbar_init(&bars.done[i], 1);
         }
-        uint64_t *one[] = {&bars.fullQ, &bars.emptyQ, &bars.qk_full, &bars.o_full, &bars.h0_done,
-                           &bars.ds_full, &bars.done};
+        for (int i = 0; i < 4; ++i) {
+            ptx::mbar_init(&bars.kq_full[i], 8);
+            ptx::mbar_init(&bars.kq_free[i], 1);
+        }
+        uint64_t *one[] = {&bars.fullQ, &bars.emptyQ, &bars.qk_full, &bars.o_full, &bars.o_stored, &bars.ds_full};
         for (uint64_t *b : one) ptx::mbar_init(b, 1);
         ptx::mbar_init(&bars.p_ready, 4);
         ptx::mbar_init(&bars.o_free, 4);
+        ptx::mbar_init(&bars.o_staged, 4);
         ptx::mbar_init(&bars.s_ready, 8);
         ptx::mbar_init(&bars.ds_free, 8);
         ptx::fence_mbar_init();
@@ -171,28 +189,40 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t tmem = tmem_base_sh;
     const uint32_t lane_off = static_cast<uint32_t>(32 * q4) << 16;
     auto sK = [&](int j) { return smem + LY::oK + (j & 1) * LY::kK; };
-    auto sV = [&](int j) { return smem + LY::oV + (j & 1) * LY::kV; };
+    constexpr int NV = LY::NV;
+    auto sV = [&](int j) { return smem + LY::oV + (j % NV) * LY::kV; };
 
     if (warp == 0) {
         // ======================================================== TMA
         if (lane == 0 && !stall) {
-            int last_kv = -1, last_q = -1;
-            Walk w(a, lo), wq(a, lo);
-            auto load_kv = [&](int j) {
-                if (j >= 2 && !wait_bar(&bars.emptyKV[j & 1], ((j >> 1) - 1) & 1, &s_abort, st, bar_limit)) return false;
+            int last_k = -1, last_v = -1, last_q = -1;
+            Walk wk(a, STATE_ONLY ? hi - 1 : lo), wv = wk, wq(a, lo);
+            auto load_k = [&](int j) {
+                if (j >= 2 && !wait_bar(&bars.emptyK[j & 1], ((j >> 1) - 1) & 1, &s_abort, st, bar_limit)) return false;
                 ptx::mbar_arrive_expect_tx(&bars.fullK[j & 1], LY::kK);
 #pragma unroll
                 for (int b = 0; b < K / 64; ++b)
-                    ptx::tma_load_3d(sK(j) + b * C * 128, &tm_k, &bars.fullK[j & 1], b * 64, w.row(), (int)w.seq);
-                ptx::mbar_arrive_expect_tx(&bars.fullV[j & 1], LY::kV);
+                    ptx::tma_load_3d(sK(j) + b * C * 128, &tm_k, &bars.fullK[j & 1], b * 64, wk.row(), (int)wk.seq);
+                // a single V waits for its buffer: bring it as far as L2 meanwhile
+                if (NV == 1) {
 #pragma unroll
-                for (int b = 0; b < V / 64; ++b)
-                    ptx::tma_load_3d(sV(j) + b * C * 128, &tm_v, &bars.fullV[j & 1], b * 64, w.row(), (int)w.seq);
-                last_kv = j;
-                w.next();
+                    for (int b = 0; b < V / 64; ++b) ptx::tma_prefetch_3d(&tm_v, b * 64, wk.row(), (int)wk.seq);
+                }
+                last_k = j;
+                STATE_ONLY ? wk.prev() : wk.next();
                 return true;
             };
-            bool ok = load_kv(0);
+            auto load_v = [&](int j) {
+                if (j >= NV && !wait_bar(&bars.emptyV[j % NV], (j / NV - 1) & 1, &s_abort, st, bar_limit)) return false;
+                ptx::mbar_arrive_expect_tx(&bars.fullV[j % NV], LY::kV);
+#pragma unroll
+                for (int b = 0; b < V / 64; ++b)
+                    ptx::tma_load_3d(sV(j) + b * C * 128, &tm_v, &bars.fullV[j % NV], b * 64, wv.row(), (int)wv.seq);
+                last_v = j;
+                STATE_ONLY ? wv.prev() : wv.next();
+                return true;
+            };
+            bool ok = load_k(0) && (!STATE_ONLY || load_v(0));
             for (int j = 0; j < n && ok; ++j) {
                 if (!STATE_ONLY) {
                     if (j >= 1 && !wait_bar(&bars.emptyQ, (j - 1) & 1, &s_abort, st, bar_limit)) break;
@@ -202,135 +232,146 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         ptx::tma_load_3d(smem + LY::oQ + b * C * 128, &tm_q, &bars.fullQ, b * 64, wq.row(), (int)wq.seq);
                     last_q = j;
                     wq.next();
-                    // the next Q waits for this buffer: bring it as far as L2 meanwhile
-                    if (j + 1 < n && wq.row() >= 0) {
+                    if (j + 1 < n) {   // as V
 #pragma unroll
                         for (int b = 0; b < K / 64; ++b) ptx::tma_prefetch_3d(&tm_q, b * 64, wq.row(), (int)wq.seq);
                     }
                 }
-                if (j + 1 < n) ok = load_kv(j + 1);
+                if (STATE_ONLY) ok = j + 1 == n || (load_k(j + 1) && load_v(j + 1));
+                else ok = load_v(j) && (j + 1 == n || load_k(j + 1));
             }
             // every copy has landed before the CTA ends, also after an abort
-            for (int j = max(0, last_kv - 1); j <= last_kv; ++j) {
-                drain_bar(&bars.fullK[j & 1], (j >> 1) & 1);
-                drain_bar(&bars.fullV[j & 1], (j >> 1) & 1);
-            }
+            for (int j = max(0, last_k - 1); j <= last_k; ++j) drain_bar(&bars.fullK[j & 1], (j >> 1) & 1);
+            for (int j = max(0, last_v - NV + 1); j <= last_v; ++j) drain_bar(&bars.fullV[j % NV], (j / NV) & 1);
             if (last_q >= 0) drain_bar(&bars.fullQ, last_q & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ======================================================== MMA issue
-        if (lane == 0) {
-            auto pw = [&](uint64_t &b, int parity) { return wait_poll(&b, parity & 1, &s_abort, st, poll_limit); };
+        // ======================================================== MMA issue: the outputs
+        if (lane == 0 && !STATE_ONLY) {
             const uint32_t id_qk = ptx::idesc_bf16(C, C, 0, 0), id_qs = ptx::idesc_bf16(C, V, 0, 0);
-            const uint32_t id_pv = ptx::idesc_bf16(C, V, 0, 1), id_d = ptx::idesc_bf16(V, K, 1, 1);
+            const uint32_t id_pv = ptx::idesc_bf16(C, V, 0, 1);
             const uint32_t q = ptx::smem_u32(smem + LY::oQ), s = ptx::smem_u32(smem + LY::oS);
-            const uint32_t km = ptx::smem_u32(smem + LY::oM), kl = ptx::smem_u32(smem + LY::oL);
+#pragma unroll 1
             for (int j = 0; j < n; ++j) {
                 const uint32_t k = ptx::smem_u32(sK(j)), v = ptx::smem_u32(sV(j));
-                auto add_half = [&](int h) {   // V^T K^ over the half's tokens, small parts first
-#pragma unroll
-                    for (int part = 2; part >= 0; --part) {
-                        const uint64_t db = part == 0 ? dmn0(k, C * 128) + mnoff(4 * h)
-                                                      : dmn0(part == 1 ? km : kl, C * 64);
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            ptx::umma_bf16(tmem + kColD, dmn0(v, C * 128) + mnoff(4 * h + ks), db + mnoff(ks), id_d,
-                                           h > 0 || part < 2 || ks > 0);
-                    }
-                };
-                if (!pw(bars.fullK[j & 1], j >> 1)) break;
-                if (!STATE_ONLY) {
-                    // P's columns are free once the last P V has completed
-                    if (!pw(bars.fullQ, j) || (j && !pw(bars.o_full, j - 1))) break;
-                    ptx::tc_fence_after();
-#pragma unroll
-                    for (int ks = 0; ks < K / 16; ++ks)
-                        ptx::umma_bf16(tmem + kColP, dk0(q) + koff(C, ks), dk0(k) + koff(C, ks), id_qk, ks > 0);
-                    ptx::umma_commit(&bars.qk_full);
-                    if (!pw(bars.s_ready, j) || (j && !pw(bars.o_free, j - 1))) break;
-                    ptx::tc_fence_after();
-#pragma unroll
-                    for (int ks = 0; ks < K / 16; ++ks)
-                        ptx::umma_bf16(tmem + kColO1, dk0(q) + koff(C, ks), dk0(s) + koff(V, ks), id_qs, ks > 0);
-                    ptx::umma_commit(&bars.emptyQ);
-                }
-                if (!pw(bars.fullV[j & 1], j >> 1) || !pw(bars.kh[0], j) || (j && !pw(bars.ds_free, j - 1))) break;
+                // P's columns are free once the last P V has completed
+                if (!poll(bars.fullK[j & 1], j >> 1) || !poll(bars.fullQ, j) || (j && !poll(bars.o_full, j - 1))) break;
                 ptx::tc_fence_after();
-                add_half(0);
-                ptx::umma_commit(&bars.h0_done);
-                if (!STATE_ONLY) {
-                    if (!pw(bars.p_ready, j)) break;
-                    ptx::tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < C / 16; ++ks)
-                        ptx::umma_bf16_ts(tmem + kColO2, tmem + kColP + 8 * ks, dmn0(v, C * 128) + mnoff(ks), id_pv,
-                                          ks > 0);
-                    ptx::umma_commit(&bars.o_full);
-                }
-                if (!pw(bars.kh[1], j)) break;
+                for (int ks = 0; ks < K / 16; ++ks)
+                    ptx::umma_bf16(tmem + kColP, dk0(q) + koff(C, ks), dk0(k) + koff(C, ks), id_qk, ks > 0);
+                ptx::umma_commit(&bars.qk_full);
+                if (!poll(bars.s_ready, j) || (j && !poll(bars.o_free, j - 1))) break;
                 ptx::tc_fence_after();
-                add_half(1);
-                ptx::umma_commit(&bars.ds_full);
-                ptx::umma_commit(&bars.emptyKV[j & 1]);
+#pragma unroll
+                for (int ks = 0; ks < K / 16; ++ks)
+                    ptx::umma_bf16(tmem + kColO1, dk0(q) + koff(C, ks), dk0(s) + koff(V, ks), id_qs, ks > 0);
+                ptx::umma_commit(&bars.emptyQ);
+                if (!poll(bars.fullV[j % NV], j / NV) || !poll(bars.p_ready, j)) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < C / 16; ++ks)
+                    ptx::umma_bf16_ts(tmem + kColO2, tmem + kColP + 8 * ks, dmn0(v, C * 128) + mnoff(ks), id_pv, ks > 0);
+                ptx::umma_commit(&bars.o_full);
+                ptx::umma_commit(&bars.emptyV[j % NV]);
             }
             // every product issued has completed before TMEM is released
-            ptx::umma_commit(&bars.done);
-            drain_bar(&bars.done, 0);
+            ptx::umma_commit(&bars.done[0]);
+            drain_bar(&bars.done[0], 0);
+        }
+        __syncwarp();
+    } else if (warp == 14) {
+        // ======================================================== MMA issue: the state
+        if (lane == 0) {
+            const uint32_t id_d = ptx::idesc_bf16(V, K, 1, 1);
+            const uint32_t parts = ptx::smem_u32(smem + LY::oP);
+            bool ok = true;
+            for (int j = 0; j < n && ok; ++j) {
+                const uint32_t k = ptx::smem_u32(sK(j)), v = ptx::smem_u32(sV(j));
+                ok = poll(bars.fullV[j % NV], j / NV) && (STATE_ONLY || !j || poll(bars.ds_free, j - 1));
+#pragma unroll 1
+                for (int qt = 0; ok && qt < 4; ++qt) {   // V^T K^ quarter by quarter, small parts first
+                    if (!(ok = poll(bars.kq_full[qt], j))) break;
+                    ptx::tc_fence_after();
+#pragma unroll
+                    for (int part = 2; part >= 0; --part) {
+                        const uint64_t db = part == 0 ? dmn0(k, C * 128) + mnoff(2 * qt)
+                                                      : dmn0(parts + (part - 1) * LY::kK, C * 128) + mnoff(2 * qt);
+#pragma unroll
+                        for (int ks = 0; ks < 2; ++ks)
+                            ptx::umma_bf16(tmem + kColD, dmn0(v, C * 128) + mnoff(2 * qt + ks), db + mnoff(ks), id_d,
+                                           qt > 0 || part < 2 || ks > 0 || (STATE_ONLY && j > 0));
+                    }
+                    if (STATE_ONLY) ptx::umma_commit(&bars.kq_free[qt]);
+                }
+                if (!ok) break;
+                if (!STATE_ONLY || j == n - 1) ptx::umma_commit(&bars.ds_full);
+                ptx::umma_commit(&bars.emptyK[j & 1]);
+                ptx::umma_commit(&bars.emptyV[j % NV]);
+            }
+            ptx::umma_commit(&bars.done[1]);
+            drain_bar(&bars.done[1], 0);
         }
         __syncwarp();
     } else if (warp < 6) {
         // ======================================================== P and O
         if (!STATE_ONLY) {
             const int r = 32 * q4 + lane;   // row of the chunk
-            float *tab = s_pow[warp - 2];
+            // Key block b (32 columns) against the row's own block, d blocks away: the weight of
+            // column m is far[d-1] col[m], far from the row to the near end of the block and col
+            // from there on; on the diagonal it is a^gap, read from the same table, which holds
+            // zeros where the gap is negative.
+            float *col = s_pow[warp - 2] + 32;
+            const float *diag = col + (p.rev ? -lane : 31 - lane);
             float wq = 0.0f, far[3] = {0.0f, 0.0f, 0.0f};
             long long have = -1;
+            int have_len = 0;
             Walk w(a, lo);
             for (int j = 0; j < n; ++j, w.next()) {
-                if (w.seq != have) {
-                    // a^m; the row's power on the carry; a^(gap to the near end of block 1, 2, 3 away)
+                const int len = w.len();
+                if (w.seq != have || len != have_len) {
                     const float dec = p.decay[w.seq % p.H];
                     __syncwarp();
-                    tab[lane] = decay_pow(dec, lane).hi;
+                    col[lane] = decay_pow(dec, p.rev ? lane : 31 - lane).hi;
+                    col[lane - 32] = col[lane + 32] = 0.0f;
                     __syncwarp();
-                    wq = decay_pow(dec, p.rev ? C - 1 - r : r + 1).hi;
-                    const int near = p.rev ? 31 - lane : lane;
+                    wq = decay_pow(dec, p.rev ? max(len - 1 - r, 0) : r + 1).hi;
 #pragma unroll
-                    for (int d = 0; d < 3; ++d) far[d] = decay_pow(dec, near + 1 + 32 * d).hi;
+                    for (int d = 0; d < 3; ++d) far[d] = decay_pow(dec, (p.rev ? 31 - lane : lane) + 1 + 32 * d).hi;
                     have = w.seq;
+                    have_len = len;
                 }
                 if (!wait(bars.qk_full, j)) break;
                 ptx::tc_fence_after();
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    const int d = p.rev ? b - q4 : q4 - b;
+                    float pk[16];
+                    if (d < 0) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {   // 32 columns: keys 32 b ..
-                    const int d = p.rev ? b - q4 : q4 - b;   // blocks between the row's and the keys'
-                    float x[32];
-                    uint32_t pk[16];
-                    if (d >= 0) {
+                        for (int m = 0; m < 16; ++m) pk[m] = 0.0f;
+                    } else {
+                        float x[32];
                         tc::tmem_ld32(tmem + lane_off + kColP + 32 * b, x);
                         if (d == 0) {
 #pragma unroll
-                            for (int m = 0; m < 32; ++m) {
-                                const int gap = p.rev ? m - lane : lane - m;
-                                x[m] = gap >= 0 ? x[m] * tab[max(gap, 0)] : 0.0f;
-                            }
+                            for (int m = 0; m < 16; ++m)
+                                pk[m] = __uint_as_float(tc::pack_bf16x2(x[2 * m] * diag[2 * m], x[2 * m + 1] * diag[2 * m + 1]));
                         } else {
                             const float f = d == 1 ? far[0] : d == 2 ? far[1] : far[2];
+                            const float2 ff = make_float2(f, f);
 #pragma unroll
-                            for (int m = 0; m < 32; ++m) x[m] *= f * tab[p.rev ? m : 31 - m];
+                            for (int m = 0; m < 16; m += 2) {
+                                const float4 c = *reinterpret_cast<const float4 *>(col + 2 * m);
+                                const float2 y = __fmul2_rn(__fmul2_rn(make_float2(x[2 * m], x[2 * m + 1]), ff), make_float2(c.x, c.y));
+                                const float2 z = __fmul2_rn(__fmul2_rn(make_float2(x[2 * m + 2], x[2 * m + 3]), ff), make_float2(c.z, c.w));
+                                pk[m] = __uint_as_float(tc::pack_bf16x2(y.x, y.y));
+                                pk[m + 1] = __uint_as_float(tc::pack_bf16x2(z.x, z.y));
+                            }
                         }
-                    } else {
-#pragma unroll
-                        for (int m = 0; m < 32; ++m) x[m] = 0.0f;
                     }
-                    float packed[16];
-#pragma unroll
-                    for (int m = 0; m < 16; ++m) {
-                        pk[m] = tc::pack_bf16x2(x[2 * m], x[2 * m + 1]);
-                        packed[m] = __uint_as_float(pk[m]);
-                    }
-                    ptx::tmem_st16(tmem + lane_off + kColP + 16 * b, packed);
+                    ptx::tmem_st16(tmem + lane_off + kColP + 16 * b, pk);
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
@@ -338,158 +379,170 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
                 if (!wait(bars.o_full, j)) break;
                 ptx::tc_fence_after();
-                const int t = w.row() + r;
-                const bool live = t >= 0 && t < p.T;
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)w.seq * p.T + max(t, 0)) * V;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < V; c += 32) {
-                    float x[32], y[32];
-                    tc::tmem_ld32(tmem + lane_off + kColO1 + c, x);
-                    tc::tmem_ld32(tmem + lane_off + kColO2 + c, y);
+                    float x[2][16], y[2][16];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ptx::tmem_ld16(tmem + lane_off + kColO1 + c + 16 * h, x[h]);
+                        ptx::tmem_ld16(tmem + lane_off + kColO2 + c + 16 * h, y[h]);
+                    }
+                    ptx::tmem_wait_ld();
                     if (c + 32 == V) {
                         ptx::tc_fence_before();
                         arrive(bars.o_free);
                     }
 #pragma unroll
-                    for (int h = 0; h < 32; h += 16) {
-                        uint32_t out[8];
+                    for (int h = 0; h < 2; ++h) {
+                        float z[16];
 #pragma unroll
-                        for (int m = 0; m < 8; ++m)
-                            out[m] = tc::pack_bf16x2(fmaf(wq, x[h + 2 * m], y[h + 2 * m]),
-                                                     fmaf(wq, x[h + 2 * m + 1], y[h + 2 * m + 1]));
-                        if (live) {
-                            *reinterpret_cast<uint4 *>(o + c + h) = make_uint4(out[0], out[1], out[2], out[3]);
-                            *reinterpret_cast<uint4 *>(o + c + h + 8) = make_uint4(out[4], out[5], out[6], out[7]);
+                        for (int m = 0; m < 16; m += 2) {
+                            const float2 u = __ffma2_rn(make_float2(wq, wq), make_float2(x[h][m], x[h][m + 1]),
+                                                        make_float2(y[h][m], y[h][m + 1]));
+                            z[m] = u.x;
+                            z[m + 1] = u.y;
                         }
+                        tc::st_row_sw128(smem + LY::oS, C, r, c + 16 * h, z, 16);
                     }
+                }
+                ptx::fence_proxy_async_smem();
+                arrive(bars.o_staged);
+                if (warp == 2) {   // rows past the sequence's end are clipped
+                    if (!wait(bars.o_staged, j)) break;
+                    if (lane == 0) {
+#pragma unroll
+                        for (int b = 0; b < V / 64; ++b)
+                            ptx::tma_store_3d(&tm_o, smem + LY::oS + b * C * 128, b * 64, w.row(), (int)w.seq);
+                        ptx::bulk_commit_group();
+                        ptx::bulk_wait_read_all();
+                    }
+                    arrive(bars.o_stored);
                 }
             }
         }
-    } else if (warp < 10) {
-        // ======================================================== K^
-        const int rt = (tid - 192) & 63, c0 = ((tid - 192) >> 6) * (K / 2);   // row of the half, first column
-        float wk[2] = {0.0f, 0.0f};
+    } else {
+        // ======================================================== K^ and the state
+        // row i of S: TMEM lane i (V = 128) or 32 (i / 16) + i % 16 (V = 64); columns c0 ..
+        constexpr int NC = K / 2;
+        const int c0 = ((warp - 6) >> 2) * NC;
+        const int row = V == 128 ? 32 * q4 + lane : 16 * q4 + lane;
+        const bool act = V == 128 || lane < 16;
+        constexpr size_t sb = (size_t)K * V;
+        // K^: lane = row of the quarter; a warp takes K / 8 columns
+        const int k0 = (warp - 6) * (K / 8);
+        float S[NC], wk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        Pow f = {1.0f, 0.0f};   // the chunk's whole decay; STATE_ONLY: from the chunk's end to the range's
+        Pow fc = {1.0f, 0.0f};
         long long have = -1;
         int have_len = 0;
-        Walk w(a, lo);
-        for (int j = 0; j < n; ++j, w.next()) {
+        bool ok = true;
+        Walk w(a, STATE_ONLY ? hi - 1 : lo);
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
             const int len = w.len();
             if (w.seq != have || len != have_len) {
                 const float dec = p.decay[w.seq % p.H];
                 if (!decay_ok(dec)) report_status(st, OSDN_ERR_DEVICE);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int qt = 0; qt < 4; ++qt) {
                     // the token's distance to the chunk's end, in the pass's direction
-                    const int row = 64 * h + rt, e = p.rev ? len - C + 1 + row : len - 1 - row;
-                    wk[h] = decay_pow(dec, max(e, 0)).hi;
+                    const int kr = kQ * qt + lane, e = p.rev ? kr + 1 : len - 1 - kr;
+                    wk[qt] = decay_pow(dec, max(e, 0)).hi;
                 }
+                fc = decay_pow(dec, len);
+                if (!STATE_ONLY) f = fc;
                 have = w.seq;
                 have_len = len;
             }
-            // K as loaded has been read by Q K^T; the halves' buffers by the last chunk's update
-            if (STATE_ONLY ? !wait(bars.fullK[j & 1], j >> 1) : !wait(bars.qk_full, j)) break;
-            if (j && !wait(bars.ds_full, j - 1)) break;
-            bool ok = true;
+            if (!STATE_ONLY) {
+                if (j == 0 || w.u == 0) {   // the state entering the range, or a sequence
+                    const float *src = nullptr;
+                    bool tr = false;
+                    if (w.u > 0) {
+                        src = a.states + (size_t)g * sb;
+                    } else if (p.S0.p) {
+                        src = p.S0.p + (size_t)w.seq * sb;
+                        tr = p.S0.transposed;
+                    }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (h && !wait(bars.h0_done, j)) {
-                    ok = false;
-                    break;
+                    for (int e = 0; e < NC; e += 4) {
+                        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        if (src && act && !tr) load4(src + (size_t)row * K + c0 + e, x);
+                        if (src && act && tr) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) x[i] = src[(size_t)(c0 + e + i) * V + row];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) S[e + i] = x[i];
+                    }
                 }
-                uint8_t *hi_row = sK(j) + (c0 >> 6) * C * 128 + (64 * h + rt) * 128;
-                uint8_t *mid_row = smem + LY::oM + (c0 >> 6) * C * 64 + rt * 128;
-                uint8_t *lo_row = smem + LY::oL + (c0 >> 6) * C * 64 + rt * 128;
+                // the last chunk's O, which took the place of its state's copy, has left
+                if (j && !(ok = wait(bars.o_stored, j - 1))) break;
+                if (act) tc::st_row_sw128(smem + LY::oS, V, row, c0, S, NC);
+                ptx::fence_proxy_async_smem();
+                arrive(bars.s_ready);
+            }
+            // K as loaded has been read by Q K^T
+            if (!(ok = STATE_ONLY ? wait(bars.fullK[j & 1], j >> 1) : wait(bars.qk_full, j))) break;
+#pragma unroll 1
+            for (int qt = 0; qt < 4; ++qt) {
+                // the other parts have been read by the last chunk's product (before its S was)
+                if (STATE_ONLY && j && !(ok = wait(bars.kq_free[qt], j - 1))) break;
+                const int at = (k0 >> 6) * C * 128 + (kQ * qt + lane) * 128;
+                uint8_t *hi_row = sK(j) + at, *mid_row = smem + LY::oP + at, *lo_row = mid_row + LY::kK;
+                float wt = qt < 2 ? (qt ? wk[1] : wk[0]) : (qt == 2 ? wk[2] : wk[3]);
+                if (STATE_ONLY) wt *= f.hi;
+                const float2 ww = make_float2(wt, wt), minus = make_float2(-1.0f, -1.0f);
 #pragma unroll
-                for (int i = 0; i < K / 16; ++i) {
-                    const int off = ((((c0 & 63) >> 3) + i) ^ (rt & 7)) * 16;
+                for (int c = 0; c < K / 64; ++c) {
+                    const int off = ((((k0 & 63) >> 3) + c) ^ (lane & 7)) * 16;
                     const uint4 u = *reinterpret_cast<const uint4 *>(hi_row + off);
                     const uint32_t in[4] = {u.x, u.y, u.z, u.w};
                     uint32_t ph[4], pm[4], pl[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float x0 = __uint_as_float(in[e] << 16) * wk[h];
-                        const float x1 = __uint_as_float(in[e] & 0xffff0000u) * wk[h];
-                        const float m0 = x0 - top(x0), m1 = x1 - top(x1);
-                        ph[e] = top2(x0, x1);
-                        pm[e] = top2(m0, m1);
-                        pl[e] = top2(m0 - top(m0), m1 - top(m1));
+                        const float2 x = __fmul2_rn(make_float2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), ww);
+                        const float2 m = __ffma2_rn(make_float2(top(x.x), top(x.y)), minus, x);
+                        const float2 l = __ffma2_rn(make_float2(top(m.x), top(m.y)), minus, m);
+                        ph[e] = top2(x.x, x.y);
+                        pm[e] = top2(m.x, m.y);
+                        pl[e] = top2(l.x, l.y);
                     }
                     *reinterpret_cast<uint4 *>(hi_row + off) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
                     *reinterpret_cast<uint4 *>(mid_row + off) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
                     *reinterpret_cast<uint4 *>(lo_row + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
                 }
                 ptx::fence_proxy_async_smem();
-                arrive(bars.kh[h]);
+                arrive(bars.kq_full[qt]);
             }
             if (!ok) break;
-        }
-    } else {
-        // ======================================================== state
-        // row i of S: TMEM lane i (V = 128) or 32 (i / 16) + i % 16 (V = 64); columns c0 ..
-        constexpr int NC = K / 2;
-        const int c0 = ((warp - 10) >> 2) * NC;
-        const int row = V == 128 ? 32 * q4 + lane : 16 * q4 + lane;
-        const bool act = V == 128 || lane < 16;
-        constexpr size_t sb = (size_t)K * V;
-        float S[NC];
-        Pow f = {0.0f, 0.0f};
-        long long have = -1;
-        int have_len = 0;
-        Walk w(a, lo);
-        for (int j = 0; j < n; ++j, w.next()) {
-            const int len = w.len();
-            if (w.seq != have || len != have_len) {
-                f = decay_pow(p.decay[w.seq % p.H], len);
-                have = w.seq;
-                have_len = len;
+            if (STATE_ONLY) {
+                f = pow_mul(f, fc);
+                w.prev();
+                if (j < n - 1) continue;
             }
-            if (j == 0 || w.u == 0) {   // the state entering the range, or a sequence
-                const float *src = nullptr;
-                bool tr = false;
-                if (!STATE_ONLY && w.u > 0) {
-                    src = a.states + (size_t)g * sb;
-                } else if (!STATE_ONLY && p.S0.p) {
-                    src = p.S0.p + (size_t)w.seq * sb;
-                    tr = p.S0.transposed;
-                }
-#pragma unroll
-                for (int e = 0; e < NC; e += 4) {
-                    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (src && act && !tr) load4(src + (size_t)row * K + c0 + e, x);
-                    if (src && act && tr) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[i] = src[(size_t)(c0 + e + i) * V + row];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) S[e + i] = x[i];
-                }
-            }
-            if (!STATE_ONLY) {
-                // the copy of the last chunk's state has been read by Q S^T
-                if (j && !wait(bars.emptyQ, j - 1)) break;
-                if (act) tc::st_row_sw128(smem + LY::oS, V, row, c0, S, NC);
-                ptx::fence_proxy_async_smem();
-                arrive(bars.s_ready);
-            }
-            if (!wait(bars.ds_full, j)) break;
+            if (!(ok = wait(bars.ds_full, STATE_ONLY ? 0 : j))) break;
             ptx::tc_fence_after();
 #pragma unroll
-            for (int e = 0; e < NC; e += 16) {
-                float x[16];
-                ptx::tmem_ld16(tmem + lane_off + kColD + c0 + e, x);
-                ptx::tmem_wait_ld();
+            for (int e = 0; e < NC; e += 32) {
+                float x[32];
+                tc::tmem_ld32(tmem + lane_off + kColD + c0 + e, x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[e + i] = fmaf(f.hi, S[e + i], fmaf(f.lo, S[e + i], x[i]));
+                for (int i = 0; i < 32; ++i)
+                    S[e + i] = STATE_ONLY ? x[i] : fmaf(f.hi, S[e + i], fmaf(f.lo, S[e + i], x[i]));
             }
-            ptx::tc_fence_before();
-            arrive(bars.ds_free);
             float *dst = nullptr;
             bool tr = false;
             if (STATE_ONLY) {
-                if (j == n - 1) dst = a.states + (size_t)(g + 1) * sb;
-            } else if (w.u == a.s.nch - 1 && p.ST.p) {
-                dst = p.ST.p + (size_t)w.seq * sb;
-                tr = p.ST.transposed;
+                dst = a.states + (size_t)(g + 1) * sb;
+            } else {
+                ptx::tc_fence_before();
+                arrive(bars.ds_free);
+                if (w.u == a.s.nch - 1 && p.ST.p) {
+                    dst = p.ST.p + (size_t)w.seq * sb;
+                    tr = p.ST.transposed;
+                }
+                w.next();
             }
             if (dst && act) {
 #pragma unroll
@@ -512,26 +565,26 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 template <int K, int V, bool STATE_ONLY>
-cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Args &a,
-                   cudaStream_t stream) {
-    constexpr int smem = Lay<K, V>::kAlloc;
+cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
+                   const Args &a, cudaStream_t stream) {
+    constexpr int smem = Lay<K, V, STATE_ONLY>::kAlloc;
     static std::atomic<unsigned long long> attr_done{0};
     cudaError_t e = smem_attr_once((const void *)attend_tc_kernel<K, V, STATE_ONLY>, smem, attr_done);
     if (e != cudaSuccess) return e;
     // no range follows the last one, so nothing needs its state
-    attend_tc_kernel<K, V, STATE_ONLY><<<a.s.G - (STATE_ONLY ? 1 : 0), kThreads, smem, stream>>>(mq, mk, mv, a);
+    attend_tc_kernel<K, V, STATE_ONLY><<<a.s.G - (STATE_ONLY ? 1 : 0), kThreads, smem, stream>>>(mq, mk, mv, mo, a);
     return cudaGetLastError();
 }
 
 template <int K, int V>
-cudaError_t run(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Args &a,
-                cudaStream_t stream) {
+cudaError_t run(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
+                const Args &a, cudaStream_t stream) {
     if (!unsplit(a.s, a.p.BH)) {
-        cudaError_t e = launch<K, V, true>(mq, mk, mv, a, stream);
+        cudaError_t e = launch<K, V, true>(mq, mk, mv, mo, a, stream);
         if (e == cudaSuccess) e = chain_states(a.p, a.s, a.states, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch<K, V, false>(mq, mk, mv, a, stream);
+    return launch<K, V, false>(mq, mk, mv, mo, a, stream);
 }
 
 }  // namespace
@@ -539,6 +592,7 @@ cudaError_t run(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap 
 Split tc_split(int BH, int T, int, int) {
     Split s;
     s.unit = C;
+    s.natural = 1;
     s.nch = (T + C - 1) / C;
     s.G = BH;
     const long long slots = tc::sm_count(), N = (long long)BH * s.nch, G = std::min(N, slots);
@@ -552,17 +606,17 @@ Split tc_split(int BH, int T, int, int) {
 
 cudaError_t attend_tc(const Pass &p, void *scratch, int *status, cudaStream_t stream) {
     if (!tc::tensor_map_encoder_ready()) return cudaErrorNotSupported;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     if (!tc::make_map(&mq, p.q, p.BH, p.T, p.K, C) || !tc::make_map(&mk, p.k, p.BH, p.T, p.K, C) ||
-        !tc::make_map(&mv, p.v, p.BH, p.T, p.V, C))
+        !tc::make_map(&mv, p.v, p.BH, p.T, p.V, C) || !tc::make_map(&mo, p.o, p.BH, p.T, p.V, C))
         return cudaErrorInvalidValue;
     Args a;
     a.p = p;
     a.s = tc_split(p.BH, p.T, p.K, p.V);
     a.states = static_cast<float *>(scratch);
     a.status = status;
-    if (p.K == 128) return p.V == 128 ? run<128, 128>(mq, mk, mv, a, stream) : run<128, 64>(mq, mk, mv, a, stream);
-    return p.V == 128 ? run<64, 128>(mq, mk, mv, a, stream) : run<64, 64>(mq, mk, mv, a, stream);
+    if (p.K == 128) return p.V == 128 ? run<128, 128>(mq, mk, mv, mo, a, stream) : run<128, 64>(mq, mk, mv, mo, a, stream);
+    return p.V == 128 ? run<64, 128>(mq, mk, mv, mo, a, stream) : run<64, 64>(mq, mk, mv, mo, a, stream);
 }
 
 }  // namespace da
