@@ -184,13 +184,11 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
             }
         }
         float *dst = nullptr;
-        bool tr = false;
         const size_t sb = (size_t)p.K * p.V;
         if (STATE_ONLY) {
             dst = a.states + (size_t)(g + 1) * sb;
-        } else if (tend == p.T && p.ST.p) {
-            dst = p.ST.p + (size_t)seq * sb;
-            tr = p.ST.transposed;
+        } else if (tend == p.T && p.ST) {
+            dst = p.ST + (size_t)seq * sb;
         }
         if (dst) {
 #pragma unroll
@@ -199,12 +197,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
                 for (int m = 0; m < M; ++m) {
                     const int c = 16 * m + 4 * pc, i = row0 + row + r;
                     const float x[4] = {S[r][m][0].x, S[r][m][0].y, S[r][m][1].x, S[r][m][1].y};
-                    if (!tr) {
-                        store4(dst + (size_t)i * K + c, x);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) dst[(size_t)(c + e) * p.V + i] = x[e];
-                    }
+                    store4(dst + (size_t)i * K + c, x);
                 }
         }
     }

@@ -18,10 +18,10 @@
 namespace osdn {
 namespace da {
 
-// A [rows][cols] fp32 state of each sequence at `p` (NULL: zeros, or not
-// written), in this layout or transposed ([cols][rows]).
+// The [V][K] fp32 state that each sequence starts from (NULL: zeros), in this
+// layout or transposed ([K][V]).
 struct State {
-    float *p = nullptr;
+    const float *p = nullptr;
     int transposed = 0;
 };
 
@@ -30,7 +30,8 @@ struct Pass {
     int BH, H, T, K, V, rev;
     const void *q, *k, *v;
     const float *decay;
-    State S0, ST;
+    State S0;
+    float *ST;   // NULL: not written
     void *o;
 };
 

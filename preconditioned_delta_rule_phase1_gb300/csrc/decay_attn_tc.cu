@@ -29,16 +29,18 @@
 // them, the second launch does the work.  That reads K and V once more, so
 // ranges that hold whole sequences are preferred where they fill the GPU.
 //
-// Roles (15 warps): 0 TMA; 1 MMA issue for the outputs, 14 for the state;
-// 2-5 P out of TMEM, weighted, back as a TMEM operand, and O to global
-// memory; 6-13 the state: K^ in quarters of 32 tokens (the first part over K,
-// the others in buffers of their own), each multiplied while the next is
-// formed, then the update of S.  STATE_ONLY takes its chunks last to
-// first with weights up to the range's end, so that they add up in TMEM and
-// only the sum is read; it also leaves in L2 what the second launch reads
-// first.  The roles' loops are kept short (no unrolling beyond a quarter, a
-// block): each runs once a chunk, and unrolled they miss the instruction
-// cache (2x16x8192x128: 124 -> 80 us for the second launch).
+// Roles (15 warps): 0 TMA; 1 MMA issue for the outputs; 2-5 P out of TMEM,
+// weighted, back as a TMEM operand, and O, turned in shared memory so that
+// whole rows are stored; 6-13 the state: K^ in two steps of 64 tokens, each multiplied while
+// the next is formed, and, behind the first step of the chunk after it, the
+// update of S; 14 MMA issue for the state.
+// Buffers are single (224 KB hold one chunk's K, V, Q, S and three parts of
+// K^): the next chunk's tiles wait in L2, brought there a chunk ahead.
+// STATE_ONLY takes its chunks last to first with weights up to the range's
+// end, so that they add up in TMEM and only the sum is read; it also leaves
+// in L2 what the second launch reads first.  The roles' loops are kept short
+// (little unrolling): each runs once a chunk, and unrolled they miss the
+// instruction cache (2x16x8192x128: 124 -> 80 us for the second launch).
 // Every wait is bounded: one that runs out records OSDN_ERR_TIMEOUT and all
 // roles leave their loops; no role waits for another in any other way.
 #include <algorithm>
@@ -60,8 +62,11 @@ using tc::wait_bar;
 using tc::wait_poll;
 
 constexpr int C = 128;          // tokens a chunk
-constexpr int kThreads = 480;
-constexpr int kQ = 32;          // tokens of K^ formed at a time (a quarter)
+constexpr int kStep = 64;       // tokens of K^ formed at a time
+constexpr int kSteps = C / kStep;
+// warps that form K^ (the first eight of them also hold the state), and a launch's threads
+constexpr int state_warps(bool state_only) { return state_only ? 16 : 8; }
+constexpr int threads(bool state_only) { return (7 + state_warps(state_only)) * 32; }
 constexpr uint32_t kColP = 0;     // Q K^T, then P (bf16) over it
 constexpr uint32_t kColO1 = 128;  // Q S^T
 constexpr uint32_t kColO2 = 256;  // P V
@@ -70,12 +75,12 @@ constexpr uint32_t kTmemCols = 512;
 
 template <int K, int V, bool STATE_ONLY>
 struct Lay {
-    static constexpr int NV = STATE_ONLY ? 2 : 1;    // tiles of V (two do not fit beside Q and S)
+    static constexpr int NB = STATE_ONLY ? 2 : 1;    // tiles of K and V (two do not fit beside Q and S)
     static constexpr int kK = C * K * 2, kV = C * V * 2;   // a tile of K (or Q), of V
     static constexpr int oK = 0;
-    static constexpr int oV = oK + 2 * kK;
-    static constexpr int oP = oV + NV * kV;          // second and third parts of K^
-    static constexpr int oQ = oP + 2 * kK;
+    static constexpr int oV = oK + NB * kK;
+    static constexpr int oP = oV + NB * kV;          // the three parts of K^
+    static constexpr int oQ = oP + 3 * kK;
     // bf16 S (V rows of K columns); between its last use and the next S, O on its way out
     static constexpr int oS = oQ + (STATE_ONLY ? 0 : kK);
     static constexpr int kBytes = oS + (STATE_ONLY ? 0 : V * 2 * C);
@@ -91,9 +96,12 @@ struct Args {
 
 struct Bars {
     uint64_t fullK[2], emptyK[2], fullV[2], emptyV[2], fullQ, emptyQ;
-    uint64_t qk_full, p_ready, o_full, o_free, o_staged, o_stored;
-    uint64_t kq_full[4], kq_free[4], s_ready, ds_full, ds_free, done[2];
+    uint64_t qk_full, p_ready, o_full, o_free, o_stored;
+    uint64_t kq_full[kSteps], kq_free[kSteps], s_ready, ds_full, ds_free, done[2];
 };
+
+// A condition whose code is kept out of the loop's straight line.
+__device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
 
 // The chunks of a range, one after another.
 struct Walk {
@@ -121,10 +129,11 @@ __device__ __forceinline__ uint32_t top2(float a, float b) {   // the upper 16 b
 __device__ __forceinline__ float top(float a) { return __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
 
 template <int K, int V, bool STATE_ONLY>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads(STATE_ONLY), 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, Args a) {
+                 const __grid_constant__ CUtensorMap tm_v, Args a) {
     using LY = Lay<K, V, STATE_ONLY>;
+    constexpr int NB = LY::NB, NW = state_warps(STATE_ONLY);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = tc::align1024(smem_raw);
     __shared__ Bars bars;
@@ -161,19 +170,20 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bars.fullK[i], 1);
             ptx::mbar_init(&bars.fullV[i], 1);
-            ptx::mbar_init(&bars.emptyK[i], 1);
-            ptx::mbar_init(&bars.emptyV[i], STATE_ONLY ? 1 : 2);   // one from either issuer
+            // K: read by Q K^T and by the warps that form K^; V: by either issuer's products
+            ptx::mbar_init(&bars.emptyK[i], NW + (STATE_ONLY ? 0 : 1));
+            ptx::mbar_init(&bars.emptyV[i], STATE_ONLY ? 1 : 2);
             ptx::mbar_init(&bars.done[i], 1);
         }
-        for (int i = 0; i < 4; ++i) {
-            ptx::mbar_init(&bars.kq_full[i], 8);
+        for (int i = 0; i < kSteps; ++i) {
+            ptx::mbar_init(&bars.kq_full[i], NW);
             ptx::mbar_init(&bars.kq_free[i], 1);
         }
-        uint64_t *one[] = {&bars.fullQ, &bars.emptyQ, &bars.qk_full, &bars.o_full, &bars.o_stored, &bars.ds_full};
+        uint64_t *one[] = {&bars.fullQ, &bars.emptyQ, &bars.qk_full, &bars.o_full, &bars.ds_full};
         for (uint64_t *b : one) ptx::mbar_init(b, 1);
         ptx::mbar_init(&bars.p_ready, 4);
         ptx::mbar_init(&bars.o_free, 4);
-        ptx::mbar_init(&bars.o_staged, 4);
+        ptx::mbar_init(&bars.o_stored, 4);
         ptx::mbar_init(&bars.s_ready, 8);
         ptx::mbar_init(&bars.ds_free, 8);
         ptx::fence_mbar_init();
@@ -188,61 +198,44 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
     const uint32_t lane_off = static_cast<uint32_t>(32 * q4) << 16;
-    auto sK = [&](int j) { return smem + LY::oK + (j & 1) * LY::kK; };
-    constexpr int NV = LY::NV;
-    auto sV = [&](int j) { return smem + LY::oV + (j % NV) * LY::kV; };
+    auto sK = [&](int j) { return smem + LY::oK + (j % NB) * LY::kK; };
+    auto sV = [&](int j) { return smem + LY::oV + (j % NB) * LY::kV; };
 
     if (warp == 0) {
         // ======================================================== TMA
         if (lane == 0 && !stall) {
             int last_k = -1, last_v = -1, last_q = -1;
             Walk wk(a, STATE_ONLY ? hi - 1 : lo), wv = wk, wq(a, lo);
-            auto load_k = [&](int j) {
-                if (j >= 2 && !wait_bar(&bars.emptyK[j & 1], ((j >> 1) - 1) & 1, &s_abort, st, bar_limit)) return false;
-                ptx::mbar_arrive_expect_tx(&bars.fullK[j & 1], LY::kK);
-#pragma unroll
-                for (int b = 0; b < K / 64; ++b)
-                    ptx::tma_load_3d(sK(j) + b * C * 128, &tm_k, &bars.fullK[j & 1], b * 64, wk.row(), (int)wk.seq);
-                // a single V waits for its buffer: bring it as far as L2 meanwhile
-                if (NV == 1) {
-#pragma unroll
-                    for (int b = 0; b < V / 64; ++b) ptx::tma_prefetch_3d(&tm_v, b * 64, wk.row(), (int)wk.seq);
-                }
+            // A tile that waits for its buffer is brought as far as L2 meanwhile: `ahead`, the
+            // chunk after the one that is loaded.
+            auto load = [&](const CUtensorMap &tm, uint8_t *dst, uint64_t &full, int width, Walk &w, bool ahead) {
+                ptx::mbar_arrive_expect_tx(&full, C * width * 2);
+                for (int b = 0; b < width / 64; ++b)
+                    ptx::tma_load_3d(dst + b * C * 128, &tm, &full, b * 64, w.row(), (int)w.seq);
+                STATE_ONLY ? w.prev() : w.next();
+                if (ahead)
+                    for (int b = 0; b < width / 64; ++b) ptx::tma_prefetch_3d(&tm, b * 64, w.row(), (int)w.seq);
+            };
+            auto free = [&](uint64_t *empty, int j) {   // chunk j's buffer of NB
+                return j < NB || wait_bar(&empty[j % NB], (j / NB - 1) & 1, &s_abort, st, bar_limit);
+            };
+            for (int j = 0; j < n; ++j) {
+                const bool ahead = NB == 1 && j + 1 < n;
+                if (!free(bars.emptyK, j)) break;
+                load(tm_k, sK(j), bars.fullK[j % NB], K, wk, ahead);
                 last_k = j;
-                STATE_ONLY ? wk.prev() : wk.next();
-                return true;
-            };
-            auto load_v = [&](int j) {
-                if (j >= NV && !wait_bar(&bars.emptyV[j % NV], (j / NV - 1) & 1, &s_abort, st, bar_limit)) return false;
-                ptx::mbar_arrive_expect_tx(&bars.fullV[j % NV], LY::kV);
-#pragma unroll
-                for (int b = 0; b < V / 64; ++b)
-                    ptx::tma_load_3d(sV(j) + b * C * 128, &tm_v, &bars.fullV[j % NV], b * 64, wv.row(), (int)wv.seq);
-                last_v = j;
-                STATE_ONLY ? wv.prev() : wv.next();
-                return true;
-            };
-            bool ok = load_k(0) && (!STATE_ONLY || load_v(0));
-            for (int j = 0; j < n && ok; ++j) {
                 if (!STATE_ONLY) {
                     if (j >= 1 && !wait_bar(&bars.emptyQ, (j - 1) & 1, &s_abort, st, bar_limit)) break;
-                    ptx::mbar_arrive_expect_tx(&bars.fullQ, LY::kK);
-#pragma unroll
-                    for (int b = 0; b < K / 64; ++b)
-                        ptx::tma_load_3d(smem + LY::oQ + b * C * 128, &tm_q, &bars.fullQ, b * 64, wq.row(), (int)wq.seq);
+                    load(tm_q, smem + LY::oQ, bars.fullQ, K, wq, ahead);
                     last_q = j;
-                    wq.next();
-                    if (j + 1 < n) {   // as V
-#pragma unroll
-                        for (int b = 0; b < K / 64; ++b) ptx::tma_prefetch_3d(&tm_q, b * 64, wq.row(), (int)wq.seq);
-                    }
                 }
-                if (STATE_ONLY) ok = j + 1 == n || (load_k(j + 1) && load_v(j + 1));
-                else ok = load_v(j) && (j + 1 == n || load_k(j + 1));
+                if (!free(bars.emptyV, j)) break;
+                load(tm_v, sV(j), bars.fullV[j % NB], V, wv, ahead);
+                last_v = j;
             }
             // every copy has landed before the CTA ends, also after an abort
-            for (int j = max(0, last_k - 1); j <= last_k; ++j) drain_bar(&bars.fullK[j & 1], (j >> 1) & 1);
-            for (int j = max(0, last_v - NV + 1); j <= last_v; ++j) drain_bar(&bars.fullV[j % NV], (j / NV) & 1);
+            for (int j = max(0, last_k - NB + 1); j <= last_k; ++j) drain_bar(&bars.fullK[j % NB], (j / NB) & 1);
+            for (int j = max(0, last_v - NB + 1); j <= last_v; ++j) drain_bar(&bars.fullV[j % NB], (j / NB) & 1);
             if (last_q >= 0) drain_bar(&bars.fullQ, last_q & 1);
         }
         __syncwarp();
@@ -256,59 +249,59 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int j = 0; j < n; ++j) {
                 const uint32_t k = ptx::smem_u32(sK(j)), v = ptx::smem_u32(sV(j));
                 // P's columns are free once the last P V has completed
-                if (!poll(bars.fullK[j & 1], j >> 1) || !poll(bars.fullQ, j) || (j && !poll(bars.o_full, j - 1))) break;
+                if (!poll(bars.fullK[j % NB], j / NB) || !poll(bars.fullQ, j) || (j && !poll(bars.o_full, j - 1))) break;
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < K / 16; ++ks)
                     ptx::umma_bf16(tmem + kColP, dk0(q) + koff(C, ks), dk0(k) + koff(C, ks), id_qk, ks > 0);
                 ptx::umma_commit(&bars.qk_full);
+                ptx::umma_commit(&bars.emptyK[j % NB]);
                 if (!poll(bars.s_ready, j) || (j && !poll(bars.o_free, j - 1))) break;
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < K / 16; ++ks)
                     ptx::umma_bf16(tmem + kColO1, dk0(q) + koff(C, ks), dk0(s) + koff(V, ks), id_qs, ks > 0);
                 ptx::umma_commit(&bars.emptyQ);
-                if (!poll(bars.fullV[j % NV], j / NV) || !poll(bars.p_ready, j)) break;
+                if (!poll(bars.fullV[j % NB], j / NB) || !poll(bars.p_ready, j)) break;
                 ptx::tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < C / 16; ++ks)
                     ptx::umma_bf16_ts(tmem + kColO2, tmem + kColP + 8 * ks, dmn0(v, C * 128) + mnoff(ks), id_pv, ks > 0);
                 ptx::umma_commit(&bars.o_full);
-                ptx::umma_commit(&bars.emptyV[j % NV]);
+                ptx::umma_commit(&bars.emptyV[j % NB]);
             }
             // every product issued has completed before TMEM is released
             ptx::umma_commit(&bars.done[0]);
             drain_bar(&bars.done[0], 0);
         }
         __syncwarp();
-    } else if (warp == 14) {
+    } else if (warp == 6 + NW) {
         // ======================================================== MMA issue: the state
         if (lane == 0) {
             const uint32_t id_d = ptx::idesc_bf16(V, K, 1, 1);
             const uint32_t parts = ptx::smem_u32(smem + LY::oP);
             bool ok = true;
             for (int j = 0; j < n && ok; ++j) {
-                const uint32_t k = ptx::smem_u32(sK(j)), v = ptx::smem_u32(sV(j));
-                ok = poll(bars.fullV[j % NV], j / NV) && (STATE_ONLY || !j || poll(bars.ds_free, j - 1));
+                const uint32_t v = ptx::smem_u32(sV(j));
+                ok = poll(bars.fullV[j % NB], j / NB) && (STATE_ONLY || !j || poll(bars.ds_free, j - 1));
 #pragma unroll 1
-                for (int qt = 0; ok && qt < 4; ++qt) {   // V^T K^ quarter by quarter, small parts first
-                    if (!(ok = poll(bars.kq_full[qt], j))) break;
+                for (int h = 0; ok && h < kSteps; ++h) {   // V^T K^ step by step, small parts first
+                    if (!(ok = poll(bars.kq_full[h], j))) break;
                     ptx::tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int part = 2; part >= 0; --part) {
-                        const uint64_t db = part == 0 ? dmn0(k, C * 128) + mnoff(2 * qt)
-                                                      : dmn0(parts + (part - 1) * LY::kK, C * 128) + mnoff(2 * qt);
+                        const uint64_t da = dmn0(v, C * 128) + mnoff(kStep / 16 * h);
+                        const uint64_t db = dmn0(parts + part * LY::kK, C * 128) + mnoff(kStep / 16 * h);
 #pragma unroll
-                        for (int ks = 0; ks < 2; ++ks)
-                            ptx::umma_bf16(tmem + kColD, dmn0(v, C * 128) + mnoff(2 * qt + ks), db + mnoff(ks), id_d,
-                                           qt > 0 || part < 2 || ks > 0 || (STATE_ONLY && j > 0));
+                        for (int ks = 0; ks < kStep / 16; ++ks)
+                            ptx::umma_bf16(tmem + kColD, da + mnoff(ks), db + mnoff(ks), id_d,
+                                           h > 0 || part < 2 || ks > 0 || (STATE_ONLY && j > 0));
                     }
-                    if (STATE_ONLY) ptx::umma_commit(&bars.kq_free[qt]);
+                    ptx::umma_commit(&bars.kq_free[h]);
                 }
                 if (!ok) break;
                 if (!STATE_ONLY || j == n - 1) ptx::umma_commit(&bars.ds_full);
-                ptx::umma_commit(&bars.emptyK[j & 1]);
-                ptx::umma_commit(&bars.emptyV[j % NV]);
+                ptx::umma_commit(&bars.emptyV[j % NB]);
             }
             ptx::umma_commit(&bars.done[1]);
             drain_bar(&bars.done[1], 0);
@@ -330,7 +323,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             Walk w(a, lo);
             for (int j = 0; j < n; ++j, w.next()) {
                 const int len = w.len();
-                if (w.seq != have || len != have_len) {
+                if (rare(w.seq != have || len != have_len)) {
                     const float dec = p.decay[w.seq % p.H];
                     __syncwarp();
                     col[lane] = decay_pow(dec, p.rev ? lane : 31 - lane).hi;
@@ -405,18 +398,27 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         tc::st_row_sw128(smem + LY::oS, C, r, c + 16 * h, z, 16);
                     }
                 }
-                ptx::fence_proxy_async_smem();
-                arrive(bars.o_staged);
-                if (warp == 2) {   // rows past the sequence's end are clipped
-                    if (!wait(bars.o_staged, j)) break;
-                    if (lane == 0) {
+                // the warp's 32 rows back out of shared memory, 16 bytes a lane and whole rows at a time
+                __syncwarp();
+                constexpr int LR = V / 8, RI = 32 / LR;   // lanes a row, rows at a time
+                const int rows = len - 32 * q4;
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) +
+                                   ((size_t)w.seq * p.T + w.row() + 32 * q4) * V + lane % LR * 8;
+                const uint8_t *src = smem + LY::oS + (lane % LR >> 3) * C * 128 + 32 * q4 * 128;
+#pragma unroll 1
+                for (int i = 0; i < 32; i += 4 * RI) {
+                    uint4 out[4];
 #pragma unroll
-                        for (int b = 0; b < V / 64; ++b)
-                            ptx::tma_store_3d(&tm_o, smem + LY::oS + b * C * 128, b * 64, w.row(), (int)w.seq);
-                        ptx::bulk_commit_group();
-                        ptx::bulk_wait_read_all();
+                    for (int m = 0; m < 4; ++m) {
+                        const int rr = i + m * RI + lane / LR;
+                        out[m] = *reinterpret_cast<const uint4 *>(src + rr * 128 + (((lane % LR) & 7) ^ (rr & 7)) * 16);
                     }
-                    arrive(bars.o_stored);
+                    if (i + 4 * RI == 32) arrive(bars.o_stored);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const int rr = i + m * RI + lane / LR;
+                        if (rr < rows) *reinterpret_cast<uint4 *>(o + (size_t)rr * V) = out[m];
+                    }
                 }
             }
         }
@@ -428,40 +430,109 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int row = V == 128 ? 32 * q4 + lane : 16 * q4 + lane;
         const bool act = V == 128 || lane < 16;
         constexpr size_t sb = (size_t)K * V;
-        // K^: lane = row of the quarter; a warp takes K / 8 columns
-        const int k0 = (warp - 6) * (K / 8);
-        float S[NC], wk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        Pow f = {1.0f, 0.0f};   // the chunk's whole decay; STATE_ONLY: from the chunk's end to the range's
-        Pow fc = {1.0f, 0.0f};
+        // K^: a lane takes the rows of its number in 32s, a warp NC8 pieces of eight columns (and,
+        // where there are more warps than pieces, a share of the rows)
+        constexpr int P8 = K / 8, NC8 = P8 > NW ? P8 / NW : 1, RG = NW > P8 ? NW / P8 : 1;
+        constexpr int NR = kStep / 32 / RG;   // 32s of rows a step
+        const int piece = (warp - 6) % (P8 / NC8) * NC8, rg = (warp - 6) / (P8 / NC8) * NR;
+        float S[STATE_ONLY ? 1 : NC], wk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        Pow f = {1.0f, 0.0f};    // the chunk's whole decay; STATE_ONLY: from the chunk's end to the range's
+        Pow fc = {1.0f, 0.0f}, fs;
         long long have = -1;
         int have_len = 0;
         bool ok = true;
-        Walk w(a, STATE_ONLY ? hi - 1 : lo);
+        Walk w(a, STATE_ONLY ? hi - 1 : lo), ws = w;   // the chunk whose K^ is formed; the one S enters
+        // Step by step K^; behind the first step of chunk j, while its products wait for it, the
+        // update of S by chunk j - 1 and the copy that chunk j reads.
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
-            const int len = w.len();
-            if (w.seq != have || len != have_len) {
-                const float dec = p.decay[w.seq % p.H];
-                if (!decay_ok(dec)) report_status(st, OSDN_ERR_DEVICE);
+        for (int step = 0; step <= n * kSteps; ++step) {
+            const int j = step / kSteps, h = step % kSteps;
+            if (h == 0) {
+                fs = f;
+                const int len = w.len();
+                if (rare(j < n && (w.seq != have || len != have_len))) {
+                    const float dec = p.decay[w.seq % p.H];
+                    if (!decay_ok(dec)) report_status(st, OSDN_ERR_DEVICE);
 #pragma unroll
-                for (int qt = 0; qt < 4; ++qt) {
-                    // the token's distance to the chunk's end, in the pass's direction
-                    const int kr = kQ * qt + lane, e = p.rev ? kr + 1 : len - 1 - kr;
-                    wk[qt] = decay_pow(dec, max(e, 0)).hi;
+                    for (int qt = 0; qt < 4; ++qt) {
+                        // the token's distance to the chunk's end, in the pass's direction
+                        const int kr = 32 * qt + lane, e = p.rev ? kr + 1 : len - 1 - kr;
+                        wk[qt] = decay_pow(dec, max(e, 0)).hi;
+                    }
+                    fc = decay_pow(dec, len);
+                    if (!STATE_ONLY) f = fc;
+                    have = w.seq;
+                    have_len = len;
                 }
-                fc = decay_pow(dec, len);
-                if (!STATE_ONLY) f = fc;
-                have = w.seq;
-                have_len = len;
             }
-            if (!STATE_ONLY) {
-                if (j == 0 || w.u == 0) {   // the state entering the range, or a sequence
+            if (j < n) {
+                if (!(ok = wait(bars.fullK[j % NB], j / NB))) break;
+                // K^ of the last chunk has been read
+                if (j && !(ok = wait(bars.kq_free[h], j - 1))) break;
+                const float2 minus = make_float2(-1.0f, -1.0f);
+#pragma unroll
+                for (int i = 0; i < NR * NC8; ++i) {
+                    const int r32 = h * (kStep / 32) + rg + i / NC8, c = piece + i % NC8;
+                    float wt = r32 < 2 ? (r32 ? wk[1] : wk[0]) : (r32 == 2 ? wk[2] : wk[3]);
+                    if (STATE_ONLY) wt *= f.hi;
+                    const float2 ww = make_float2(wt, wt);
+                    const int at = (c >> 3) * C * 128 + (32 * r32 + lane) * 128 + ((c & 7) ^ (lane & 7)) * 16;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(sK(j) + at);
+                    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t ph[4], pm[4], pl[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 x = __fmul2_rn(make_float2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), ww);
+                        const float2 m = __ffma2_rn(make_float2(top(x.x), top(x.y)), minus, x);
+                        const float2 l = __ffma2_rn(make_float2(top(m.x), top(m.y)), minus, m);
+                        ph[e] = top2(x.x, x.y);
+                        pm[e] = top2(m.x, m.y);
+                        pl[e] = top2(l.x, l.y);
+                    }
+                    uint8_t *dst = smem + LY::oP + at;
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                    *reinterpret_cast<uint4 *>(dst + LY::kK) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
+                    *reinterpret_cast<uint4 *>(dst + 2 * LY::kK) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                }
+                ptx::fence_proxy_async_smem();
+                arrive(bars.kq_full[h]);
+                if (h == kSteps - 1) {
+                    arrive(bars.emptyK[j % NB]);
+                    STATE_ONLY ? w.prev() : w.next();
+                    if (STATE_ONLY) f = pow_mul(f, fc);
+                }
+            }
+            if (STATE_ONLY || h) continue;
+            if (j) {
+                if (!(ok = wait(bars.ds_full, j - 1))) break;
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int e = 0; e < NC; e += 32) {
+                    float x[32];
+                    tc::tmem_ld32(tmem + lane_off + kColD + c0 + e, x);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) S[e + i] = fmaf(fs.hi, S[e + i], fmaf(fs.lo, S[e + i], x[i]));
+                }
+                ptx::tc_fence_before();
+                arrive(bars.ds_free);
+                if (rare(ws.u == a.s.nch - 1 && p.ST && act)) {
+                    float *dst = p.ST + (size_t)ws.seq * sb;
+#pragma unroll
+                    for (int e = 0; e < NC; e += 4) {
+                        const float x[4] = {S[e], S[e + 1], S[e + 2], S[e + 3]};
+                        store4(dst + (size_t)row * K + c0 + e, x);
+                    }
+                }
+                ws.next();
+            }
+            if (j < n) {
+                if (rare(j == 0 || ws.u == 0)) {   // the state entering the range, or a sequence
                     const float *src = nullptr;
                     bool tr = false;
-                    if (w.u > 0) {
+                    if (ws.u > 0) {
                         src = a.states + (size_t)g * sb;
                     } else if (p.S0.p) {
-                        src = p.S0.p + (size_t)w.seq * sb;
+                        src = p.S0.p + (size_t)ws.seq * sb;
                         tr = p.S0.transposed;
                     }
 #pragma unroll
@@ -482,78 +553,19 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 ptx::fence_proxy_async_smem();
                 arrive(bars.s_ready);
             }
-            // K as loaded has been read by Q K^T
-            if (!(ok = STATE_ONLY ? wait(bars.fullK[j & 1], j >> 1) : wait(bars.qk_full, j))) break;
-#pragma unroll 1
-            for (int qt = 0; qt < 4; ++qt) {
-                // the other parts have been read by the last chunk's product (before its S was)
-                if (STATE_ONLY && j && !(ok = wait(bars.kq_free[qt], j - 1))) break;
-                const int at = (k0 >> 6) * C * 128 + (kQ * qt + lane) * 128;
-                uint8_t *hi_row = sK(j) + at, *mid_row = smem + LY::oP + at, *lo_row = mid_row + LY::kK;
-                float wt = qt < 2 ? (qt ? wk[1] : wk[0]) : (qt == 2 ? wk[2] : wk[3]);
-                if (STATE_ONLY) wt *= f.hi;
-                const float2 ww = make_float2(wt, wt), minus = make_float2(-1.0f, -1.0f);
-#pragma unroll
-                for (int c = 0; c < K / 64; ++c) {
-                    const int off = ((((k0 & 63) >> 3) + c) ^ (lane & 7)) * 16;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(hi_row + off);
-                    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-                    uint32_t ph[4], pm[4], pl[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 x = __fmul2_rn(make_float2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), ww);
-                        const float2 m = __ffma2_rn(make_float2(top(x.x), top(x.y)), minus, x);
-                        const float2 l = __ffma2_rn(make_float2(top(m.x), top(m.y)), minus, m);
-                        ph[e] = top2(x.x, x.y);
-                        pm[e] = top2(m.x, m.y);
-                        pl[e] = top2(l.x, l.y);
-                    }
-                    *reinterpret_cast<uint4 *>(hi_row + off) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-                    *reinterpret_cast<uint4 *>(mid_row + off) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
-                    *reinterpret_cast<uint4 *>(lo_row + off) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-                }
-                ptx::fence_proxy_async_smem();
-                arrive(bars.kq_full[qt]);
-            }
-            if (!ok) break;
-            if (STATE_ONLY) {
-                f = pow_mul(f, fc);
-                w.prev();
-                if (j < n - 1) continue;
-            }
-            if (!(ok = wait(bars.ds_full, STATE_ONLY ? 0 : j))) break;
+        }
+        if (STATE_ONLY && ok && warp < 14 && wait(bars.ds_full, 0)) {   // eight warps read the sum
             ptx::tc_fence_after();
-#pragma unroll
+            float *dst = a.states + (size_t)(g + 1) * sb + (size_t)row * K + c0;
+#pragma unroll 1
             for (int e = 0; e < NC; e += 32) {
                 float x[32];
                 tc::tmem_ld32(tmem + lane_off + kColD + c0 + e, x);
+                if (!act) continue;
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    S[e + i] = STATE_ONLY ? x[i] : fmaf(f.hi, S[e + i], fmaf(f.lo, S[e + i], x[i]));
-            }
-            float *dst = nullptr;
-            bool tr = false;
-            if (STATE_ONLY) {
-                dst = a.states + (size_t)(g + 1) * sb;
-            } else {
-                ptx::tc_fence_before();
-                arrive(bars.ds_free);
-                if (w.u == a.s.nch - 1 && p.ST.p) {
-                    dst = p.ST.p + (size_t)w.seq * sb;
-                    tr = p.ST.transposed;
-                }
-                w.next();
-            }
-            if (dst && act) {
-#pragma unroll
-                for (int e = 0; e < NC; e += 4) {
-                    const float x[4] = {S[e], S[e + 1], S[e + 2], S[e + 3]};
-                    if (!tr) {
-                        store4(dst + (size_t)row * K + c0 + e, x);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) dst[(size_t)(c0 + e + i) * V + row] = x[i];
-                    }
+                for (int i = 0; i < 32; i += 4) {
+                    const float y[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
+                    store4(dst + e + i, y);
                 }
             }
         }
@@ -565,26 +577,26 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 template <int K, int V, bool STATE_ONLY>
-cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
-                   const Args &a, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Args &a,
+                   cudaStream_t stream) {
     constexpr int smem = Lay<K, V, STATE_ONLY>::kAlloc;
     static std::atomic<unsigned long long> attr_done{0};
     cudaError_t e = smem_attr_once((const void *)attend_tc_kernel<K, V, STATE_ONLY>, smem, attr_done);
     if (e != cudaSuccess) return e;
     // no range follows the last one, so nothing needs its state
-    attend_tc_kernel<K, V, STATE_ONLY><<<a.s.G - (STATE_ONLY ? 1 : 0), kThreads, smem, stream>>>(mq, mk, mv, mo, a);
+    attend_tc_kernel<K, V, STATE_ONLY><<<a.s.G - (STATE_ONLY ? 1 : 0), threads(STATE_ONLY), smem, stream>>>(mq, mk, mv, a);
     return cudaGetLastError();
 }
 
 template <int K, int V>
-cudaError_t run(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
-                const Args &a, cudaStream_t stream) {
+cudaError_t run(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Args &a,
+                cudaStream_t stream) {
     if (!unsplit(a.s, a.p.BH)) {
-        cudaError_t e = launch<K, V, true>(mq, mk, mv, mo, a, stream);
+        cudaError_t e = launch<K, V, true>(mq, mk, mv, a, stream);
         if (e == cudaSuccess) e = chain_states(a.p, a.s, a.states, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch<K, V, false>(mq, mk, mv, mo, a, stream);
+    return launch<K, V, false>(mq, mk, mv, a, stream);
 }
 
 }  // namespace
@@ -606,17 +618,17 @@ Split tc_split(int BH, int T, int, int) {
 
 cudaError_t attend_tc(const Pass &p, void *scratch, int *status, cudaStream_t stream) {
     if (!tc::tensor_map_encoder_ready()) return cudaErrorNotSupported;
-    CUtensorMap mq, mk, mv, mo;
+    CUtensorMap mq, mk, mv;
     if (!tc::make_map(&mq, p.q, p.BH, p.T, p.K, C) || !tc::make_map(&mk, p.k, p.BH, p.T, p.K, C) ||
-        !tc::make_map(&mv, p.v, p.BH, p.T, p.V, C) || !tc::make_map(&mo, p.o, p.BH, p.T, p.V, C))
+        !tc::make_map(&mv, p.v, p.BH, p.T, p.V, C))
         return cudaErrorInvalidValue;
     Args a;
     a.p = p;
     a.s = tc_split(p.BH, p.T, p.K, p.V);
     a.states = static_cast<float *>(scratch);
     a.status = status;
-    if (p.K == 128) return p.V == 128 ? run<128, 128>(mq, mk, mv, mo, a, stream) : run<128, 64>(mq, mk, mv, mo, a, stream);
-    return p.V == 128 ? run<64, 128>(mq, mk, mv, mo, a, stream) : run<64, 64>(mq, mk, mv, mo, a, stream);
+    if (p.K == 128) return p.V == 128 ? run<128, 128>(mq, mk, mv, a, stream) : run<128, 64>(mq, mk, mv, a, stream);
+    return p.V == 128 ? run<64, 128>(mq, mk, mv, a, stream) : run<64, 64>(mq, mk, mv, a, stream);
 }
 
 }  // namespace da

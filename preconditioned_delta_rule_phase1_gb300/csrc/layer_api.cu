@@ -77,7 +77,7 @@ int done(cudaError_t e) { return e == cudaSuccess ? OSDN_OK : OSDN_ERR_CUDA; }
 
 osdn::da::Pass make_pass(int BH, int H, int T, int K, int V, const void *q, const void *k,
                          const void *v, const float *decay, osdn::da::State S0, void *o,
-                         osdn::da::State ST, int rev) {
+                         float *ST, int rev) {
     osdn::da::Pass p;
     p.BH = BH; p.H = H; p.T = T; p.K = K; p.V = V;
     p.rev = rev;
@@ -90,7 +90,7 @@ osdn::da::Pass make_pass(int BH, int H, int T, int K, int V, const void *q, cons
 }
 osdn::da::State state(const float *p, int transposed = 0) {
     osdn::da::State s;
-    s.p = const_cast<float *>(p);
+    s.p = p;
     s.transposed = transposed;
     return s;
 }
@@ -131,7 +131,7 @@ int osdn_decay_attn(int io, int B, int H, int T, int K, int V, const void *q, co
     if (int c = check_device()) return c;
     cudaStream_t st = (cudaStream_t)stream;
     if (T == 0) return done(osdn::fill_state_launch(ST ? sb / 4 : 0, S0, 0.0f, ST, st));
-    const auto p = make_pass((int)BH, H, T, K, V, q, k, v, decay, state(S0), o, state(ST), 0);
+    const auto p = make_pass((int)BH, H, T, K, V, q, k, v, decay, state(S0), o, ST, 0);
     return done(attend(io, p, static_cast<char *>(workspace) + kStatusBytes,
                        static_cast<int *>(workspace), st));
 }
@@ -182,14 +182,13 @@ int osdn_decay_attn_backward(int io, int B, int H, int T, int K, int V, const vo
     if (T == 0) return done(osdn::fill_state_launch(dS0 ? sb / 4 : 0, d_ST, 0.0f, dS0, st));
     void *scratch = static_cast<char *>(workspace) + kStatusBytes;
     int *status = static_cast<int *>(workspace);
-    const auto none = state(nullptr);
-    cudaError_t r = attend(io, make_pass((int)BH, H, T, V, K, d_o, v, k, decay, state(S0, 1), dq, none, 0),
+    cudaError_t r = attend(io, make_pass((int)BH, H, T, V, K, d_o, v, k, decay, state(S0, 1), dq, nullptr, 0),
                            scratch, status, st);
     if (r == cudaSuccess)
-        r = attend(io, make_pass((int)BH, H, T, V, K, v, d_o, q, decay, state(d_ST, 1), dk, none, 1),
+        r = attend(io, make_pass((int)BH, H, T, V, K, v, d_o, q, decay, state(d_ST, 1), dk, nullptr, 1),
                    scratch, status, st);
     if (r == cudaSuccess)
-        r = attend(io, make_pass((int)BH, H, T, K, V, k, q, d_o, decay, state(d_ST), dv, state(dS0), 1),
+        r = attend(io, make_pass((int)BH, H, T, K, V, k, q, d_o, decay, state(d_ST), dv, dS0, 1),
                    scratch, status, st);
     return done(r);
 }
