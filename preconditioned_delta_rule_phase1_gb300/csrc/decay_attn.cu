@@ -30,7 +30,7 @@ constexpr int kUnit = 64;    // tokens a unit of the split
 struct Args {
     Pass p;
     Split s;
-    float *states;   // [G][V][K], see chain_states
+    float *states;   // [G][V][K], see chain_states; NULL: every range is a whole sequence
     int *status;
 };
 
@@ -45,11 +45,14 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
     const int pc = lane & 3, row = warp * 16 + (lane >> 2) * 2, row0 = blockIdx.x * kRows;
     const int g = blockIdx.y + gridDim.y * blockIdx.z;
     if (g >= a.s.G) return;
-    long long lo = a.s.lo(g, p.BH);
-    const long long hi = a.s.lo(g + 1, p.BH);
+    int lo = a.s.lo(g);
+    const int hi = a.s.lo(g + 1);
     if (STATE_ONLY) {   // only the sequence that this range leaves unfinished
+        dependents_may_start();
         if (g + 1 >= a.s.G || hi % a.s.nch == 0) return;
         lo = max(lo, hi / a.s.nch * a.s.nch);
+    } else if (a.states) {
+        dependency_wait();
     }
     const float *q = static_cast<const float *>(p.q), *k = static_cast<const float *>(p.k);
     const float *v = static_cast<const float *>(p.v);
@@ -57,10 +60,8 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
 
     constexpr int NK = kStage * K / (kThreads * 4), NV = kStage * kRows / (kThreads * 4);
     float rk[NK][4], rq[STATE_ONLY ? 1 : NK][4], rv[NV][4];
-    for (long long at = lo; at < hi;) {
-        const long long seq = at / a.s.nch;
-        const int u0 = (int)(at - seq * a.s.nch);
-        const int u1 = (int)min((long long)a.s.nch, u0 + (hi - at));
+    for (int at = lo; at < hi;) {
+        const int seq = at / a.s.nch, u0 = at - seq * a.s.nch, u1 = min(a.s.nch, u0 + (hi - at));
         const int tbeg = u0 * kUnit, tend = min(p.T, u1 * kUnit);
         at += u1 - u0;
         const float dec = p.decay[seq % p.H];
@@ -204,21 +205,22 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
 }
 
 // One thread per four state elements of a sequence: the states entering the
-// sequence's ranges, one after another.
+// sequence's ranges, one after another.  Up to kAhead ranges' states are
+// loaded before the first is used, and the powers between them (thread i's
+// the i-th) come first, so that the chain itself is fused multiply-adds
+//.
+constexpr int kAhead = 8;
 __global__ void __launch_bounds__(256) chain_states_kernel(Pass p, Split s, float *states) {
+    __shared__ Pow pows[kAhead];
     const size_t seq = grid_seq();
     if (seq >= (size_t)p.BH) return;
-    const int n = p.K * p.V;
-    const int e = (blockIdx.x * blockDim.x + threadIdx.x) * 4;
-    if (e >= n) return;
-    const long long beg = (long long)seq * s.nch, end = beg + s.nch;
+    const int n = p.K * p.V, tid = threadIdx.x;
+    const int e = (blockIdx.x * blockDim.x + tid) * 4;
+    const int beg = (int)seq * s.nch, end = beg + s.nch;
     // the first range that starts inside this sequence: the least g with lo(g) > beg
-    const long long N = (long long)p.BH * s.nch;
-    long long g = beg * s.G / N;
-    while (s.lo((int)g, p.BH) <= beg) ++g;
-    if (s.lo((int)g, p.BH) >= end) return;
+    int g = beg < s.more * (s.each + 1) ? beg / (s.each + 1) + 1 : s.more + (beg - s.more * (s.each + 1)) / s.each + 1;
     float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (p.S0.p) {
+    if (p.S0.p && e < n) {
         const float *src = p.S0.p + seq * n;
         if (!p.S0.transposed) {
             load4(src + e, c);
@@ -228,64 +230,73 @@ __global__ void __launch_bounds__(256) chain_states_kernel(Pass p, Split s, floa
         }
     }
     const float dec = p.decay[seq % p.H];
-    long long from = beg;
-    for (;;) {
-        const long long at = s.lo((int)g, p.BH);
-        if (at >= end) break;
-        float *st = states + (size_t)g * n + e;
-        float x[4];
-        load4(st, x);
-        const Pow f = decay_pow(dec, (unsigned)(s.before((int)(at - beg), p.T, p.rev) -
-                                                s.before((int)(from - beg), p.T, p.rev)));
+    dependents_may_start();
+    bool waited = false;
+    for (; g < s.G && s.lo(g) < end; g += kAhead) {
+        int m = 0;   // ranges of this round
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = fmaf(f.hi, c[i], fmaf(f.lo, c[i], x[i]));
-        store4(st, c);
-        from = at;
-        ++g;
+        for (int i = 0; i < kAhead; ++i) m += g + i < s.G && s.lo(g + i) < end;
+        __syncthreads();   // the last round's powers have been read
+        if (tid < m) {
+            const int at = s.lo(g + tid), from = max(beg, s.lo(g + tid - 1));
+            pows[tid] = decay_pow(dec, (unsigned)(s.before(at - beg, p.T, p.rev) - s.before(from - beg, p.T, p.rev)));
+        }
+        if (!waited) dependency_wait();
+        waited = true;
+        float x[kAhead][4];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (i < m && e < n) load4(states + (size_t)(g + i) * n + e, x[i]);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (i >= m) break;
+            const Pow f = pows[i];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[k] = fmaf(f.hi, c[k], fmaf(f.lo, c[k], x[i][k]));
+            if (e < n) store4(states + (size_t)(g + i) * n + e, c);
+        }
     }
+    // this launch completes only after the one before, whatever it had to do
+    if (!waited) dependency_wait();
 }
 
 template <int K>
 cudaError_t launch_simt(const Args &a, cudaStream_t stream) {
     const dim3 grid = seq_grid(a.p.V / kRows, a.s.G);
-    if (!unsplit(a.s, a.p.BH)) {
-        attend_simt_kernel<K, true><<<grid, kThreads, 0, stream>>>(a);
-        cudaError_t e = cudaGetLastError();
+    const bool split = a.states != nullptr;
+    cudaError_t e = cudaSuccess;
+    if (split) {
+        e = launch_overlapped(false, attend_simt_kernel<K, true>, grid, kThreads, 0, stream, a);
         if (e == cudaSuccess) e = chain_states(a.p, a.s, a.states, stream);
-        if (e != cudaSuccess) return e;
     }
-    attend_simt_kernel<K, false><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(split, attend_simt_kernel<K, false>, grid, kThreads, 0, stream, a);
 }
 
 }  // namespace
 
 cudaError_t chain_states(const Pass &p, const Split &s, float *states, cudaStream_t stream) {
     const dim3 grid = seq_grid((p.K * p.V / 4 + 255) / 256, p.BH);
-    chain_states_kernel<<<grid, 256, 0, stream>>>(p, s, states);
-    return cudaGetLastError();
+    return launch_overlapped(true, chain_states_kernel, grid, 256, 0, stream, p, s, states);
 }
 
 Split simt_split(int BH, int T, int K, int V) {
-    Split s;
-    s.unit = kUnit;
-    s.nch = (T + kUnit - 1) / kUnit;
-    s.G = BH;
+    const int nch = (int)(((long long)T + kUnit - 1) / kUnit);
     const long long slots = 152LL * 3 / (V / kRows);   // CTAs resident at once, in ranges
-    const long long N = (long long)BH * s.nch, G = std::min(N, slots);
+    const long long N = (long long)BH * nch, G = std::min(N, slots);
     // units in a row, one by one: a split pass costs about two thirds more, and two launches
     // (about 16 units' time)
-    const long long whole = (BH + slots - 1) / slots * s.nch;
+    const long long whole = (BH + slots - 1) / slots * nch;
     const long long split = (N + G - 1) / G * 5 / 3 + 16;
-    if (G > BH && split < whole) s.G = (int)G;
-    return s;
+    return make_split(kUnit, 0, BH, T, (int)(G > BH && split < whole ? G : BH));
 }
 
 cudaError_t attend_simt(const Pass &p, void *scratch, int *status, cudaStream_t stream) {
     Args a;
     a.p = p;
     a.s = simt_split(p.BH, p.T, p.K, p.V);
-    a.states = static_cast<float *>(scratch);
+    a.states = unsplit(a.s, p.BH) ? nullptr : static_cast<float *>(scratch);
     a.status = status;
     return p.K == 128 ? launch_simt<128>(a, stream) : launch_simt<64>(a, stream);
 }

@@ -37,7 +37,7 @@ struct Pass {
 
 // The time axis in `nch` units of `unit` tokens a sequence; the BH nch units,
 // sequence by sequence, are cut into G ranges of nearly equal length, one a
-// CTA.  A range that starts inside a sequence starts from the state that the
+// CTA (BH nch fits 31 bits: a unit is 8 KB or more of K alone).  A range that starts inside a sequence starts from the state that the
 // range before it leaves: a first pass forms what each range adds to that
 // state (its units of the sequence it ends in), a small kernel chains them.
 // Backwards in time the units start at the sequence's last token or, with
@@ -45,9 +45,8 @@ struct Pass {
 // that may be short then comes first).
 struct Split {
     int unit, nch, G, natural = 0;
-    __host__ __device__ long long lo(int g, int BH) const {
-        return (long long)BH * nch * g / G;
-    }
+    int each, more;   // range g: each units, and one more for g < more
+    __host__ __device__ int lo(int g) const { return g * each + (g < more ? g : more); }
     // tokens before unit u of a sequence, in the pass's direction
     __device__ long long before(int u, int T, int rev) const {
         return rev && natural && u > 0 ? T - (long long)(nch - u) * unit : (long long)u * unit;
@@ -74,8 +73,24 @@ __device__ __forceinline__ Pow decay_pow(float a, unsigned n) {
     }
     return r;
 }
+// a^n for a weight that is used once (an exponent of a chunk's length, so that rounding
+// n log2(a) costs 1e-7 where the weight counts), from log2(a); a = 0: 0^0 = 1.
+__device__ __forceinline__ float decay_log2(float a) { return fmaxf(log2f(a), -1e30f); }
+__device__ __forceinline__ float weight(float l2, int n) { return exp2f(l2 * (float)n); }
 __device__ __forceinline__ bool decay_ok(float a) { return a >= 0.0f && a <= 1.0f; }
 
+// The units cut into G ranges.
+inline Split make_split(int unit, int natural, int BH, int T, int G) {
+    Split s;
+    s.unit = unit;
+    s.natural = natural;
+    s.nch = (int)(((long long)T + unit - 1) / unit);
+    s.G = G;
+    const long long n = (long long)BH * s.nch;
+    s.each = (int)(n / G);
+    s.more = (int)(n % G);
+    return s;
+}
 // Bytes of the ranges' states ([G][V][K] fp32; none for a single range a sequence).
 inline size_t split_bytes(const Split &s, int BH, int K, int V) {
     return s.G > BH ? (size_t)s.G * K * V * 4 : 0;
@@ -86,6 +101,28 @@ inline bool unsplit(const Split &s, int BH) { return s.G == BH; }
 // states[g], g = 1 .. G-1: in, what range g-1 adds to the state it was given;
 // out, the state entering range g (ranges that start a sequence: untouched).
 cudaError_t chain_states(const Pass &p, const Split &s, float *states, cudaStream_t stream);
+
+// The three launches of a split pass overlap: each may start while the one before still runs, does
+// what does not depend on it, and waits (dependency_wait) for its completion before the rest.
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependents_may_start() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(bool overlap, void (*kernel)(P...), dim3 grid, int block, size_t smem,
+                              cudaStream_t stream, const A &...args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = grid;
+    c.blockDim = dim3(block);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &at;
+    c.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&c, kernel, args...);
+}
 
 // The token recurrence (fp32 I/O) and the chunked tensor-core form (bf16 I/O).
 Split simt_split(int BH, int T, int K, int V);

@@ -90,7 +90,7 @@ struct Lay {
 struct Args {
     Pass p;
     Split s;
-    float *states;   // [G][V][K], see chain_states
+    float *states;   // [G][V][K], see chain_states; NULL: every range is a whole sequence
     int *status;     // status[1]: test word, see osdn.h
 };
 
@@ -105,11 +105,10 @@ __device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
 
 // The chunks of a range, one after another.
 struct Walk {
-    long long seq;
-    int u, nch, T, rev;
-    __device__ Walk(const Args &a, long long at) : nch(a.s.nch), T(a.p.T), rev(a.p.rev) {
+    int seq, u, nch, T, rev;
+    __device__ Walk(const Args &a, int at) : nch(a.s.nch), T(a.p.T), rev(a.p.rev) {
         seq = at / nch;
-        u = (int)(at - seq * nch);
+        u = at - seq * nch;
     }
     __device__ void next() {
         if (++u == nch) {
@@ -144,13 +143,14 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, q4 = warp & 3;
     const int g = blockIdx.x;
     const Pass &p = a.p;
-    long long lo = a.s.lo(g, p.BH);
-    const long long hi = a.s.lo(g + 1, p.BH);
+    int lo = a.s.lo(g);
+    const int hi = a.s.lo(g + 1);
     if (STATE_ONLY) {   // only the sequence that this range leaves unfinished
+        dependents_may_start();
         if (hi % a.s.nch == 0) return;
         lo = max(lo, hi / a.s.nch * a.s.nch);
     }
-    const int n = (int)(hi - lo);
+    const int n = hi - lo;
     int *st = a.status;
     const int stall = *reinterpret_cast<volatile int *>(st + 1);
     const uint32_t bar_limit = stall ? 64u : tc::kWaitLimit;
@@ -211,10 +211,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             auto load = [&](const CUtensorMap &tm, uint8_t *dst, uint64_t &full, int width, Walk &w, bool ahead) {
                 ptx::mbar_arrive_expect_tx(&full, C * width * 2);
                 for (int b = 0; b < width / 64; ++b)
-                    ptx::tma_load_3d(dst + b * C * 128, &tm, &full, b * 64, w.row(), (int)w.seq);
+                    ptx::tma_load_3d(dst + b * C * 128, &tm, &full, b * 64, w.row(), w.seq);
                 STATE_ONLY ? w.prev() : w.next();
                 if (ahead)
-                    for (int b = 0; b < width / 64; ++b) ptx::tma_prefetch_3d(&tm, b * 64, w.row(), (int)w.seq);
+                    for (int b = 0; b < width / 64; ++b) ptx::tma_prefetch_3d(&tm, b * 64, w.row(), w.seq);
             };
             auto free = [&](uint64_t *empty, int j) {   // chunk j's buffer of NB
                 return j < NB || wait_bar(&empty[j % NB], (j / NB - 1) & 1, &s_abort, st, bar_limit);
@@ -318,7 +318,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             float *col = s_pow[warp - 2] + 32;
             const float *diag = col + (p.rev ? -lane : 31 - lane);
             float wq = 0.0f, far[3] = {0.0f, 0.0f, 0.0f};
-            long long have = -1;
+            int have = -1;
             int have_len = 0;
             Walk w(a, lo);
             for (int j = 0; j < n; ++j, w.next()) {
@@ -326,12 +326,13 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (rare(w.seq != have || len != have_len)) {
                     const float dec = p.decay[w.seq % p.H];
                     __syncwarp();
-                    col[lane] = decay_pow(dec, p.rev ? lane : 31 - lane).hi;
+                    const float l2 = decay_log2(dec);
+                    col[lane] = weight(l2, p.rev ? lane : 31 - lane);
                     col[lane - 32] = col[lane + 32] = 0.0f;
                     __syncwarp();
-                    wq = decay_pow(dec, p.rev ? max(len - 1 - r, 0) : r + 1).hi;
+                    wq = weight(l2, p.rev ? max(len - 1 - r, 0) : r + 1);
 #pragma unroll
-                    for (int d = 0; d < 3; ++d) far[d] = decay_pow(dec, (p.rev ? 31 - lane : lane) + 1 + 32 * d).hi;
+                    for (int d = 0; d < 3; ++d) far[d] = weight(l2, (p.rev ? 31 - lane : lane) + 1 + 32 * d);
                     have = w.seq;
                     have_len = len;
                 }
@@ -438,7 +439,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         float S[STATE_ONLY ? 1 : NC], wk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         Pow f = {1.0f, 0.0f};    // the chunk's whole decay; STATE_ONLY: from the chunk's end to the range's
         Pow fc = {1.0f, 0.0f}, fs;
-        long long have = -1;
+        int have = -1;
         int have_len = 0;
         bool ok = true;
         Walk w(a, STATE_ONLY ? hi - 1 : lo), ws = w;   // the chunk whose K^ is formed; the one S enters
@@ -453,11 +454,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (rare(j < n && (w.seq != have || len != have_len))) {
                     const float dec = p.decay[w.seq % p.H];
                     if (!decay_ok(dec)) report_status(st, OSDN_ERR_DEVICE);
+                    const float l2 = decay_log2(dec);
 #pragma unroll
                     for (int qt = 0; qt < 4; ++qt) {
                         // the token's distance to the chunk's end, in the pass's direction
                         const int kr = 32 * qt + lane, e = p.rev ? kr + 1 : len - 1 - kr;
-                        wk[qt] = decay_pow(dec, max(e, 0)).hi;
+                        wk[qt] = weight(l2, max(e, 0));
                     }
                     fc = decay_pow(dec, len);
                     if (!STATE_ONLY) f = fc;
@@ -530,6 +532,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     const float *src = nullptr;
                     bool tr = false;
                     if (ws.u > 0) {
+                        dependency_wait();
                         src = a.states + (size_t)g * sb;
                     } else if (p.S0.p) {
                         src = p.S0.p + (size_t)ws.seq * sb;
@@ -584,14 +587,14 @@ cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorM
     cudaError_t e = smem_attr_once((const void *)attend_tc_kernel<K, V, STATE_ONLY>, smem, attr_done);
     if (e != cudaSuccess) return e;
     // no range follows the last one, so nothing needs its state
-    attend_tc_kernel<K, V, STATE_ONLY><<<a.s.G - (STATE_ONLY ? 1 : 0), threads(STATE_ONLY), smem, stream>>>(mq, mk, mv, a);
-    return cudaGetLastError();
+    return launch_overlapped(!STATE_ONLY && a.states, attend_tc_kernel<K, V, STATE_ONLY>,
+                             dim3(a.s.G - (STATE_ONLY ? 1 : 0)), threads(STATE_ONLY), smem, stream, mq, mk, mv, a);
 }
 
 template <int K, int V>
 cudaError_t run(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Args &a,
                 cudaStream_t stream) {
-    if (!unsplit(a.s, a.p.BH)) {
+    if (a.states) {
         cudaError_t e = launch<K, V, true>(mq, mk, mv, a, stream);
         if (e == cudaSuccess) e = chain_states(a.p, a.s, a.states, stream);
         if (e != cudaSuccess) return e;
@@ -602,18 +605,13 @@ cudaError_t run(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap 
 }  // namespace
 
 Split tc_split(int BH, int T, int, int) {
-    Split s;
-    s.unit = C;
-    s.natural = 1;
-    s.nch = (T + C - 1) / C;
-    s.G = BH;
-    const long long slots = tc::sm_count(), N = (long long)BH * s.nch, G = std::min(N, slots);
+    const int nch = (int)(((long long)T + C - 1) / C);
+    const long long slots = tc::sm_count(), N = (long long)BH * nch, G = std::min(N, slots);
     // chunks in a row: a split pass reads K and V twice (half as much again), and has two more
     // launches (about three chunks' time)
-    const long long whole = (BH + slots - 1) / slots * s.nch;
+    const long long whole = (BH + slots - 1) / slots * nch;
     const long long split = (N + G - 1) / G * 3 / 2 + 3;
-    if (G > BH && split < whole) s.G = (int)G;
-    return s;
+    return make_split(C, 1, BH, T, (int)(G > BH && split < whole ? G : BH));
 }
 
 cudaError_t attend_tc(const Pass &p, void *scratch, int *status, cudaStream_t stream) {
@@ -625,7 +623,7 @@ cudaError_t attend_tc(const Pass &p, void *scratch, int *status, cudaStream_t st
     Args a;
     a.p = p;
     a.s = tc_split(p.BH, p.T, p.K, p.V);
-    a.states = static_cast<float *>(scratch);
+    a.states = unsplit(a.s, p.BH) ? nullptr : static_cast<float *>(scratch);
     a.status = status;
     if (p.K == 128) return p.V == 128 ? run<128, 128>(mq, mk, mv, a, stream) : run<128, 64>(mq, mk, mv, a, stream);
     return p.V == 128 ? run<64, 128>(mq, mk, mv, a, stream) : run<64, 64>(mq, mk, mv, a, stream);

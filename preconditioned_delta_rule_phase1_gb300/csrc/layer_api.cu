@@ -43,6 +43,10 @@ bool dims_ok(int B, int H, int T) {
     return B >= 0 && H >= 0 && T >= 0 && T <= kMaxTokens && (size_t)B * (size_t)H <= kMaxSeqs;
 }
 
+// Units of the attention's time axis over all sequences, numbered in 31 bits (2^31 of the smaller
+// ones are 17 TB of K).
+size_t units(size_t BH, int T) { return BH * (((size_t)T + 63) / 64); }
+
 int check_device() {
     int dev = 0, major = 0, minor = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -128,6 +132,7 @@ int osdn_decay_attn(int io, int B, int H, int T, int K, int V, const void *q, co
     const Buf bufs[] = {{q, kb, false}, {k, kb, false}, {v, vb, false}, {decay, (size_t)H * 4, false},
                         {S0, sb, false}, {o, vb, true}, {ST, sb, true}, {workspace, workspace_bytes, true}};
     if (int c = check_bufs(bufs)) return c;
+    if (units(BH, T) > 0x7fffffff) return OSDN_ERR_DIMS;
     if (int c = check_device()) return c;
     cudaStream_t st = (cudaStream_t)stream;
     if (T == 0) return done(osdn::fill_state_launch(ST ? sb / 4 : 0, S0, 0.0f, ST, st));
@@ -177,6 +182,7 @@ int osdn_decay_attn_backward(int io, int B, int H, int T, int K, int V, const vo
                         {S0, sb, false}, {d_o, vb, false}, {d_ST, sb, false}, {dq, kb, true},
                         {dk, kb, true}, {dv, vb, true}, {dS0, sb, true}, {workspace, workspace_bytes, true}};
     if (int c = check_bufs(bufs)) return c;
+    if (units(BH, T) > 0x7fffffff) return OSDN_ERR_DIMS;
     if (int c = check_device()) return c;
     cudaStream_t st = (cudaStream_t)stream;
     if (T == 0) return done(osdn::fill_state_launch(dS0 ? sb / 4 : 0, d_ST, 0.0f, dS0, st));
