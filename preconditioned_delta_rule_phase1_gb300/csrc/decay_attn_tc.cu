@@ -35,7 +35,8 @@
 // the next is formed, and, behind the first step of the chunk after it, the
 // update of S; 14 MMA issue for the state.
 // Buffers are single (224 KB hold one chunk's K, V, Q, S and three parts of
-// K^): the next chunk's tiles wait in L2, brought there a chunk ahead.
+// K^): the next chunk's tiles wait in L2, brought there a chunk ahead, and
+// are loaded as their places fall free, K by halves.
 // STATE_ONLY takes its chunks last to first with weights up to the range's
 // end, so that they add up in TMEM and only the sum is read; it also leaves
 // in L2 what the second launch reads first.  The roles' loops are kept short
@@ -75,12 +76,14 @@ constexpr uint32_t kTmemCols = 512;
 
 template <int K, int V, bool STATE_ONLY>
 struct Lay {
-    static constexpr int NB = STATE_ONLY ? 2 : 1;    // tiles of K and V (two do not fit beside Q and S)
+    static constexpr int NV = STATE_ONLY ? 2 : 1;          // tiles of V (two do not fit beside Q and S)
     static constexpr int kK = C * K * 2, kV = C * V * 2;   // a tile of K (or Q), of V
     static constexpr int oK = 0;
-    static constexpr int oV = oK + NB * kK;
-    static constexpr int oP = oV + NB * kV;          // the three parts of K^
-    static constexpr int oQ = oP + 3 * kK;
+    static constexpr int oV = oK + 2 * kK;
+    // the parts of K^: the second and third (the first takes K's place), in STATE_ONLY all three
+    // (K's place is free the earlier)
+    static constexpr int oP = oV + NV * kV;
+    static constexpr int oQ = oP + (STATE_ONLY ? 3 : 2) * kK;
     // bf16 S (V rows of K columns); between its last use and the next S, O on its way out
     static constexpr int oS = oQ + (STATE_ONLY ? 0 : kK);
     static constexpr int kBytes = oS + (STATE_ONLY ? 0 : V * 2 * C);
@@ -102,6 +105,14 @@ struct Bars {
 
 // A condition whose code is kept out of the loop's straight line.
 __device__ __forceinline__ bool rare(bool c) { return __builtin_expect(c, 0); }
+
+// The waits' loops, once in the kernel instead of at every wait.
+__device__ __noinline__ bool wait_on(uint64_t *b, uint32_t parity, volatile int *abort, int *st, uint32_t limit) {
+    return wait_bar(b, parity, abort, st, limit);
+}
+__device__ __noinline__ bool poll_on(uint64_t *b, uint32_t parity, volatile int *abort, int *st, uint32_t limit) {
+    return wait_poll(b, parity, abort, st, limit);
+}
 
 // The chunks of a range, one after another.
 struct Walk {
@@ -132,7 +143,7 @@ __global__ void __launch_bounds__(threads(STATE_ONLY), 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, Args a) {
     using LY = Lay<K, V, STATE_ONLY>;
-    constexpr int NB = LY::NB, NW = state_warps(STATE_ONLY);
+    constexpr int NV = LY::NV, NW = state_warps(STATE_ONLY);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = tc::align1024(smem_raw);
     __shared__ Bars bars;
@@ -156,10 +167,10 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t bar_limit = stall ? 64u : tc::kWaitLimit;
     const uint32_t poll_limit = stall ? (1u << 14) : (tc::kWaitLimit << 11);
     auto wait = [&](uint64_t &b, int parity) {   // by a whole warp
-        return __all_sync(kFullMask, wait_bar(&b, parity & 1, &s_abort, st, bar_limit));
+        return __all_sync(kFullMask, ptx::mbar_try_wait(&b, parity & 1) || wait_on(&b, parity & 1, &s_abort, st, bar_limit));
     };
     auto poll = [&](uint64_t &b, int parity) {   // by one thread, on the critical path
-        return wait_poll(&b, parity & 1, &s_abort, st, poll_limit);
+        return ptx::mbar_try_wait(&b, parity & 1) || poll_on(&b, parity & 1, &s_abort, st, poll_limit);
     };
     auto arrive = [&](uint64_t &b) {
         __syncwarp();
@@ -170,8 +181,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&bars.fullK[i], 1);
             ptx::mbar_init(&bars.fullV[i], 1);
-            // K: read by Q K^T and by the warps that form K^; V: by either issuer's products
-            ptx::mbar_init(&bars.emptyK[i], NW + (STATE_ONLY ? 0 : 1));
+            // K's place: free once it has been read (STATE_ONLY) or, as K^'s first part, multiplied
+            ptx::mbar_init(&bars.emptyK[i], STATE_ONLY ? NW : 1);
             ptx::mbar_init(&bars.emptyV[i], STATE_ONLY ? 1 : 2);
             ptx::mbar_init(&bars.done[i], 1);
         }
@@ -198,45 +209,41 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     ptx::tc_fence_after();
     const uint32_t tmem = tmem_base_sh;
     const uint32_t lane_off = static_cast<uint32_t>(32 * q4) << 16;
-    auto sK = [&](int j) { return smem + LY::oK + (j % NB) * LY::kK; };
-    auto sV = [&](int j) { return smem + LY::oV + (j % NB) * LY::kV; };
+    auto sK = [&](int j) { return smem + LY::oK + (j & 1) * LY::kK; };
+    auto sV = [&](int j) { return smem + LY::oV + (j % NV) * LY::kV; };
 
     if (warp == 0) {
         // ======================================================== TMA
         if (lane == 0 && !stall) {
-            int last_k = -1, last_v = -1, last_q = -1;
-            Walk wk(a, STATE_ONLY ? hi - 1 : lo), wv = wk, wq(a, lo);
-            // A tile that waits for its buffer is brought as far as L2 meanwhile: `ahead`, the
-            // chunk after the one that is loaded.
-            auto load = [&](const CUtensorMap &tm, uint8_t *dst, uint64_t &full, int width, Walk &w, bool ahead) {
-                ptx::mbar_arrive_expect_tx(&full, C * width * 2);
+            // One loop over all loads, in the order in which their places fall free: K a chunk ahead,
+            // (not STATE_ONLY) Q, V.
+            constexpr int kinds = STATE_ONLY ? 2 : 3;
+            int last[3] = {-1, -1, -1};
+            Walk w(a, STATE_ONLY ? hi - 1 : lo);
+#pragma unroll 1
+            for (int i = 0; i < n * kinds; ++i) {
+                const int j = i / kinds, kind = i % kinds;
+                const bool is_k = kind == 0, is_v = kind == kinds - 1;
+                const int nb = is_k ? 2 : is_v ? NV : 1, at = is_k ? j & 1 : is_v ? j % NV : 0;
+                uint64_t *full = is_v ? &bars.fullV[at] : is_k ? &bars.fullK[at] : &bars.fullQ;
+                uint64_t *empty = is_v ? &bars.emptyV[at] : is_k ? &bars.emptyK[at] : &bars.emptyQ;
+                if (j >= nb && !wait_on(empty, (j / nb - 1) & 1, &s_abort, st, bar_limit)) break;
+                const CUtensorMap *tm = is_v ? &tm_v : is_k ? &tm_k : &tm_q;
+                uint8_t *dst = is_v ? sV(j) : is_k ? sK(j) : smem + LY::oQ;
+                const int width = is_v ? V : K;
+                ptx::mbar_arrive_expect_tx(full, C * width * 2);
+#pragma unroll 1
                 for (int b = 0; b < width / 64; ++b)
-                    ptx::tma_load_3d(dst + b * C * 128, &tm, &full, b * 64, w.row(), w.seq);
-                STATE_ONLY ? w.prev() : w.next();
-                if (ahead)
-                    for (int b = 0; b < width / 64; ++b) ptx::tma_prefetch_3d(&tm, b * 64, w.row(), w.seq);
-            };
-            auto free = [&](uint64_t *empty, int j) {   // chunk j's buffer of NB
-                return j < NB || wait_bar(&empty[j % NB], (j / NB - 1) & 1, &s_abort, st, bar_limit);
-            };
-            for (int j = 0; j < n; ++j) {
-                const bool ahead = NB == 1 && j + 1 < n;
-                if (!free(bars.emptyK, j)) break;
-                load(tm_k, sK(j), bars.fullK[j % NB], K, wk, ahead);
-                last_k = j;
-                if (!STATE_ONLY) {
-                    if (j >= 1 && !wait_bar(&bars.emptyQ, (j - 1) & 1, &s_abort, st, bar_limit)) break;
-                    load(tm_q, smem + LY::oQ, bars.fullQ, K, wq, ahead);
-                    last_q = j;
-                }
-                if (!free(bars.emptyV, j)) break;
-                load(tm_v, sV(j), bars.fullV[j % NB], V, wv, ahead);
-                last_v = j;
+                    ptx::tma_load_3d(dst + b * C * 128, tm, full, b * 64, w.row(), w.seq);
+                if (is_k) last[0] = j;
+                else if (is_v) last[2] = j;
+                else last[1] = j;
+                if (is_v) STATE_ONLY ? w.prev() : w.next();
             }
             // every copy has landed before the CTA ends, also after an abort
-            for (int j = max(0, last_k - NB + 1); j <= last_k; ++j) drain_bar(&bars.fullK[j % NB], (j / NB) & 1);
-            for (int j = max(0, last_v - NB + 1); j <= last_v; ++j) drain_bar(&bars.fullV[j % NB], (j / NB) & 1);
-            if (last_q >= 0) drain_bar(&bars.fullQ, last_q & 1);
+            for (int j = max(0, last[0] - 1); j <= last[0]; ++j) drain_bar(&bars.fullK[j & 1], (j >> 1) & 1);
+            for (int j = max(0, last[2] - NV + 1); j <= last[2]; ++j) drain_bar(&bars.fullV[j % NV], (j / NV) & 1);
+            if (last[1] >= 0) drain_bar(&bars.fullQ, last[1] & 1);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -249,26 +256,31 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int j = 0; j < n; ++j) {
                 const uint32_t k = ptx::smem_u32(sK(j)), v = ptx::smem_u32(sV(j));
                 // P's columns are free once the last P V has completed
-                if (!poll(bars.fullK[j % NB], j / NB) || !poll(bars.fullQ, j) || (j && !poll(bars.o_full, j - 1))) break;
+                if (!poll(bars.fullK[j & 1], j >> 1) || !poll(bars.fullQ, j) || (j && !poll(bars.o_full, j - 1))) break;
                 ptx::tc_fence_after();
+#pragma unroll 1
+                for (int b = 0; b < K / 64; ++b)
 #pragma unroll
-                for (int ks = 0; ks < K / 16; ++ks)
-                    ptx::umma_bf16(tmem + kColP, dk0(q) + koff(C, ks), dk0(k) + koff(C, ks), id_qk, ks > 0);
+                    for (int ks = 0; ks < 4; ++ks)
+                        ptx::umma_bf16(tmem + kColP, dk0(q + b * C * 128) + koff(C, ks), dk0(k + b * C * 128) + koff(C, ks), id_qk, b + ks > 0);
                 ptx::umma_commit(&bars.qk_full);
-                ptx::umma_commit(&bars.emptyK[j % NB]);
                 if (!poll(bars.s_ready, j) || (j && !poll(bars.o_free, j - 1))) break;
                 ptx::tc_fence_after();
+#pragma unroll 1
+                for (int b = 0; b < K / 64; ++b)
 #pragma unroll
-                for (int ks = 0; ks < K / 16; ++ks)
-                    ptx::umma_bf16(tmem + kColO1, dk0(q) + koff(C, ks), dk0(s) + koff(V, ks), id_qs, ks > 0);
+                    for (int ks = 0; ks < 4; ++ks)
+                        ptx::umma_bf16(tmem + kColO1, dk0(q + b * C * 128) + koff(C, ks), dk0(s + b * V * 128) + koff(V, ks), id_qs, b + ks > 0);
                 ptx::umma_commit(&bars.emptyQ);
-                if (!poll(bars.fullV[j % NB], j / NB) || !poll(bars.p_ready, j)) break;
+                if (!poll(bars.fullV[j % NV], j / NV) || !poll(bars.p_ready, j)) break;
                 ptx::tc_fence_after();
+#pragma unroll 1
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int ks = 0; ks < C / 16; ++ks)
-                    ptx::umma_bf16_ts(tmem + kColO2, tmem + kColP + 8 * ks, dmn0(v, C * 128) + mnoff(ks), id_pv, ks > 0);
+                    for (int ks = 0; ks < C / 32; ++ks)
+                        ptx::umma_bf16_ts(tmem + kColO2, tmem + kColP + 8 * (ks + b * C / 32), dmn0(v + b * C * 64, C * 128) + mnoff(ks), id_pv, b + ks > 0);
                 ptx::umma_commit(&bars.o_full);
-                ptx::umma_commit(&bars.emptyV[j % NB]);
+                ptx::umma_commit(&bars.emptyV[j % NV]);
             }
             // every product issued has completed before TMEM is released
             ptx::umma_commit(&bars.done[0]);
@@ -283,7 +295,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             bool ok = true;
             for (int j = 0; j < n && ok; ++j) {
                 const uint32_t v = ptx::smem_u32(sV(j));
-                ok = poll(bars.fullV[j % NB], j / NB) && (STATE_ONLY || !j || poll(bars.ds_free, j - 1));
+                ok = poll(bars.fullV[j % NV], j / NV) && (STATE_ONLY || !j || poll(bars.ds_free, j - 1));
 #pragma unroll 1
                 for (int h = 0; ok && h < kSteps; ++h) {   // V^T K^ step by step, small parts first
                     if (!(ok = poll(bars.kq_full[h], j))) break;
@@ -291,17 +303,19 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
                     for (int part = 2; part >= 0; --part) {
                         const uint64_t da = dmn0(v, C * 128) + mnoff(kStep / 16 * h);
-                        const uint64_t db = dmn0(parts + part * LY::kK, C * 128) + mnoff(kStep / 16 * h);
+                        const uint32_t at = STATE_ONLY ? parts + part * LY::kK : part ? parts + (part - 1) * LY::kK : ptx::smem_u32(sK(j));
+                        const uint64_t db = dmn0(at, C * 128) + mnoff(kStep / 16 * h);
 #pragma unroll
                         for (int ks = 0; ks < kStep / 16; ++ks)
                             ptx::umma_bf16(tmem + kColD, da + mnoff(ks), db + mnoff(ks), id_d,
                                            h > 0 || part < 2 || ks > 0 || (STATE_ONLY && j > 0));
                     }
-                    ptx::umma_commit(&bars.kq_free[h]);
+                    if (STATE_ONLY) ptx::umma_commit(&bars.kq_free[h]);
                 }
                 if (!ok) break;
                 if (!STATE_ONLY || j == n - 1) ptx::umma_commit(&bars.ds_full);
-                ptx::umma_commit(&bars.emptyV[j % NB]);
+                ptx::umma_commit(&bars.emptyV[j % NV]);
+                if (!STATE_ONLY) ptx::umma_commit(&bars.emptyK[j & 1]);
             }
             ptx::umma_commit(&bars.done[1]);
             drain_bar(&bars.done[1], 0);
@@ -438,104 +452,37 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int piece = (warp - 6) % (P8 / NC8) * NC8, rg = (warp - 6) / (P8 / NC8) * NR;
         float S[STATE_ONLY ? 1 : NC], wk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         Pow f = {1.0f, 0.0f};    // the chunk's whole decay; STATE_ONLY: from the chunk's end to the range's
-        Pow fc = {1.0f, 0.0f}, fs;
-        int have = -1;
-        int have_len = 0;
+        Pow fc = {1.0f, 0.0f};
+        int have = -1, have_len = 0;
         bool ok = true;
-        Walk w(a, STATE_ONLY ? hi - 1 : lo), ws = w;   // the chunk whose K^ is formed; the one S enters
-        // Step by step K^; behind the first step of chunk j, while its products wait for it, the
-        // update of S by chunk j - 1 and the copy that chunk j reads.
+        Walk w(a, STATE_ONLY ? hi - 1 : lo);
 #pragma unroll 1
-        for (int step = 0; step <= n * kSteps; ++step) {
-            const int j = step / kSteps, h = step % kSteps;
-            if (h == 0) {
-                fs = f;
-                const int len = w.len();
-                if (rare(j < n && (w.seq != have || len != have_len))) {
-                    const float dec = p.decay[w.seq % p.H];
-                    if (!decay_ok(dec)) report_status(st, OSDN_ERR_DEVICE);
-                    const float l2 = decay_log2(dec);
+        for (int j = 0; j < n && ok; ++j) {
+            const int len = w.len();
+            if (rare(w.seq != have || len != have_len)) {
+                const float dec = p.decay[w.seq % p.H];
+                if (!decay_ok(dec)) report_status(st, OSDN_ERR_DEVICE);
+                const float l2 = decay_log2(dec);
 #pragma unroll
-                    for (int qt = 0; qt < 4; ++qt) {
-                        // the token's distance to the chunk's end, in the pass's direction
-                        const int kr = 32 * qt + lane, e = p.rev ? kr + 1 : len - 1 - kr;
-                        wk[qt] = weight(l2, max(e, 0));
-                    }
-                    fc = decay_pow(dec, len);
-                    if (!STATE_ONLY) f = fc;
-                    have = w.seq;
-                    have_len = len;
+                for (int qt = 0; qt < 4; ++qt) {
+                    // the token's distance to the chunk's end, in the pass's direction
+                    const int kr = 32 * qt + lane, e = p.rev ? kr + 1 : len - 1 - kr;
+                    wk[qt] = weight(l2, max(e, 0));
                 }
+                fc = decay_pow(dec, len);
+                if (!STATE_ONLY) f = fc;
+                have = w.seq;
+                have_len = len;
             }
-            if (j < n) {
-                if (!(ok = wait(bars.fullK[j % NB], j / NB))) break;
-                // K^ of the last chunk has been read
-                if (j && !(ok = wait(bars.kq_free[h], j - 1))) break;
-                const float2 minus = make_float2(-1.0f, -1.0f);
-#pragma unroll
-                for (int i = 0; i < NR * NC8; ++i) {
-                    const int r32 = h * (kStep / 32) + rg + i / NC8, c = piece + i % NC8;
-                    float wt = r32 < 2 ? (r32 ? wk[1] : wk[0]) : (r32 == 2 ? wk[2] : wk[3]);
-                    if (STATE_ONLY) wt *= f.hi;
-                    const float2 ww = make_float2(wt, wt);
-                    const int at = (c >> 3) * C * 128 + (32 * r32 + lane) * 128 + ((c & 7) ^ (lane & 7)) * 16;
-                    const uint4 u = *reinterpret_cast<const uint4 *>(sK(j) + at);
-                    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-                    uint32_t ph[4], pm[4], pl[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 x = __fmul2_rn(make_float2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), ww);
-                        const float2 m = __ffma2_rn(make_float2(top(x.x), top(x.y)), minus, x);
-                        const float2 l = __ffma2_rn(make_float2(top(m.x), top(m.y)), minus, m);
-                        ph[e] = top2(x.x, x.y);
-                        pm[e] = top2(m.x, m.y);
-                        pl[e] = top2(l.x, l.y);
-                    }
-                    uint8_t *dst = smem + LY::oP + at;
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-                    *reinterpret_cast<uint4 *>(dst + LY::kK) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
-                    *reinterpret_cast<uint4 *>(dst + 2 * LY::kK) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-                }
-                ptx::fence_proxy_async_smem();
-                arrive(bars.kq_full[h]);
-                if (h == kSteps - 1) {
-                    arrive(bars.emptyK[j % NB]);
-                    STATE_ONLY ? w.prev() : w.next();
-                    if (STATE_ONLY) f = pow_mul(f, fc);
-                }
-            }
-            if (STATE_ONLY || h) continue;
-            if (j) {
-                if (!(ok = wait(bars.ds_full, j - 1))) break;
-                ptx::tc_fence_after();
-#pragma unroll
-                for (int e = 0; e < NC; e += 32) {
-                    float x[32];
-                    tc::tmem_ld32(tmem + lane_off + kColD + c0 + e, x);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) S[e + i] = fmaf(fs.hi, S[e + i], fmaf(fs.lo, S[e + i], x[i]));
-                }
-                ptx::tc_fence_before();
-                arrive(bars.ds_free);
-                if (rare(ws.u == a.s.nch - 1 && p.ST && act)) {
-                    float *dst = p.ST + (size_t)ws.seq * sb;
-#pragma unroll
-                    for (int e = 0; e < NC; e += 4) {
-                        const float x[4] = {S[e], S[e + 1], S[e + 2], S[e + 3]};
-                        store4(dst + (size_t)row * K + c0 + e, x);
-                    }
-                }
-                ws.next();
-            }
-            if (j < n) {
-                if (rare(j == 0 || ws.u == 0)) {   // the state entering the range, or a sequence
+            if (!STATE_ONLY) {
+                if (rare(j == 0 || w.u == 0)) {   // the state entering the range, or a sequence
                     const float *src = nullptr;
                     bool tr = false;
-                    if (ws.u > 0) {
+                    if (w.u > 0) {
                         dependency_wait();
                         src = a.states + (size_t)g * sb;
                     } else if (p.S0.p) {
-                        src = p.S0.p + (size_t)ws.seq * sb;
+                        src = p.S0.p + (size_t)w.seq * sb;
                         tr = p.S0.transposed;
                     }
 #pragma unroll
@@ -555,6 +502,73 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (act) tc::st_row_sw128(smem + LY::oS, V, row, c0, S, NC);
                 ptx::fence_proxy_async_smem();
                 arrive(bars.s_ready);
+            }
+            // K has arrived, and been read by Q K^T where its first part takes its place
+            if (!(ok = STATE_ONLY ? wait(bars.fullK[j & 1], j >> 1) : wait(bars.qk_full, j))) break;
+#pragma unroll 1
+            for (int h = 0; h < kSteps; ++h) {
+                // K^ of the last chunk has been read (before its state was, where that is read)
+                if (STATE_ONLY && j && !(ok = wait(bars.kq_free[h], j - 1))) break;
+                const float2 minus = make_float2(-1.0f, -1.0f);
+#pragma unroll 2
+                for (int i = 0; i < NR * NC8; ++i) {
+                    const int r32 = h * (kStep / 32) + rg + i / NC8, c = piece + i % NC8;
+                    float wt = r32 < 2 ? (r32 ? wk[1] : wk[0]) : (r32 == 2 ? wk[2] : wk[3]);
+                    if (STATE_ONLY) wt *= f.hi;
+                    const float2 ww = make_float2(wt, wt);
+                    const int at = (c >> 3) * C * 128 + (32 * r32 + lane) * 128 + ((c & 7) ^ (lane & 7)) * 16;
+                    const uint4 u = *reinterpret_cast<const uint4 *>(sK(j) + at);
+                    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+                    uint32_t ph[4], pm[4], pl[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 x = __fmul2_rn(make_float2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), ww);
+                        const float2 m = __ffma2_rn(make_float2(top(x.x), top(x.y)), minus, x);
+                        const float2 l = __ffma2_rn(make_float2(top(m.x), top(m.y)), minus, m);
+                        ph[e] = top2(x.x, x.y);
+                        pm[e] = top2(m.x, m.y);
+                        pl[e] = top2(l.x, l.y);
+                    }
+                    uint8_t *dst = smem + LY::oP + at + (STATE_ONLY ? LY::kK : 0);
+                    *reinterpret_cast<uint4 *>(STATE_ONLY ? smem + LY::oP + at : sK(j) + at) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
+                    *reinterpret_cast<uint4 *>(dst + LY::kK) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                }
+                ptx::fence_proxy_async_smem();
+                arrive(bars.kq_full[h]);
+            }
+            if (!ok) break;
+            if (STATE_ONLY) {
+                arrive(bars.emptyK[j & 1]);
+                f = pow_mul(f, fc);
+                w.prev();
+            } else {
+                if (!(ok = wait(bars.ds_full, j))) break;
+                ptx::tc_fence_after();
+                const float2 fh = make_float2(f.hi, f.hi), fl = make_float2(f.lo, f.lo);
+#pragma unroll
+                for (int e = 0; e < NC; e += 32) {
+                    float x[32];
+                    tc::tmem_ld32(tmem + lane_off + kColD + c0 + e, x);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float2 s = make_float2(S[e + i], S[e + i + 1]);
+                        const float2 u = __ffma2_rn(fh, s, __ffma2_rn(fl, s, make_float2(x[i], x[i + 1])));
+                        S[e + i] = u.x;
+                        S[e + i + 1] = u.y;
+                    }
+                }
+                ptx::tc_fence_before();
+                arrive(bars.ds_free);
+                if (rare(w.u == a.s.nch - 1 && p.ST && act)) {
+                    float *dst = p.ST + (size_t)w.seq * sb;
+#pragma unroll
+                    for (int e = 0; e < NC; e += 4) {
+                        const float x[4] = {S[e], S[e + 1], S[e + 2], S[e + 3]};
+                        store4(dst + (size_t)row * K + c0 + e, x);
+                    }
+                }
+                w.next();
             }
         }
         if (STATE_ONLY && ok && warp < 14 && wait(bars.ds_full, 0)) {   // eight warps read the sum
