@@ -98,6 +98,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
             bool tr = false;
             if (!STATE_ONLY && u0 > 0) {
                 src = a.states + (size_t)g * sb;
+                tr = p.given;
             } else if (!STATE_ONLY && p.S0.p) {
                 src = p.S0.p + (size_t)seq * sb;
                 tr = p.S0.transposed;
@@ -266,12 +267,12 @@ cudaError_t launch_simt(const Args &a, cudaStream_t stream) {
     const dim3 grid = seq_grid(a.p.V / kRows, a.s.G);
     const bool split = a.states != nullptr;
     cudaError_t e = cudaSuccess;
-    if (split) {
+    if (split && !a.p.given) {
         e = launch_overlapped(false, attend_simt_kernel<K, true>, grid, kThreads, 0, stream, a);
         if (e == cudaSuccess) e = chain_states(a.p, a.s, a.states, stream);
     }
     if (e != cudaSuccess) return e;
-    return launch_overlapped(split, attend_simt_kernel<K, false>, grid, kThreads, 0, stream, a);
+    return launch_overlapped(split && !a.p.given, attend_simt_kernel<K, false>, grid, kThreads, 0, stream, a);
 }
 
 }  // namespace
@@ -283,7 +284,8 @@ cudaError_t chain_states(const Pass &p, const Split &s, float *states, cudaStrea
 
 Split simt_split(int BH, int T, int K, int V) {
     const int nch = (int)(((long long)T + kUnit - 1) / kUnit);
-    const long long slots = 152LL * 3 / (V / kRows);   // CTAs resident at once, in ranges
+    // CTAs resident at once, in ranges (the same for K and V exchanged)
+    const long long slots = 152LL * 3 / (std::max(K, V) / kRows);
     const long long N = (long long)BH * nch, G = std::min(N, slots);
     // units in a row, one by one: a split pass costs about two thirds more, and two launches
     // (about 16 units' time)

@@ -33,6 +33,9 @@ struct Pass {
     State S0;
     float *ST;   // NULL: not written
     void *o;
+    // The states entering the ranges are in the scratch already, transposed: the pass before ran on
+    // the same ranges with k and v exchanged (the same sums of v k^T, so dk can follow dv).
+    int given = 0;
 };
 
 // The time axis in `nch` units of `unit` tokens a sequence; the BH nch units,

@@ -235,6 +235,13 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
                 for (int b = 0; b < width / 64; ++b)
                     ptx::tma_load_3d(dst + b * C * 128, tm, full, b * 64, w.row(), w.seq);
+                // a single place: the next tile is brought as far as L2 meanwhile
+                if (!STATE_ONLY && !is_k && j + 1 < n) {
+                    Walk x = w;
+                    x.next();
+                    ptx::bulk_prefetch_l2(static_cast<const __nv_bfloat16 *>(is_v ? p.v : p.q) +
+                                              ((size_t)x.seq * p.T + x.row()) * width, x.len() * width * 2);
+                }
                 if (is_k) last[0] = j;
                 else if (is_v) last[2] = j;
                 else last[1] = j;
@@ -481,6 +488,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     if (w.u > 0) {
                         dependency_wait();
                         src = a.states + (size_t)g * sb;
+                        tr = p.given;
                     } else if (p.S0.p) {
                         src = p.S0.p + (size_t)w.seq * sb;
                         tr = p.S0.transposed;
@@ -601,14 +609,14 @@ cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorM
     cudaError_t e = smem_attr_once((const void *)attend_tc_kernel<K, V, STATE_ONLY>, smem, attr_done);
     if (e != cudaSuccess) return e;
     // no range follows the last one, so nothing needs its state
-    return launch_overlapped(!STATE_ONLY && a.states, attend_tc_kernel<K, V, STATE_ONLY>,
+    return launch_overlapped(!STATE_ONLY && a.states && !a.p.given, attend_tc_kernel<K, V, STATE_ONLY>,
                              dim3(a.s.G - (STATE_ONLY ? 1 : 0)), threads(STATE_ONLY), smem, stream, mq, mk, mv, a);
 }
 
 template <int K, int V>
 cudaError_t run(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Args &a,
                 cudaStream_t stream) {
-    if (a.states) {
+    if (a.states && !a.p.given) {
         cudaError_t e = launch<K, V, true>(mq, mk, mv, a, stream);
         if (e == cudaSuccess) e = chain_states(a.p, a.s, a.states, stream);
         if (e != cudaSuccess) return e;

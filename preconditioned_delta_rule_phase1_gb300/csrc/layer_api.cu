@@ -191,11 +191,13 @@ int osdn_decay_attn_backward(int io, int B, int H, int T, int K, int V, const vo
     cudaError_t r = attend(io, make_pass((int)BH, H, T, V, K, d_o, v, k, decay, state(S0, 1), dq, nullptr, 0),
                            scratch, status, st);
     if (r == cudaSuccess)
-        r = attend(io, make_pass((int)BH, H, T, V, K, v, d_o, q, decay, state(d_ST, 1), dk, nullptr, 1),
-                   scratch, status, st);
-    if (r == cudaSuccess)
         r = attend(io, make_pass((int)BH, H, T, K, V, k, q, d_o, decay, state(d_ST), dv, dS0, 1),
                    scratch, status, st);
+    if (r == cudaSuccess) {
+        auto p = make_pass((int)BH, H, T, V, K, v, d_o, q, decay, state(d_ST, 1), dk, nullptr, 1);
+        p.given = 1;   // dv's states, transposed
+        r = attend(io, p, scratch, status, st);
+    }
     return done(r);
 }
 

@@ -98,6 +98,10 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int c0, 
         "r"(c0), "r"(c1), "r"(c2)
         : "memory");
 }
+// Bring `bytes` bytes (a multiple of 16, from a 16-byte boundary) into L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void prefetch_tmap(const CUtensorMap *map) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
