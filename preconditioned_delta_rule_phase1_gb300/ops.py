@@ -14,6 +14,7 @@ of the wrong type would otherwise be read or written out of its bounds.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -509,20 +510,61 @@ def forward_kda(q, k, v, beta, r=None, eta=0.1, d0=None, alpha_k=None, S0=None, 
     return ktilde, dT, o, ST
 
 
+# The decayed layer's calls.  Its steps and norms take a few microseconds on the device, so the
+# checks above are made in one pass per tensor, and addresses go to ctypes as plain integers.
+
+_IO = {torch.float32: OSDN_F32, torch.bfloat16: OSDN_BF16}
+
+
+def _arg(name, t, shape, dtype, device):
+    """The address of `t` (None for an absent argument) after the checks of ``_expect``."""
+    if t is None:
+        return None
+    try:
+        if (t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous()):
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _expect(name, t, shape, dtype, device)
+    raise ValueError("%s does not fit the call" % name)
+
+
+def _run(name, device, stream, args, workspace=None, nbytes=0):
+    """Call `name` with `args`, then the workspace (if given) and the stream, on `device`."""
+    if device.type != "cuda":
+        raise ValueError("OSDN operates on CUDA tensors only")
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _run(name, device, stream, args, workspace, nbytes)
+    if workspace is not None:
+        if workspace.buf.numel() < nbytes:
+            workspace.ensure(nbytes)
+        args += (workspace.buf.data_ptr(), workspace.buf.numel())
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    code = getattr(_lib or lib(), name)(*args, s.cuda_stream)
+    if code:
+        raise OsdnError(code, name)
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes(name, *shape) -> int:
+    return int(getattr(lib(), name)(*shape))
+
+
 def decay_attn_workspace_bytes(io, B, H, T, K, V) -> int:
-    return int(lib().osdn_decay_attn_workspace_bytes(io, B, H, T, K, V))
+    return _bytes("osdn_decay_attn_workspace_bytes", io, B, H, T, K, V)
 
 
 def decay_attn_backward_workspace_bytes(io, B, H, T, K, V) -> int:
-    return int(lib().osdn_decay_attn_backward_workspace_bytes(io, B, H, T, K, V))
+    return _bytes("osdn_decay_attn_backward_workspace_bytes", io, B, H, T, K, V)
 
 
 def group_norm_backward_workspace_bytes(B, G, T, D) -> int:
-    return int(lib().osdn_group_norm_backward_workspace_bytes(B, G, T, D))
+    return _bytes("osdn_group_norm_backward_workspace_bytes", B, G, T, D)
 
 
 def clip_grad_norm_workspace_bytes(n) -> int:
-    return int(lib().osdn_clip_grad_norm_workspace_bytes(n))
+    return _bytes("osdn_clip_grad_norm_workspace_bytes", n)
 
 
 def decay_attn(q, k, v, decay, S0=None, o=None, ST=None, workspace=None, stream=None):
@@ -531,25 +573,18 @@ def decay_attn(q, k, v, decay, S0=None, o=None, ST=None, workspace=None, stream=
     returns (o, ST)."""
     B, H, T, K = k.shape
     V = v.shape[-1]
-    io, dev = _io(k), k.device
-    _expect("q", q, (B, H, T, K), k.dtype, dev)
-    _expect("k", k, (B, H, T, K), k.dtype, dev)
-    _expect("v", v, (B, H, T, V), k.dtype, dev)
-    _expect("decay", decay, (H,), F32, dev)
-    _expect("S0", S0, (B, H, V, K), F32, dev)
+    dt, dev = k.dtype, k.device
+    io = _io(k)
+    qk, vo, st = (B, H, T, K), (B, H, T, V), (B, H, V, K)
     if o is None:
-        o = torch.empty(B, H, T, V, dtype=k.dtype, device=dev)
+        o = torch.empty(vo, dtype=dt, device=dev)
     if ST is None:
-        ST = torch.empty(B, H, V, K, dtype=F32, device=dev)
-    _expect("o", o, (B, H, T, V), k.dtype, dev)
-    _expect("ST", ST, (B, H, V, K), F32, dev)
-    ws = _workspace(workspace, dev)
-    with _on(dev):
-        ws.ensure(decay_attn_workspace_bytes(io, B, H, T, K, V))
-        code = lib().osdn_decay_attn(io, B, H, T, K, V, _ptr(q), _ptr(k), _ptr(v), _ptr(decay),
-                                     _ptr(S0), _ptr(o), _ptr(ST), ws.ptr, ws.nbytes,
-                                     _stream(stream, dev))
-    _check(code, "osdn_decay_attn")
+        ST = torch.empty(st, dtype=F32, device=dev)
+    args = (io, B, H, T, K, V, _arg("q", q, qk, dt, dev), _arg("k", k, qk, dt, dev),
+            _arg("v", v, vo, dt, dev), _arg("decay", decay, (H,), F32, dev),
+            _arg("S0", S0, st, F32, dev), _arg("o", o, vo, dt, dev), _arg("ST", ST, st, F32, dev))
+    _run("osdn_decay_attn", dev, stream, args, _workspace(workspace, dev),
+         decay_attn_workspace_bytes(io, B, H, T, K, V))
     return o, ST
 
 
@@ -558,21 +593,14 @@ def decay_attn_step(q, k, v, decay, S, o=None, workspace=None, stream=None):
     (fp32) in place for the token q, k [B,H,K], v [B,H,V] (io); returns o."""
     B, H, K = k.shape
     V = v.shape[-1]
-    io, dev = _io(k), k.device
-    _expect("q", q, (B, H, K), k.dtype, dev)
-    _expect("k", k, (B, H, K), k.dtype, dev)
-    _expect("v", v, (B, H, V), k.dtype, dev)
-    _expect("decay", decay, (H,), F32, dev)
-    _expect("S", S, (B, H, V, K), F32, dev)
+    dt, dev = k.dtype, k.device
+    io = _io(k)
     if o is None:
-        o = torch.empty(B, H, V, dtype=k.dtype, device=dev)
-    _expect("o", o, (B, H, V), k.dtype, dev)
-    ws = _workspace(workspace, dev)
-    with _on(dev):
-        code = lib().osdn_decay_attn_step(io, B, H, K, V, _ptr(q), _ptr(k), _ptr(v), _ptr(decay),
-                                          _ptr(S), _ptr(o), ws.ptr, ws.nbytes,
-                                          _stream(stream, dev))
-    _check(code, "osdn_decay_attn_step")
+        o = torch.empty((B, H, V), dtype=dt, device=dev)
+    args = (io, B, H, K, V, _arg("q", q, (B, H, K), dt, dev), _arg("k", k, (B, H, K), dt, dev),
+            _arg("v", v, (B, H, V), dt, dev), _arg("decay", decay, (H,), F32, dev),
+            _arg("S", S, (B, H, V, K), F32, dev), _arg("o", o, (B, H, V), dt, dev))
+    _run("osdn_decay_attn_step", dev, stream, args, _workspace(workspace, dev))
     return o
 
 
@@ -583,25 +611,19 @@ def decay_attn_backward(q, k, v, decay, S0=None, *, do, dST=None, workspace=None
     is a constant and has no gradient."""
     B, H, T, K = k.shape
     V = v.shape[-1]
-    io, dev = _io(k), k.device
-    _expect("q", q, (B, H, T, K), k.dtype, dev)
-    _expect("k", k, (B, H, T, K), k.dtype, dev)
-    _expect("v", v, (B, H, T, V), k.dtype, dev)
-    _expect("decay", decay, (H,), F32, dev)
-    _expect("S0", S0, (B, H, V, K), F32, dev)
-    _expect("do", do, (B, H, T, V), k.dtype, dev)
-    _expect("dST", dST, (B, H, V, K), F32, dev)
+    dt, dev = k.dtype, k.device
+    io = _io(k)
+    qk, vo, st = (B, H, T, K), (B, H, T, V), (B, H, V, K)
+    args = (io, B, H, T, K, V, _arg("q", q, qk, dt, dev), _arg("k", k, qk, dt, dev),
+            _arg("v", v, vo, dt, dev), _arg("decay", decay, (H,), F32, dev),
+            _arg("S0", S0, st, F32, dev), _arg("do", do, vo, dt, dev), _arg("dST", dST, st, F32, dev))
     g = {"q": torch.empty_like(k), "k": torch.empty_like(k), "v": torch.empty_like(v)}
     if S0 is not None:
         g["S0"] = torch.empty_like(S0)
-    ws = _workspace(workspace, dev)
-    with _on(dev):
-        ws.ensure(decay_attn_backward_workspace_bytes(io, B, H, T, K, V))
-        code = lib().osdn_decay_attn_backward(
-            io, B, H, T, K, V, _ptr(q), _ptr(k), _ptr(v), _ptr(decay), _ptr(S0), _ptr(do),
-            _ptr(dST), _ptr(g["q"]), _ptr(g["k"]), _ptr(g["v"]), _ptr(g.get("S0")), ws.ptr,
-            ws.nbytes, _stream(stream, dev))
-    _check(code, "osdn_decay_attn_backward")
+    args += (g["q"].data_ptr(), g["k"].data_ptr(), g["v"].data_ptr(),
+             None if S0 is None else g["S0"].data_ptr())
+    _run("osdn_decay_attn_backward", dev, stream, args, _workspace(workspace, dev),
+         decay_attn_backward_workspace_bytes(io, B, H, T, K, V))
     return g
 
 
@@ -621,16 +643,10 @@ def _norm_shape(x, groups):
     return B, groups, T, C // groups, 0
 
 
-def _norm_inputs(x, weight, bias, gate, groups, act):
+def _act(act):
     if act not in ACTS:
         raise ValueError("act must be one of %s, got %r" % (sorted(ACTS), act))
-    B, G, T, D, first = _norm_shape(x, groups)
-    io, dev = _io(x), x.device
-    _expect("x", x, x.shape, x.dtype, dev)
-    _expect("weight", weight, (G * D,), F32, dev)
-    _expect("bias", bias, (G * D,), F32, dev)
-    _expect("gate", gate, (B, T, G * D), x.dtype, dev)
-    return io, B, G, T, D, first, dev
+    return ACTS[act]
 
 
 def group_norm(x, weight=None, bias=None, gate=None, groups=None, act="none", eps=1e-5, y=None,
@@ -641,15 +657,15 @@ def group_norm(x, weight=None, bias=None, gate=None, groups=None, act="none", ep
     [B,T,C] with `groups`; weight, bias [C] fp32; gate [B,T,C] (io).  Returns
     y [B,T,C] = act(norm(x)), or norm(x) act(gate) with a gate; act is "none",
     "silu" or "sigmoid"."""
-    io, B, G, T, D, first, dev = _norm_inputs(x, weight, bias, gate, groups, act)
+    a = _act(act)
+    B, G, T, D, first = _norm_shape(x, groups)
+    io, dt, dev, C = _io(x), x.dtype, x.device, G * D
     if y is None:
-        y = torch.empty(B, T, G * D, dtype=x.dtype, device=dev)
-    _expect("y", y, (B, T, G * D), x.dtype, dev)
-    with _on(dev):
-        code = lib().osdn_group_norm(io, B, G, T, D, first, _ptr(x), _ptr(weight), _ptr(bias),
-                                     _ptr(gate), ACTS[act], float(eps), _ptr(y),
-                                     _stream(stream, dev))
-    _check(code, "osdn_group_norm")
+        y = torch.empty((B, T, C), dtype=dt, device=dev)
+    args = (io, B, G, T, D, first, _arg("x", x, x.shape, dt, dev), _arg("weight", weight, (C,), F32, dev),
+            _arg("bias", bias, (C,), F32, dev), _arg("gate", gate, (B, T, C), dt, dev), a, float(eps),
+            _arg("y", y, (B, T, C), dt, dev))
+    _run("osdn_group_norm", dev, stream, args)
     return y
 
 
@@ -657,20 +673,20 @@ def group_norm_backward(x, dy, weight=None, bias=None, gate=None, groups=None, a
                         eps=1e-5, workspace=None, stream=None):
     """Gradients of ``group_norm`` (osdn_group_norm_backward) given dy [B,T,C]:
     a dict with x (in x's layout) and weight, bias, gate for those given."""
-    io, B, G, T, D, first, dev = _norm_inputs(x, weight, bias, gate, groups, act)
-    _expect("dy", dy, (B, T, G * D), x.dtype, dev)
+    a = _act(act)
+    B, G, T, D, first = _norm_shape(x, groups)
+    io, dt, dev, C = _io(x), x.dtype, x.device, G * D
+    args = (io, B, G, T, D, first, _arg("x", x, x.shape, dt, dev), _arg("dy", dy, (B, T, C), dt, dev),
+            _arg("weight", weight, (C,), F32, dev), _arg("bias", bias, (C,), F32, dev),
+            _arg("gate", gate, (B, T, C), dt, dev), a, float(eps))
     g = {"x": torch.empty_like(x)}
     for name, t in (("weight", weight), ("bias", bias), ("gate", gate)):
         if t is not None:
             g[name] = torch.empty_like(t)
-    ws = _workspace(workspace, dev)
-    with _on(dev):
-        ws.ensure(group_norm_backward_workspace_bytes(B, G, T, D))
-        code = lib().osdn_group_norm_backward(
-            io, B, G, T, D, first, _ptr(x), _ptr(dy), _ptr(weight), _ptr(bias), _ptr(gate),
-            ACTS[act], float(eps), _ptr(g["x"]), _ptr(g.get("gate")), _ptr(g.get("weight")),
-            _ptr(g.get("bias")), ws.ptr, ws.nbytes, _stream(stream, dev))
-    _check(code, "osdn_group_norm_backward")
+    at = lambda name: g[name].data_ptr() if name in g else None  # noqa: E731
+    args += (at("x"), at("gate"), at("weight"), at("bias"))
+    _run("osdn_group_norm_backward", dev, stream, args, _workspace(workspace, dev),
+         group_norm_backward_workspace_bytes(B, G, T, D))
     return g
 
 
@@ -683,32 +699,36 @@ def clip_grad_norm(grads, max_norm, outs=None, norm=None, workspace=None, stream
     if n == 0 and norm is None:
         raise ValueError("no gradients and no norm tensor: the device is unknown")
     dev = grads[0].device if n else norm.device
-    ios, sizes = (ctypes.c_int * n)(), (ctypes.c_longlong * n)()
-    gp, op = (ctypes.c_void_p * n)(), None
-    for i, g in enumerate(grads):
-        if g.device != dev or not g.is_contiguous():
+    at = dev.index if dev.type == "cuda" else -1
+    if not all(g.get_device() == at and g.is_contiguous() for g in grads):
+        for i, g in enumerate(grads):
             _expect("grads[%d]" % i, g, g.shape, g.dtype, dev)
-        ios[i], sizes[i], gp[i] = _io(g), g.numel(), g.data_ptr()
+    try:
+        ios = [_IO[g.dtype] for g in grads]
+    except KeyError as e:
+        raise TypeError("gradients must be float32 or bfloat16, got %s" % e) from None
+    sizes = [g.numel() for g in grads]
+    gp = written = [g.data_ptr() for g in grads]
+    op = None
     if outs is not None:
         outs = list(outs)
         if len(outs) != n:
             raise ValueError("%d gradients, %d outputs" % (n, len(outs)))
-        op = (ctypes.c_void_p * n)()
-        for i, (g, o) in enumerate(zip(grads, outs)):
-            _expect("outs[%d]" % i, o, g.shape, g.dtype, dev)
-            op[i] = o.data_ptr()
-    written = [p for p, s in zip(gp if op is None else op, sizes) if s]
+        if not all(o.shape == g.shape and o.dtype == g.dtype and o.get_device() == at and o.is_contiguous()
+                   for g, o in zip(grads, outs)):
+            for i, (g, o) in enumerate(zip(grads, outs)):
+                _expect("outs[%d]" % i, o, g.shape, g.dtype, dev)
+        written = [o.data_ptr() for o in outs]
+        op = (ctypes.c_void_p * n)(*written)
+    written = [p for p, s in zip(written, sizes) if s]
     if len(set(written)) != len(written):
         raise ValueError("a tensor is written twice")
     if norm is None:
         norm = torch.empty(1, dtype=F32, device=dev)
-    _expect("norm", norm, (1,), F32, dev)
-    ws = _workspace(workspace, dev)
-    with _on(dev):
-        ws.ensure(clip_grad_norm_workspace_bytes(n))
-        code = lib().osdn_clip_grad_norm(n, gp, op, sizes, ios, float(max_norm), _ptr(norm),
-                                         ws.ptr, ws.nbytes, _stream(stream, dev))
-    _check(code, "osdn_clip_grad_norm")
+    args = (n, (ctypes.c_void_p * n)(*gp), op, (ctypes.c_longlong * n)(*sizes), (ctypes.c_int * n)(*ios),
+            float(max_norm), _arg("norm", norm, (1,), F32, dev))
+    _run("osdn_clip_grad_norm", dev, stream, args, _workspace(workspace, dev),
+         clip_grad_norm_workspace_bytes(n))
     return norm
 
 
