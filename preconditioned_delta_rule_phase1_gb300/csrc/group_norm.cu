@@ -16,12 +16,13 @@
 //
 // Every tensor is read and written once, so both directions are HBM-bound.
 // L lanes (the power of two at or above D/8, at most 32) hold a group, eight
-// channels a lane in 16-byte pieces, so a warp covers 32/L groups and its
-// loads are whole 128-byte lines for D >= 64 in bf16.  In the backward pass
-// a CTA keeps to one group g and walks tokens, so that a lane's channels
-// stay the same and dweight and dbias add up in its registers; they are
-// joined over the CTA in shared memory and over CTAs by a second kernel, in
-// a fixed order (no atomics).
+// channels a lane in 16-byte pieces; where a group is short, neighbouring
+// groups of the token stand next to it so that 16 lanes read 256 bytes in a
+// row.  A CTA keeps to its groups and walks tokens: a lane's weight and bias
+// (and in the backward pass the sums of dweight and dbias) stay in registers,
+// and the next token's pieces are on their way while one is computed.  The
+// sums are joined over the CTA in shared memory and over CTAs by a second
+// kernel, in a fixed order (no atomics).
 #include "osdn_device.cuh"
 
 namespace osdn {
@@ -41,20 +42,41 @@ struct Params {
     int splits;
 };
 
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// Eight channels as they lie in memory.
+template <typename io_t>
+struct Raw {
+    uint4 u[sizeof(io_t) / 2];
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        for (int i = 0; i < (int)sizeof(io_t) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
     }
+    __device__ __forceinline__ void load(const io_t *p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(io_t) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void wide(float (&x)[8]) const {
+        if constexpr (sizeof(io_t) == 4) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[4 * i] = __uint_as_float(u[i].x);
+                x[4 * i + 1] = __uint_as_float(u[i].y);
+                x[4 * i + 2] = __uint_as_float(u[i].z);
+                x[4 * i + 3] = __uint_as_float(u[i].w);
+            }
+        } else {
+            const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+    Raw<float> r;
+    r.load(p);
+    r.wide(x);
 }
 __device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
@@ -77,7 +99,7 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float sigmoid(float u) { return __frcp_rn(1.0f + __expf(-u)); }
+__device__ __forceinline__ float sigmoid(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
 __device__ __forceinline__ float act_of(float u, int act) {
     return act == kNone ? u : act == kSilu ? u * sigmoid(u) : sigmoid(u);
 }
@@ -93,48 +115,55 @@ __device__ __forceinline__ void act_both(float u, int act, float &f, float &d) {
     d = act == kSilu ? s * (1.0f + u * (1.0f - s)) : s * (1.0f - s);
 }
 
-// Where token `tok` (b T + t) of group g starts in x; in y and gate it is
-// (tok G + g) D.
-__device__ __forceinline__ size_t x_at(const Params &p, long long tok, int g) {
-    if (!p.heads_first) return ((size_t)tok * p.G + g) * p.D;
-    const long long b = tok / p.T, t = tok - b * p.T;
-    return (((size_t)b * p.G + g) * p.T + t) * p.D;
-}
-
-// A lane's N pieces of eight channels: piece n starts at channel (n L + l) 8.
-template <typename io_t, int L, int N>
-__global__ void __launch_bounds__(kThreads) group_norm_kernel(Params p) {
-    constexpr int GPC = kThreads / L;   // groups a CTA
-    const int l = threadIdx.x % L;
-    const long long at = (long long)blockIdx.x * GPC + threadIdx.x / L, n_all = p.tokens * p.G;
-    const bool live = at < n_all;
-    // consecutive groups lie next to each other in x: by token, or by head
-    long long tok;
-    int g;
-    if (p.heads_first) {
-        const long long bg = at / p.T;
-        g = (int)(bg % p.G);
-        tok = bg / p.G * p.T + at % p.T;
-    } else {
-        tok = at / p.G;
-        g = (int)(at % p.G);
+// The walk of a thread over its CTA's tokens: slots of GPB groups of L lanes,
+// 16 lanes or more a slot; a slot's token, its places in x and in y (and gate).
+template <int L>
+struct Walk {
+    static constexpr int GPB = L < 16 ? 16 / L : 1;   // groups side by side
+    static constexpr int S = kThreads / (L * GPB);    // tokens at a time
+    int l, g;
+    bool in_range;      // the group exists
+    long long tok, hi, b;
+    int t;
+    __device__ __forceinline__ Walk(const Params &p) {
+        l = threadIdx.x % L;
+        g = blockIdx.x * GPB + threadIdx.x / L % GPB;
+        in_range = g < p.G;
+        tok = p.tokens * blockIdx.y / p.splits + threadIdx.x / (L * GPB);
+        hi = p.tokens * (blockIdx.y + 1) / p.splits;
+        b = p.heads_first ? tok / p.T : 0;
+        t = p.heads_first ? (int)(tok - b * p.T) : 0;
     }
-    const io_t *x = static_cast<const io_t *>(p.x) + (size_t)at * p.D;
-    const size_t ya = ((size_t)tok * p.G + g) * p.D;
+    __device__ __forceinline__ bool live() const { return in_range && tok < hi; }
+    __device__ __forceinline__ size_t at_y(const Params &p) const { return ((size_t)tok * p.G + g) * p.D; }
+    __device__ __forceinline__ size_t at_x(const Params &p) const {
+        return p.heads_first ? (((size_t)b * p.G + g) * p.T + t) * p.D : at_y(p);
+    }
+    __device__ __forceinline__ void next(const Params &p) {
+        tok += S;
+        if (!p.heads_first) return;
+        t += S;
+        while (t >= p.T) {
+            t -= p.T;
+            ++b;
+        }
+    }
+    // CTAs' iterations: the same for all threads, so that shuffles see whole warps
+    __device__ __forceinline__ static int rounds(const Params &p) {
+        const long long n = p.tokens * (blockIdx.y + 1) / p.splits - p.tokens * blockIdx.y / p.splits;
+        return (int)((n + S - 1) / S);
+    }
+};
+
+// Mean and 1 / sqrt(var + eps) of a group; v leaves as x - mean.
+template <int L, int N>
+__device__ __forceinline__ float normalise(const Params &p, int l, float (&v)[N][8]) {
     const float inv = 1.0f / (float)p.D;
-    float v[N][8], gt[N][8];
     float sum = 0.0f;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const int c = (n * L + l) * 8;
-        const bool in = live && c < p.D;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[n][e] = gt[n][e] = 0.0f;
-        if (in) load8(x + c, v[n]);
-        if (in && p.gate) load8(static_cast<const io_t *>(p.gate) + ya + c, gt[n]);
+    for (int n = 0; n < N; ++n)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum += v[n][e];
-    }
     const float mean = group_sum<L>(sum) * inv;
     float sq = 0.0f, off = 0.0f;   // off: what rounding left of the mean
 #pragma unroll
@@ -148,85 +177,131 @@ __global__ void __launch_bounds__(kThreads) group_norm_kernel(Params p) {
         }
     }
     off = group_sum<L>(off) * inv;
-    const float r = 1.0f / sqrtf(fmaxf(fmaf(-off, off, group_sum<L>(sq) * inv), 0.0f) + p.eps);
-    if (!live) return;
+    const float var = fmaxf(fmaf(-off, off, group_sum<L>(sq) * inv), 0.0f);
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[n][e] -= off;
+    return rsqrtf(var + p.eps);
+}
+
+// A lane's N pieces of eight channels: piece n starts at channel (n L + l) 8.
+template <typename io_t, int L, int N>
+__global__ void __launch_bounds__(kThreads) group_norm_kernel(Params p) {
+    Walk<L> w(p);
+    const int l = w.l;
+    float wt[N][8], bs[N][8];
+    Raw<io_t> rx[N], rg[N];
+    auto fetch = [&] {
+        const bool live = w.live();
+        const io_t *x = static_cast<const io_t *>(p.x) + (live ? w.at_x(p) : 0);
+        const io_t *gate = static_cast<const io_t *>(p.gate) + (live ? w.at_y(p) : 0);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int c = (n * L + l) * 8;
+            rx[n].zero();
+            rg[n].zero();
+            if (live && c < p.D) {
+                rx[n].load(x + c);
+                if (p.gate) rg[n].load(gate + c);
+            }
+        }
+    };
+    fetch();
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const int c = (n * L + l) * 8;
-        if (c >= p.D) continue;
-        float w[8], b[8], y[8];
-        if (p.weight) load8(p.weight + (size_t)g * p.D + c, w);
-        if (p.bias) load8(p.bias + (size_t)g * p.D + c, b);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float z = (v[n][e] - off) * r;
-            if (p.weight) z *= w[e];
-            if (p.bias) z += b[e];
-            y[e] = p.gate ? z * act_of(gt[n][e], p.act) : act_of(z, p.act);
+            wt[n][e] = 1.0f;
+            bs[n][e] = 0.0f;
         }
-        store8(static_cast<io_t *>(p.y) + ya + c, y);
+        if (w.in_range && c < p.D && p.weight) load8(p.weight + (size_t)w.g * p.D + c, wt[n]);
+        if (w.in_range && c < p.D && p.bias) load8(p.bias + (size_t)w.g * p.D + c, bs[n]);
+    }
+    for (int i = Walk<L>::rounds(p); i > 0; --i) {
+        float v[N][8], gt[N][8];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            rx[n].wide(v[n]);
+            rg[n].wide(gt[n]);
+        }
+        const bool live = w.live();
+        io_t *y = static_cast<io_t *>(p.y) + (live ? w.at_y(p) : 0);
+        w.next(p);
+        if (i > 1) fetch();   // on its way while this token is computed
+        const float r = normalise<L, N>(p, l, v);
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int c = (n * L + l) * 8;
+            if (!live || c >= p.D) continue;
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float z = fmaf(v[n][e] * r, wt[n][e], bs[n][e]);
+                o[e] = p.gate ? z * act_of(gt[n][e], p.act) : act_of(z, p.act);
+            }
+            store8(y + c, o);
+        }
     }
 }
 
 template <typename io_t, int L, int N>
 __global__ void __launch_bounds__(kThreads) group_norm_backward_kernel(Params p) {
-    constexpr int S = kThreads / L;   // tokens a CTA holds at a time
-    extern __shared__ float red[];    // [S][2][N L 8]
-    const int l = threadIdx.x % L, slot = threadIdx.x / L, g = blockIdx.x;
+    extern __shared__ float red[];    // [S][GPB][2][N L 8]
+    constexpr int W = N * L * 8, S = Walk<L>::S, GPB = Walk<L>::GPB;
+    Walk<L> w(p);
+    const int l = w.l;
     const float inv = 1.0f / (float)p.D;
-    float w[N][8], b[N][8], aw[N][8], ab[N][8];
+    float wt[N][8], bs[N][8], aw[N][8], ab[N][8];
+    Raw<io_t> rx[N], rd[N], rg[N];
+    auto fetch = [&] {
+        const bool live = w.live();
+        const size_t xa = live ? w.at_x(p) : 0, ya = live ? w.at_y(p) : 0;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const int c = (n * L + l) * 8;
+            rx[n].zero();
+            rd[n].zero();
+            rg[n].zero();
+            if (live && c < p.D) {
+                rx[n].load(static_cast<const io_t *>(p.x) + xa + c);
+                rd[n].load(static_cast<const io_t *>(p.dy) + ya + c);
+                if (p.gate) rg[n].load(static_cast<const io_t *>(p.gate) + ya + c);
+            }
+        }
+    };
+    fetch();
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const int c = (n * L + l) * 8;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            w[n][e] = 1.0f;
-            b[n][e] = aw[n][e] = ab[n][e] = 0.0f;
+            wt[n][e] = 1.0f;
+            bs[n][e] = aw[n][e] = ab[n][e] = 0.0f;
         }
-        if (c < p.D && p.weight) load8(p.weight + (size_t)g * p.D + c, w[n]);
-        if (c < p.D && p.bias) load8(p.bias + (size_t)g * p.D + c, b[n]);
+        if (w.in_range && c < p.D && p.weight) load8(p.weight + (size_t)w.g * p.D + c, wt[n]);
+        if (w.in_range && c < p.D && p.bias) load8(p.bias + (size_t)w.g * p.D + c, bs[n]);
     }
-    const long long lo = p.tokens * blockIdx.y / p.splits, hi = p.tokens * (blockIdx.y + 1) / p.splits;
-    for (long long t0 = lo; t0 < hi; t0 += S) {   // uniform over the CTA: the shuffles see whole warps
-        const long long tok = t0 + slot;
-        const bool live = tok < hi;
-        const size_t xa = live ? x_at(p, tok, g) : 0, ya = ((size_t)tok * p.G + g) * p.D;
+    for (int i = Walk<L>::rounds(p); i > 0; --i) {
         float v[N][8], d[N][8], gt[N][8];
-        float sum = 0.0f;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            const int c = (n * L + l) * 8;
-            const bool in = live && c < p.D;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[n][e] = d[n][e] = gt[n][e] = 0.0f;
-            if (in) {
-                load8(static_cast<const io_t *>(p.x) + xa + c, v[n]);
-                load8(static_cast<const io_t *>(p.dy) + ya + c, d[n]);
-                if (p.gate) load8(static_cast<const io_t *>(p.gate) + ya + c, gt[n]);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum += v[n][e];
+            rx[n].wide(v[n]);
+            rd[n].wide(d[n]);
+            rg[n].wide(gt[n]);
         }
-        const float mean = group_sum<L>(sum) * inv;
-        float sq = 0.0f, off = 0.0f;   // off: what rounding left of the mean
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const bool in = (n * L + l) * 8 < p.D;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[n][e] = in ? v[n][e] - mean : 0.0f;
-                sq = fmaf(v[n][e], v[n][e], sq);
-                off += v[n][e];
-            }
-        }
-        off = group_sum<L>(off) * inv;
-        const float r = 1.0f / sqrtf(fmaxf(fmaf(-off, off, group_sum<L>(sq) * inv), 0.0f) + p.eps);
+        const bool live = w.live();
+        const size_t xa = live ? w.at_x(p) : 0, ya = live ? w.at_y(p) : 0;
+        w.next(p);
+        if (i > 1) fetch();   // on its way while this token is computed
+        const float r = normalise<L, N>(p, l, v);
         float hs = 0.0f, hx = 0.0f;
 #pragma unroll
         for (int n = 0; n < N; ++n)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float xh = (v[n][e] - off) * r, z = fmaf(xh, w[n][e], b[n][e]);
+                const float xh = v[n][e] * r, z = fmaf(xh, wt[n][e], bs[n][e]);
                 float f, df, dz;
                 if (p.gate) {
                     act_both(gt[n][e], p.act, f, df);
@@ -238,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) group_norm_backward_kernel(Params p)
                 }
                 aw[n][e] = fmaf(dz, xh, aw[n][e]);
                 ab[n][e] += dz;
-                const float h = dz * w[n][e];
+                const float h = dz * wt[n][e];
                 hs += h;
                 hx = fmaf(h, xh, hx);
                 v[n][e] = xh;
@@ -246,11 +321,10 @@ __global__ void __launch_bounds__(kThreads) group_norm_backward_kernel(Params p)
             }
         hs = group_sum<L>(hs) * inv;
         hx = group_sum<L>(hx) * inv;
-        if (!live) continue;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int c = (n * L + l) * 8;
-            if (c >= p.D) continue;
+            if (!live || c >= p.D) continue;
             float dx[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) dx[e] = r * (d[n][e] - hs - v[n][e] * hx);
@@ -259,19 +333,20 @@ __global__ void __launch_bounds__(kThreads) group_norm_backward_kernel(Params p)
         }
     }
     if (!p.part) return;
-    constexpr int W = N * L * 8;
+    float *mine = red + (size_t)(threadIdx.x / L) * 2 * W;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const int c = (n * L + l) * 8;
-        store8(red + (size_t)slot * 2 * W + c, aw[n]);
-        store8(red + (size_t)slot * 2 * W + W + c, ab[n]);
+        store8(mine + c, aw[n]);
+        store8(mine + W + c, ab[n]);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * p.D; i += kThreads) {
-        const int c = i < p.D ? i : W + i - p.D;
+    for (int i = threadIdx.x; i < GPB * 2 * p.D; i += kThreads) {
+        const int gi = i / (2 * p.D), at = i % (2 * p.D), c = at < p.D ? at : W + at - p.D;
+        const int g = blockIdx.x * GPB + gi;
         float s = 0.0f;
-        for (int k = 0; k < S; ++k) s += red[(size_t)k * 2 * W + c];
-        p.part[((size_t)blockIdx.y * p.G + g) * 2 * p.D + i] = s;
+        for (int k = 0; k < S; ++k) s += red[(size_t)(k * GPB + gi) * 2 * W + c];
+        if (g < p.G) p.part[((size_t)blockIdx.y * p.G + g) * 2 * p.D + at] = s;
     }
 }
 
@@ -307,14 +382,15 @@ __global__ void zero_kernel(long long n, float *a, float *b) {
 
 template <typename io_t, int L, int N>
 cudaError_t forward_t(const Params &p, cudaStream_t stream) {
-    const long long n = p.tokens * p.G, per = kThreads / L;
-    group_norm_kernel<io_t, L, N><<<(unsigned)((n + per - 1) / per), kThreads, 0, stream>>>(p);
+    constexpr int GPB = Walk<L>::GPB;
+    group_norm_kernel<io_t, L, N><<<dim3((p.G + GPB - 1) / GPB, p.splits), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 template <typename io_t, int L, int N>
 cudaError_t backward_t(const Params &p, cudaStream_t stream) {
+    constexpr int GPB = Walk<L>::GPB;
     const int smem = (kThreads / L) * 2 * N * L * 8 * 4;   // 16 KB a piece
-    group_norm_backward_kernel<io_t, L, N><<<dim3(p.G, p.splits), kThreads, smem, stream>>>(p);
+    group_norm_backward_kernel<io_t, L, N><<<dim3((p.G + GPB - 1) / GPB, p.splits), kThreads, smem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -335,18 +411,21 @@ cudaError_t run_d(const Params &p, cudaStream_t stream) {
     return run_t<io_t, BWD, 32, 2>(p, stream);
 }
 
-// CTAs a group in the backward pass: enough for about four a SM over all
-// groups, while each still has 64 tokens to add up.
-int backward_splits(long long tokens, int G) {
-    long long s = (152LL * 4 + G - 1) / G;
-    if (s > (tokens + 63) / 64) s = (tokens + 63) / 64;
+// CTAs that share a block of groups' tokens: enough for `per_sm` CTAs a SM
+// over all blocks, while each still has `least` tokens.
+int token_splits(long long tokens, int G, int D, int per_sm, int least) {
+    const int lanes = D <= 8 ? 1 : D <= 16 ? 2 : D <= 32 ? 4 : D <= 64 ? 8 : 16;
+    const long long blocks = (G + 16 / lanes - 1) / (16 / lanes);
+    long long s = (152LL * per_sm + blocks - 1) / blocks;
+    if (s > (tokens + least - 1) / least) s = (tokens + least - 1) / least;
     return (int)(s < 1 ? 1 : s > 65535 ? 65535 : s);
 }
+int backward_splits(long long tokens, int G, int D) { return token_splits(tokens, G, D, 4, 64); }
 
 }  // namespace gn
 
 size_t group_norm_backward_scratch_bytes(int B, int G, int T, int D) {
-    return (size_t)gn::backward_splits((long long)B * T, G) * G * 2 * D * 4;
+    return (size_t)gn::backward_splits((long long)B * T, G, D) * G * 2 * D * 4;
 }
 
 cudaError_t group_norm_launch(int io, int B, int G, int T, int D, int heads_first, const void *x,
@@ -363,6 +442,7 @@ cudaError_t group_norm_launch(int io, int B, int G, int T, int D, int heads_firs
     p.bias = bias;
     p.y = y;
     p.tokens = (long long)B * T;
+    p.splits = gn::token_splits(p.tokens, G, D, 8, 16);
     return io == OSDN_F32 ? gn::run_d<float, false>(p, stream)
                           : gn::run_d<__nv_bfloat16, false>(p, stream);
 }
@@ -391,7 +471,7 @@ cudaError_t group_norm_backward_launch(int io, int B, int G, int T, int D, int h
             gn::zero_kernel<<<(unsigned)((C + 255) / 256), 256, 0, stream>>>(C, dweight, dbias);
         return cudaGetLastError();
     }
-    p.splits = gn::backward_splits(p.tokens, G);
+    p.splits = gn::backward_splits(p.tokens, G, D);
     p.part = (dweight || dbias) ? static_cast<float *>(scratch) : nullptr;
     cudaError_t e = io == OSDN_F32 ? gn::run_d<float, true>(p, stream)
                                    : gn::run_d<__nv_bfloat16, true>(p, stream);
