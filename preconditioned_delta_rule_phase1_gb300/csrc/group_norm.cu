@@ -6,9 +6,9 @@
 //     z = weight x^ + bias,   y = act(z), or z act(gate) where a gate is given
 // with y and gate [B][T][G D], and x either [B][T][G D] or, as the attention
 // writes it, [B][G][T][D].  Statistics belong to one token alone (the norm
-// stays causal) and are taken in two steps from registers, mean first, the
-// rest that its rounding leaves in x - m taken off again, so that a large
-// mean costs no accuracy; all arithmetic is fp32.
+// stays causal) and are taken in two steps from registers, the mean (of the
+// values less the group's first, so that a large mean costs no accuracy) and
+// then the variance; all arithmetic is fp32.
 //
 // Gradients, with dz = dy act'(z) (no gate) or dy act(gate):
 //     dgate = dy z act'(gate),   dweight = sum dz x^,   dbias = sum dz,
@@ -99,20 +99,37 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ float sigmoid(float u) { return __fdividef(1.0f, 1.0f + __expf(-u)); }
-__device__ __forceinline__ float act_of(float u, int act) {
-    return act == kNone ? u : act == kSilu ? u * sigmoid(u) : sigmoid(u);
+// 1 / (1 + e^-u) from the hardware's base-2 exponential and reciprocal (2 ulp each; e^-u = inf: 0).
+__device__ __forceinline__ float sigmoid(float u) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * u));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
 }
-// act(u) and its derivative
-__device__ __forceinline__ void act_both(float u, int act, float &f, float &d) {
+// act(u) for eight values, and with DER its derivative; the choice is made once for all eight.
+template <bool DER>
+__device__ __forceinline__ void act8(int act, const float (&u)[8], float (&f)[8], float (&d)[8]) {
     if (act == kNone) {
-        f = u;
-        d = 1.0f;
-        return;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[e] = u[e];
+            if (DER) d[e] = 1.0f;
+        }
+    } else if (act == kSilu) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float s = sigmoid(u[e]);
+            f[e] = u[e] * s;
+            if (DER) d[e] = fmaf(f[e], 1.0f - s, s);
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float s = sigmoid(u[e]);
+            f[e] = s;
+            if (DER) d[e] = fmaf(-s, s, s);
+        }
     }
-    const float s = sigmoid(u);
-    f = act == kSilu ? u * s : s;
-    d = act == kSilu ? s * (1.0f + u * (1.0f - s)) : s * (1.0f - s);
 }
 
 // The walk of a thread over its CTA's tokens: slots of GPB groups of L lanes,
@@ -155,17 +172,23 @@ struct Walk {
     }
 };
 
-// Mean and 1 / sqrt(var + eps) of a group; v leaves as x - mean.
+// 1 / sqrt(var + eps) of a group; v leaves as x - mean.  The mean is taken of x less the group's
+// first value, so that rounding it is relative to the spread.
 template <int L, int N>
 __device__ __forceinline__ float normalise(const Params &p, int l, float (&v)[N][8]) {
     const float inv = 1.0f / (float)p.D;
-    float sum = 0.0f;
+    const float x0 = __shfl_sync(kFullMask, v[0][0], 0, L);
+    float sum = 0.0f, sq = 0.0f;
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+    for (int n = 0; n < N; ++n) {
+        const bool in = (n * L + l) * 8 < p.D;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += v[n][e];
+        for (int e = 0; e < 8; ++e) {
+            v[n][e] = in ? v[n][e] - x0 : 0.0f;
+            sum += v[n][e];
+        }
+    }
     const float mean = group_sum<L>(sum) * inv;
-    float sq = 0.0f, off = 0.0f;   // off: what rounding left of the mean
 #pragma unroll
     for (int n = 0; n < N; ++n) {
         const bool in = (n * L + l) * 8 < p.D;
@@ -173,16 +196,9 @@ __device__ __forceinline__ float normalise(const Params &p, int l, float (&v)[N]
         for (int e = 0; e < 8; ++e) {
             v[n][e] = in ? v[n][e] - mean : 0.0f;
             sq = fmaf(v[n][e], v[n][e], sq);
-            off += v[n][e];
         }
     }
-    off = group_sum<L>(off) * inv;
-    const float var = fmaxf(fmaf(-off, off, group_sum<L>(sq) * inv), 0.0f);
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[n][e] -= off;
-    return rsqrtf(var + p.eps);
+    return rsqrtf(fmaf(group_sum<L>(sq), inv, p.eps));
 }
 
 // A lane's N pieces of eight channels: piece n starts at channel (n L + l) 8.
@@ -235,11 +251,15 @@ __global__ void __launch_bounds__(kThreads) group_norm_kernel(Params p) {
         for (int n = 0; n < N; ++n) {
             const int c = (n * L + l) * 8;
             if (!live || c >= p.D) continue;
-            float o[8];
+            float z[8], o[8], none[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float z = fmaf(v[n][e] * r, wt[n][e], bs[n][e]);
-                o[e] = p.gate ? z * act_of(gt[n][e], p.act) : act_of(z, p.act);
+            for (int e = 0; e < 8; ++e) z[e] = fmaf(v[n][e] * r, wt[n][e], bs[n][e]);
+            if (p.gate) {
+                act8<false>(p.act, gt[n], o, none);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= z[e];
+            } else {
+                act8<false>(p.act, z, o, none);
             }
             store8(y + c, o);
         }
@@ -298,27 +318,34 @@ __global__ void __launch_bounds__(kThreads) group_norm_backward_kernel(Params p)
         const float r = normalise<L, N>(p, l, v);
         float hs = 0.0f, hx = 0.0f;
 #pragma unroll
-        for (int n = 0; n < N; ++n)
+        for (int n = 0; n < N; ++n) {
+            float z[8], f[8], df[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float xh = v[n][e] * r, z = fmaf(xh, wt[n][e], bs[n][e]);
-                float f, df, dz;
-                if (p.gate) {
-                    act_both(gt[n][e], p.act, f, df);
-                    gt[n][e] = d[n][e] * z * df;
-                    dz = d[n][e] * f;
-                } else {
-                    act_both(z, p.act, f, df);
-                    dz = d[n][e] * df;
-                }
-                aw[n][e] = fmaf(dz, xh, aw[n][e]);
-                ab[n][e] += dz;
-                const float h = dz * wt[n][e];
-                hs += h;
-                hx = fmaf(h, xh, hx);
-                v[n][e] = xh;
-                d[n][e] = h;
+                v[n][e] *= r;
+                z[e] = fmaf(v[n][e], wt[n][e], bs[n][e]);
             }
+            if (p.gate) {
+                act8<true>(p.act, gt[n], f, df);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    gt[n][e] = d[n][e] * z[e] * df[e];
+                    d[n][e] *= f[e];
+                }
+            } else {
+                act8<true>(p.act, z, f, df);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[n][e] *= df[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {   // d is dz here, then h
+                aw[n][e] = fmaf(d[n][e], v[n][e], aw[n][e]);
+                ab[n][e] += d[n][e];
+                d[n][e] *= wt[n][e];
+                hs += d[n][e];
+                hx = fmaf(d[n][e], v[n][e], hx);
+            }
+        }
         hs = group_sum<L>(hs) * inv;
         hx = group_sum<L>(hx) * inv;
 #pragma unroll
@@ -327,7 +354,7 @@ __global__ void __launch_bounds__(kThreads) group_norm_backward_kernel(Params p)
             if (!live || c >= p.D) continue;
             float dx[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dx[e] = r * (d[n][e] - hs - v[n][e] * hx);
+            for (int e = 0; e < 8; ++e) dx[e] = r * fmaf(-v[n][e], hx, d[n][e] - hs);
             store8(static_cast<io_t *>(p.dx) + xa + c, dx);
             if (p.gate) store8(static_cast<io_t *>(p.dgate) + ya + c, gt[n]);
         }
