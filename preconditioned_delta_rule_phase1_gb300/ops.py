@@ -13,8 +13,10 @@ of the wrong type would otherwise be read or written out of its bounds.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
+import operator
 import os
 import threading
 
@@ -514,6 +516,7 @@ def forward_kda(q, k, v, beta, r=None, eta=0.1, d0=None, alpha_k=None, S0=None, 
 # checks above are made in one pass per tensor, and addresses go to ctypes as plain integers.
 
 _IO = {torch.float32: OSDN_F32, torch.bfloat16: OSDN_BF16}
+_dtype_of = operator.attrgetter("dtype")
 
 
 def _arg(name, t, shape, dtype, device):
@@ -690,43 +693,50 @@ def group_norm_backward(x, dy, weight=None, bias=None, gate=None, groups=None, a
     return g
 
 
+def _tensor_table(what, tensors, dev):
+    """Addresses, element counts and io types of `tensors`, which must be dense and on
+    `dev`.  Whole-list maps: a model has hundreds of gradients."""
+    at, n = (dev.index if dev.type == "cuda" else -1), len(tensors)
+    if (list(map(torch.Tensor.get_device, tensors)).count(at) != n
+            or not all(map(torch.Tensor.is_contiguous, tensors))):
+        for i, t in enumerate(tensors):
+            _expect("%s[%d]" % (what, i), t, t.shape, t.dtype, dev)
+    try:
+        ios = array.array("i", [_IO[d] for d in map(_dtype_of, tensors)])
+    except KeyError as e:
+        raise TypeError("%s must be float32 or bfloat16, got %s" % (what, e)) from None
+    return (array.array("Q", map(torch.Tensor.data_ptr, tensors)),
+            array.array("q", map(torch.Tensor.numel, tensors)), ios)
+
+
 def clip_grad_norm(grads, max_norm, outs=None, norm=None, workspace=None, stream=None):
     """Clip tensors by their global 2-norm (osdn_clip_grad_norm): every g becomes
-    g min(1, max_norm / norm), in place, or in `outs` (tensors like `grads`).
-    Returns norm [1] fp32 on the device.  max_norm = inf: the norm alone."""
+    g min(1, max_norm / norm), in place, or in `outs` (as many elements of the
+    same types).  Returns norm [1] fp32 on the device.  max_norm = inf: the
+    norm alone."""
     grads = list(grads)
     n = len(grads)
     if n == 0 and norm is None:
         raise ValueError("no gradients and no norm tensor: the device is unknown")
     dev = grads[0].device if n else norm.device
-    at = dev.index if dev.type == "cuda" else -1
-    if not all(g.get_device() == at and g.is_contiguous() for g in grads):
-        for i, g in enumerate(grads):
-            _expect("grads[%d]" % i, g, g.shape, g.dtype, dev)
-    try:
-        ios = [_IO[g.dtype] for g in grads]
-    except KeyError as e:
-        raise TypeError("gradients must be float32 or bfloat16, got %s" % e) from None
-    sizes = [g.numel() for g in grads]
-    gp = written = [g.data_ptr() for g in grads]
-    op = None
+    gp, sizes, ios = _tensor_table("grads", grads, dev)
+    op = gp
     if outs is not None:
         outs = list(outs)
         if len(outs) != n:
             raise ValueError("%d gradients, %d outputs" % (n, len(outs)))
-        if not all(o.shape == g.shape and o.dtype == g.dtype and o.get_device() == at and o.is_contiguous()
-                   for g, o in zip(grads, outs)):
-            for i, (g, o) in enumerate(zip(grads, outs)):
-                _expect("outs[%d]" % i, o, g.shape, g.dtype, dev)
-        written = [o.data_ptr() for o in outs]
-        op = (ctypes.c_void_p * n)(*written)
-    written = [p for p, s in zip(written, sizes) if s]
-    if len(set(written)) != len(written):
-        raise ValueError("a tensor is written twice")
+        op, osizes, oios = _tensor_table("outs", outs, dev)
+        if osizes != sizes or oios != ios:
+            raise ValueError("outs must have the gradients' sizes and types")
+    if len(set(op)) != n:   # empty tensors may share an address
+        written = [p for p, s in zip(op, sizes) if s]
+        if len(set(written)) != len(written):
+            raise ValueError("a tensor is written twice")
     if norm is None:
         norm = torch.empty(1, dtype=F32, device=dev)
-    args = (n, (ctypes.c_void_p * n)(*gp), op, (ctypes.c_longlong * n)(*sizes), (ctypes.c_int * n)(*ios),
-            float(max_norm), _arg("norm", norm, (1,), F32, dev))
+    at = lambda a: a.buffer_info()[0] if n else None  # noqa: E731
+    args = (n, at(gp), None if outs is None else at(op), at(sizes), at(ios), float(max_norm),
+            _arg("norm", norm, (1,), F32, dev))
     _run("osdn_clip_grad_norm", dev, stream, args, _workspace(workspace, dev),
          clip_grad_norm_workspace_bytes(n))
     return norm
