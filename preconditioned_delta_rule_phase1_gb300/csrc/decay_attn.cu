@@ -25,7 +25,7 @@ constexpr int kThreads = 128;
 constexpr int kRows = 64;
 constexpr int kStage = 16;   // tokens staged at a time
 constexpr int kGroup = 8;    // tokens between rescalings
-constexpr int kUnit = 64;    // tokens a unit of the split
+constexpr int kUnit = kStage;   // tokens a unit of the split
 
 struct Args {
     Pass p;
@@ -39,7 +39,8 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
     constexpr int M = K / 16;
     __shared__ __align__(16) float ks[kStage][K], qs[STATE_ONLY ? 1 : kStage][K];
     __shared__ __align__(8) float vs[kStage][kRows];
-    __shared__ Pow pows[kGroup + 1];
+    __shared__ Pow pows[kGroup + 1];     // a^n
+    __shared__ float2 updown[kGroup];   // a^-x and a^x after a group's n-th token
     const Pass &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pc = lane & 3, row = warp * 16 + (lane >> 2) * 2, row0 = blockIdx.x * kRows;
@@ -130,6 +131,11 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
         };
         __syncthreads();   // the last sequence's powers have been read
         if (tid <= kGroup) pows[tid] = decay_pow(dec, tid);
+        if (tid < kGroup) {
+            // S_t = a^x S~ after the token, x counted from the group's start
+            const float down = grouped ? decay_pow(dec, tid + (p.rev ? 0 : 1)).hi : 1.0f;
+            updown[tid] = make_float2(1.0f / down, down);
+        }
         fetch(tbeg);
         for (int t0 = tbeg; t0 < tend; t0 += kStage) {
             __syncthreads();   // the last stage has been read
@@ -144,10 +150,10 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
             __syncthreads();
             if (t0 + kStage < tend) fetch(t0 + kStage);
             const int tn = min(kStage, tend - t0);
+#pragma unroll 2
             for (int tt = 0; tt < tn; ++tt) {
-                // S_t = a^x S~ after this token, x counted from the group's start
-                const int in = tt & (kGroup - 1), x = in + (p.rev ? 0 : 1);
-                const float down = grouped ? pows[x].hi : 1.0f, up = 1.0f / down;
+                const int in = tt & (kGroup - 1);
+                const float up = updown[in].x, down = updown[in].y;
                 if (!grouped && !p.rev) scale(pows[1]);
                 const float2 vv = *reinterpret_cast<const float2 *>(&vs[tt][row]);
                 const float2 w0 = make_float2(up * vv.x, up * vv.x), w1 = make_float2(up * vv.y, up * vv.y);
@@ -286,12 +292,19 @@ Split simt_split(int BH, int T, int K, int V) {
     const int nch = (int)(((long long)T + kUnit - 1) / kUnit);
     // CTAs resident at once, in ranges (the same for K and V exchanged)
     const long long slots = 152LL * 3 / (std::max(K, V) / kRows);
-    const long long N = (long long)BH * nch, G = std::min(N, slots);
-    // units in a row, one by one: a split pass costs about two thirds more, and two launches
-    // (about 16 units' time)
-    const long long whole = (BH + slots - 1) / slots * nch;
-    const long long split = (N + G - 1) / G * 5 / 3 + 16;
-    return make_split(kUnit, 0, BH, T, (int)(G > BH && split < whole ? G : BH));
+    const long long N = (long long)BH * nch;
+    // Tokens one after another: a split pass costs two thirds more, two launches (about 40 tokens'
+    // time) and, in chain_states, about one a range of a sequence.
+    const long long whole = (BH + slots - 1) / slots * T;
+    long long best = whole, G = BH;
+    for (long long g = std::min(N, slots); g > BH; g /= 2) {
+        const long long cost = (N + g - 1) / g * kUnit * 5 / 3 + 40 + g / BH;
+        if (cost < best) {
+            best = cost;
+            G = g;
+        }
+    }
+    return make_split(kUnit, 0, BH, T, (int)G);
 }
 
 cudaError_t attend_simt(const Pass &p, void *scratch, int *status, cudaStream_t stream) {

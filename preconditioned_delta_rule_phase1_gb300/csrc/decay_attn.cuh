@@ -40,7 +40,7 @@ struct Pass {
 
 // The time axis in `nch` units of `unit` tokens a sequence; the BH nch units,
 // sequence by sequence, are cut into G ranges of nearly equal length, one a
-// CTA (BH nch fits 31 bits: a unit is 8 KB or more of K alone).  A range that starts inside a sequence starts from the state that the
+// CTA (BH nch fits 31 bits: a unit is 4 KB or more of K alone).  A range that starts inside a sequence starts from the state that the
 // range before it leaves: a first pass forms what each range adds to that
 // state (its units of the sequence it ends in), a small kernel chains them.
 // Backwards in time the units start at the sequence's last token or, with

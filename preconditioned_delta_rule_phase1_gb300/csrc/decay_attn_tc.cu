@@ -628,12 +628,19 @@ cudaError_t run(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap 
 
 Split tc_split(int BH, int T, int, int) {
     const int nch = (int)(((long long)T + C - 1) / C);
-    const long long slots = tc::sm_count(), N = (long long)BH * nch, G = std::min(N, slots);
-    // chunks in a row: a split pass reads K and V twice (half as much again), and has two more
-    // launches (about three chunks' time)
-    const long long whole = (BH + slots - 1) / slots * nch;
-    const long long split = (N + G - 1) / G * 3 / 2 + 3;
-    return make_split(C, 1, BH, T, (int)(G > BH && split < whole ? G : BH));
+    const long long slots = tc::sm_count(), N = (long long)BH * nch;
+    // In sixths of a chunk's time: a split pass reads K and V twice (half as much again),
+    // has two more launches (about two chunks' time) and chains the ranges of a sequence (four in
+    // one).
+    long long best = (BH + slots - 1) / slots * nch * 6, G = BH;
+    for (long long g = std::min(N, slots); g > BH; g /= 2) {
+        const long long cost = (N + g - 1) / g * 9 + 12 + g / BH / 4;
+        if (cost < best) {
+            best = cost;
+            G = g;
+        }
+    }
+    return make_split(C, 1, BH, T, (int)G);
 }
 
 cudaError_t attend_tc(const Pass &p, void *scratch, int *status, cudaStream_t stream) {

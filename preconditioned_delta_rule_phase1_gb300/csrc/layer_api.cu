@@ -43,9 +43,9 @@ bool dims_ok(int B, int H, int T) {
     return B >= 0 && H >= 0 && T >= 0 && T <= kMaxTokens && (size_t)B * (size_t)H <= kMaxSeqs;
 }
 
-// Units of the attention's time axis over all sequences, numbered in 31 bits (2^31 of the smaller
-// ones are 17 TB of K).
-size_t units(size_t BH, int T) { return BH * (((size_t)T + 63) / 64); }
+// Units of the attention's time axis over all sequences, numbered in 31 bits (2^31 of the smallest
+// ones are 8 TB of K).
+size_t units(size_t BH, int T) { return BH * (((size_t)T + 15) / 16); }
 
 int check_device() {
     int dev = 0, major = 0, minor = 0;
@@ -113,7 +113,8 @@ cudaError_t attend(int io, const osdn::da::Pass &p, void *scratch, int *status, 
 extern "C" {
 
 size_t osdn_decay_attn_workspace_bytes(int io, int B, int H, int T, int K, int V) {
-    if (!io_ok(io) || !dims_ok(B, H, T) || !width_ok(K) || !width_ok(V) || T == 0 || B * H == 0)
+    if (!io_ok(io) || !dims_ok(B, H, T) || !width_ok(K) || !width_ok(V) || T == 0 || B * H == 0 ||
+        units((size_t)B * H, T) > 0x7fffffff)
         return kStatusBytes;
     return kStatusBytes + attend_bytes(io, B * H, T, K, V);
 }
@@ -128,11 +129,11 @@ int osdn_decay_attn(int io, int B, int H, int T, int K, int V, const void *q, co
     const size_t BH = (size_t)B * H, e = io_bytes(io);
     if (BH == 0) return OSDN_OK;
     if (T > 0 && (!q || !k || !v || !decay || !o)) return OSDN_ERR_NULL;
+    if (units(BH, T) > 0x7fffffff) return OSDN_ERR_DIMS;
     const size_t kb = BH * T * K * e, vb = BH * T * V * e, sb = BH * V * K * 4;
     const Buf bufs[] = {{q, kb, false}, {k, kb, false}, {v, vb, false}, {decay, (size_t)H * 4, false},
                         {S0, sb, false}, {o, vb, true}, {ST, sb, true}, {workspace, workspace_bytes, true}};
     if (int c = check_bufs(bufs)) return c;
-    if (units(BH, T) > 0x7fffffff) return OSDN_ERR_DIMS;
     if (int c = check_device()) return c;
     cudaStream_t st = (cudaStream_t)stream;
     if (T == 0) return done(osdn::fill_state_launch(ST ? sb / 4 : 0, S0, 0.0f, ST, st));
@@ -160,7 +161,8 @@ int osdn_decay_attn_step(int io, int B, int H, int K, int V, const void *q, cons
 }
 
 size_t osdn_decay_attn_backward_workspace_bytes(int io, int B, int H, int T, int K, int V) {
-    if (!io_ok(io) || !dims_ok(B, H, T) || !width_ok(K) || !width_ok(V) || T == 0 || B * H == 0)
+    if (!io_ok(io) || !dims_ok(B, H, T) || !width_ok(K) || !width_ok(V) || T == 0 || B * H == 0 ||
+        units((size_t)B * H, T) > 0x7fffffff)
         return kStatusBytes;
     const size_t a = attend_bytes(io, B * H, T, K, V), b = attend_bytes(io, B * H, T, V, K);
     return kStatusBytes + (a > b ? a : b);
@@ -177,12 +179,12 @@ int osdn_decay_attn_backward(int io, int B, int H, int T, int K, int V, const vo
     const size_t BH = (size_t)B * H, e = io_bytes(io);
     if (BH == 0) return OSDN_OK;
     if (T > 0 && (!q || !k || !v || !decay || !d_o || !dq || !dk || !dv)) return OSDN_ERR_NULL;
+    if (units(BH, T) > 0x7fffffff) return OSDN_ERR_DIMS;
     const size_t kb = BH * T * K * e, vb = BH * T * V * e, sb = BH * V * K * 4;
     const Buf bufs[] = {{q, kb, false}, {k, kb, false}, {v, vb, false}, {decay, (size_t)H * 4, false},
                         {S0, sb, false}, {d_o, vb, false}, {d_ST, sb, false}, {dq, kb, true},
                         {dk, kb, true}, {dv, vb, true}, {dS0, sb, true}, {workspace, workspace_bytes, true}};
     if (int c = check_bufs(bufs)) return c;
-    if (units(BH, T) > 0x7fffffff) return OSDN_ERR_DIMS;
     if (int c = check_device()) return c;
     cudaStream_t st = (cudaStream_t)stream;
     if (T == 0) return done(osdn::fill_state_launch(dS0 ? sb / 4 : 0, d_ST, 0.0f, dS0, st));
