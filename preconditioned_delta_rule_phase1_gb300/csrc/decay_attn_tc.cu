@@ -38,8 +38,8 @@
 // K^): the next chunk's tiles wait in L2, brought there a chunk ahead, and
 // are loaded as their places fall free, K by halves.
 // STATE_ONLY takes its chunks last to first with weights up to the range's
-// end, so that they add up in TMEM and only the sum is read; it also leaves
-// in L2 what the second launch reads first.  The roles' loops are kept short
+// end, so that they add up in TMEM, four at a time; it also leaves in L2 what
+// the second launch reads first.  The roles' loops are kept short
 // (little unrolling): each runs once a chunk, and unrolled they miss the
 // instruction cache (2x16x8192x128: 124 -> 80 us for the second launch).
 // Every wait is bounded: one that runs out records OSDN_ERR_TIMEOUT and all
@@ -73,6 +73,12 @@ constexpr uint32_t kColO1 = 128;  // Q S^T
 constexpr uint32_t kColO2 = 256;  // P V
 constexpr uint32_t kColD = 384;   // V^T K^
 constexpr uint32_t kTmemCols = 512;
+// STATE_ONLY adds kGroup chunks up in TMEM before the sum goes to registers: two sets of columns in
+// turn, in each one for K^'s first part and one for the others.  The tensor cores cut every sum off
+// at 24 bits, so that each of the eight products a chunk with the first part costs the sum up to
+// 2^-24; the others are 2^-8 as large and cost nothing where they have columns of their own.
+constexpr int kGroup = 4;
+__host__ __device__ constexpr uint32_t group_col(int group, int small) { return 256 * (group & 1) + 128 * small; }
 
 template <int K, int V, bool STATE_ONLY>
 struct Lay {
@@ -262,8 +268,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll 1
             for (int j = 0; j < n; ++j) {
                 const uint32_t k = ptx::smem_u32(sK(j)), v = ptx::smem_u32(sV(j));
-                // P's columns are free once the last P V has completed
-                if (!poll(bars.fullK[j & 1], j >> 1) || !poll(bars.fullQ, j) || (j && !poll(bars.o_full, j - 1))) break;
+                // P's columns are free once the last P V has completed; and every waiter has seen the
+                // last Q K^T (the warps that form K^ show it), so that no phase of qk_full is missed
+                if (!poll(bars.fullK[j & 1], j >> 1) || !poll(bars.fullQ, j) ||
+                    (j && (!poll(bars.o_full, j - 1) || !poll(bars.kq_full[0], j - 1))))
+                    break;
                 ptx::tc_fence_after();
 #pragma unroll 1
                 for (int b = 0; b < K / 64; ++b)
@@ -302,7 +311,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             bool ok = true;
             for (int j = 0; j < n && ok; ++j) {
                 const uint32_t v = ptx::smem_u32(sV(j));
-                ok = poll(bars.fullV[j % NV], j / NV) && (STATE_ONLY || !j || poll(bars.ds_free, j - 1));
+                ok = poll(bars.fullV[j % NV], j / NV) &&
+                     (STATE_ONLY || !j || poll(bars.ds_free, j - 1));
 #pragma unroll 1
                 for (int h = 0; ok && h < kSteps; ++h) {   // V^T K^ step by step, small parts first
                     if (!(ok = poll(bars.kq_full[h], j))) break;
@@ -314,13 +324,14 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         const uint64_t db = dmn0(at, C * 128) + mnoff(kStep / 16 * h);
 #pragma unroll
                         for (int ks = 0; ks < kStep / 16; ++ks)
-                            ptx::umma_bf16(tmem + kColD, da + mnoff(ks), db + mnoff(ks), id_d,
-                                           h > 0 || part < 2 || ks > 0 || (STATE_ONLY && j > 0));
+                            ptx::umma_bf16(tmem + (STATE_ONLY ? group_col(j / kGroup, part > 0) : kColD), da + mnoff(ks),
+                                           db + mnoff(ks), id_d,
+                                           STATE_ONLY ? j % kGroup || h || part == 1 || ks : h || part < 2 || ks);
                     }
                     if (STATE_ONLY) ptx::umma_commit(&bars.kq_free[h]);
                 }
                 if (!ok) break;
-                if (!STATE_ONLY || j == n - 1) ptx::umma_commit(&bars.ds_full);
+                if (!STATE_ONLY || j % kGroup == kGroup - 1 || j == n - 1) ptx::umma_commit(&bars.ds_full);
                 ptx::umma_commit(&bars.emptyV[j % NV]);
                 if (!STATE_ONLY) ptx::umma_commit(&bars.emptyK[j & 1]);
             }
@@ -447,7 +458,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else {
         // ======================================================== K^ and the state
         // row i of S: TMEM lane i (V = 128) or 32 (i / 16) + i % 16 (V = 64); columns c0 ..
-        constexpr int NC = K / 2;
+        constexpr int NC = K * 4 / NW;
         const int c0 = ((warp - 6) >> 2) * NC;
         const int row = V == 128 ? 32 * q4 + lane : 16 * q4 + lane;
         const bool act = V == 128 || lane < 16;
@@ -457,12 +468,33 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         constexpr int P8 = K / 8, NC8 = P8 > NW ? P8 / NW : 1, RG = NW > P8 ? NW / P8 : 1;
         constexpr int NR = kStep / 32 / RG;   // 32s of rows a step
         const int piece = (warp - 6) % (P8 / NC8) * NC8, rg = (warp - 6) / (P8 / NC8) * NR;
-        float S[STATE_ONLY ? 1 : NC], wk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        float S[NC], wk[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         Pow f = {1.0f, 0.0f};    // the chunk's whole decay; STATE_ONLY: from the chunk's end to the range's
         Pow fc = {1.0f, 0.0f};
         int have = -1, have_len = 0;
         bool ok = true;
         Walk w(a, STATE_ONLY ? hi - 1 : lo);
+        // STATE_ONLY: the group's sums into registers.  A warp does that before it forms more K^, so
+        // that kq_full of the group after the next finds the columns free.
+        auto add_group = [&](int group) {
+            if (!wait(bars.ds_full, group)) return false;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int e = 0; e < NC; e += 16) {
+                float x[16], y[16];
+                ptx::tmem_ld16(tmem + lane_off + group_col(group, 0) + c0 + e, x);
+                ptx::tmem_ld16(tmem + lane_off + group_col(group, 1) + c0 + e, y);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) S[e + i] += x[i] + y[i];
+            }
+            ptx::tc_fence_before();
+            return true;
+        };
+        if (STATE_ONLY) {
+#pragma unroll
+            for (int e = 0; e < NC; ++e) S[e] = 0.0f;
+        }
 #pragma unroll 1
         for (int j = 0; j < n && ok; ++j) {
             const int len = w.len();
@@ -550,6 +582,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 arrive(bars.emptyK[j & 1]);
                 f = pow_mul(f, fc);
                 w.prev();
+                if (j && j % kGroup == 0 && !(ok = add_group(j / kGroup - 1))) break;
             } else {
                 if (!(ok = wait(bars.ds_full, j))) break;
                 ptx::tc_fence_after();
@@ -579,19 +612,12 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 w.next();
             }
         }
-        if (STATE_ONLY && ok && warp < 14 && wait(bars.ds_full, 0)) {   // eight warps read the sum
-            ptx::tc_fence_after();
+        if (STATE_ONLY && ok && add_group((n - 1) / kGroup) && act) {
             float *dst = a.states + (size_t)(g + 1) * sb + (size_t)row * K + c0;
-#pragma unroll 1
-            for (int e = 0; e < NC; e += 32) {
-                float x[32];
-                tc::tmem_ld32(tmem + lane_off + kColD + c0 + e, x);
-                if (!act) continue;
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                    const float y[4] = {x[i], x[i + 1], x[i + 2], x[i + 3]};
-                    store4(dst + e + i, y);
-                }
+            for (int i = 0; i < NC; i += 4) {
+                const float y[4] = {S[i], S[i + 1], S[i + 2], S[i + 3]};
+                store4(dst + i, y);
             }
         }
     }

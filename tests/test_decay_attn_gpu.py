@@ -93,6 +93,43 @@ def test_every_way_of_cutting_the_time_axis(io, B, H, T, K, V):
     assert torch.equal(o, o2) and torch.equal(ST, ST2)
 
 
+def blocks64(q, k, v, decay, S, block=200):
+    """The recurrence in 64 bits, block by block (long sequences; autograd passes through)."""
+    q, k, v, a = (x.double() for x in (q, k, v, decay))
+    S, out = S.double(), []
+    for t in range(0, q.shape[2], block):
+        qb, kb, vb = (x[:, :, t:t + block] for x in (q, k, v))
+        i = torch.arange(qb.shape[2], device=q.device, dtype=torch.float64)
+        gap = i[:, None] - i[None, :]
+        w = torch.where(gap >= 0, a[:, None, None] ** gap.clamp(min=0), 0.0)
+        out.append(((qb @ kb.transpose(-1, -2)) * w) @ vb
+                   + (qb @ S.transpose(-1, -2)) * (a[:, None] ** (i + 1))[None, :, :, None])
+        S = S * (a ** len(i))[None, :, None, None] + (vb * (a[:, None] ** (len(i) - 1 - i))[None, :, :, None]).transpose(-1, -2) @ kb
+    return torch.cat(out, 2), S
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,T,K,V", [(1, 8, 20001, 128, 128), (2, 3, 33000, 64, 64), (1, 16, 30000, 128, 64),
+                                       (1, 16, 30000, 64, 128)])
+def test_long_ranges(io, B, H, T, K, V):
+    # ranges of many units each, forwards and backwards; the states' tolerance is that of fp32
+    # sums over a memory of thousands of tokens
+    x = inputs(B, H, T, K, V, io, seed=T + K, decay=1.0 - torch.exp2(-torch.linspace(4, 12, H)))
+    ws = ops.Workspace()
+    o, ST = forward(x, ws)
+    got = backward(x, ws)
+    assert ws.status() == 0
+    t = {n: x[n].double().requires_grad_() for n in ("q", "k", "v", "S0")}
+    ro, rS = blocks64(t["q"], t["k"], t["v"], x["decay"], t["S0"])
+    assert rel_err(o, ro.detach().cpu()) < TOL[io] and rel_err(ST, rS.detach().cpu()) < STATE_TOL
+    # in the mean the state loses nothing against fp32 sums either
+    assert float((ST.double() - rS.detach()).norm() / rS.detach().norm()) < 1e-6
+    loss = (ro * x["do"].double()).sum() + (rS * x["dST"].double()).sum()
+    for n, r in zip(t, torch.autograd.grad(loss, list(t.values()))):
+        assert rel_err(got[n], r.cpu()) < (STATE_TOL if n == "S0" else TOL[io]), n
+    assert float((got["S0"].double() - r).norm() / r.norm()) < 1e-6
+
+
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 def test_prompt_pieces_and_steps_chain(io):
     x = inputs(2, 3, 300, 128, 64, io, seed=5)
