@@ -90,9 +90,8 @@ struct Lay {
     // (K's place is free the earlier)
     static constexpr int oP = oV + NV * kV;
     static constexpr int oQ = oP + (STATE_ONLY ? 3 : 2) * kK;
-    // bf16 S (V rows of K columns); between its last use and the next S, O on its way out
-    static constexpr int oS = oQ + (STATE_ONLY ? 0 : kK);
-    static constexpr int kBytes = oS + (STATE_ONLY ? 0 : V * 2 * C);
+    static constexpr int oS = oQ + (STATE_ONLY ? 0 : kK);   // bf16 S: V rows of K columns
+    static constexpr int kBytes = oS + (STATE_ONLY ? 0 : V * K * 2);
     static constexpr int kAlloc = kBytes + 1024;
 };
 
@@ -105,7 +104,7 @@ struct Args {
 
 struct Bars {
     uint64_t fullK[2], emptyK[2], fullV[2], emptyV[2], fullQ, emptyQ;
-    uint64_t qk_full, p_ready, o_full, o_free, o_stored;
+    uint64_t qk_full, p_ready, o_full, o_free;
     uint64_t kq_full[kSteps], kq_free[kSteps], s_ready, ds_full, ds_free, done[2];
 };
 
@@ -200,7 +199,6 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (uint64_t *b : one) ptx::mbar_init(b, 1);
         ptx::mbar_init(&bars.p_ready, 4);
         ptx::mbar_init(&bars.o_free, 4);
-        ptx::mbar_init(&bars.o_stored, 4);
         ptx::mbar_init(&bars.s_ready, 8);
         ptx::mbar_init(&bars.ds_free, 8);
         ptx::fence_mbar_init();
@@ -349,6 +347,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // zeros where the gap is negative.
             float *col = s_pow[warp - 2] + 32;
             const float *diag = col + (p.rev ? -lane : 31 - lane);
+            const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
             float wq = 0.0f, far[3] = {0.0f, 0.0f, 0.0f};
             int have = -1;
             int have_len = 0;
@@ -405,6 +404,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
                 if (!wait(bars.o_full, j)) break;
                 ptx::tc_fence_after();
+                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + ((size_t)w.seq * p.T + w.row() + r) * V;
 #pragma unroll 1
                 for (int c = 0; c < V; c += 32) {
                     float x[2][16], y[2][16];
@@ -420,37 +420,20 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        float z[16];
+                        uint32_t out[8];
 #pragma unroll
-                        for (int m = 0; m < 16; m += 2) {
-                            const float2 u = __ffma2_rn(make_float2(wq, wq), make_float2(x[h][m], x[h][m + 1]),
-                                                        make_float2(y[h][m], y[h][m + 1]));
-                            z[m] = u.x;
-                            z[m + 1] = u.y;
+                        for (int m = 0; m < 8; ++m) {
+                            const float2 u = __ffma2_rn(make_float2(wq, wq), make_float2(x[h][2 * m], x[h][2 * m + 1]),
+                                                        make_float2(y[h][2 * m], y[h][2 * m + 1]));
+                            out[m] = tc::pack_bf16x2(u.x, u.y);
                         }
-                        tc::st_row_sw128(smem + LY::oS, C, r, c + 16 * h, z, 16);
-                    }
-                }
-                // the warp's 32 rows back out of shared memory, 16 bytes a lane and whole rows at a time
-                __syncwarp();
-                constexpr int LR = V / 8, RI = 32 / LR;   // lanes a row, rows at a time
-                const int rows = len - 32 * q4;
-                __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) +
-                                   ((size_t)w.seq * p.T + w.row() + 32 * q4) * V + lane % LR * 8;
-                const uint8_t *src = smem + LY::oS + (lane % LR >> 3) * C * 128 + 32 * q4 * 128;
-#pragma unroll 1
-                for (int i = 0; i < 32; i += 4 * RI) {
-                    uint4 out[4];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const int rr = i + m * RI + lane / LR;
-                        out[m] = *reinterpret_cast<const uint4 *>(src + rr * 128 + (((lane % LR) & 7) ^ (rr & 7)) * 16);
-                    }
-                    if (i + 4 * RI == 32) arrive(bars.o_stored);
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const int rr = i + m * RI + lane / LR;
-                        if (rr < rows) *reinterpret_cast<uint4 *>(o + (size_t)rr * V) = out[m];
+                        if (r >= len) continue;
+                        if (wide) {   // whole 32-byte sectors
+                            ptx::st_global_256(o + c + 16 * h, out);
+                        } else {
+                            *reinterpret_cast<uint4 *>(o + c + 16 * h) = make_uint4(out[0], out[1], out[2], out[3]);
+                            *reinterpret_cast<uint4 *>(o + c + 16 * h + 8) = make_uint4(out[4], out[5], out[6], out[7]);
+                        }
                     }
                 }
             }
@@ -537,8 +520,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         for (int i = 0; i < 4; ++i) S[e + i] = x[i];
                     }
                 }
-                // the last chunk's O, which took the place of its state's copy, has left
-                if (j && !(ok = wait(bars.o_stored, j - 1))) break;
+                // the copy of the last chunk's state has been read by Q S^T
+                if (j && !(ok = wait(bars.emptyQ, j - 1))) break;
                 if (act) tc::st_row_sw128(smem + LY::oS, V, row, c0, S, NC);
                 ptx::fence_proxy_async_smem();
                 arrive(bars.s_ready);
