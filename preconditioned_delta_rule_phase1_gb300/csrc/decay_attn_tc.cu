@@ -13,7 +13,8 @@
 // is an output and is carried over thousands of tokens, so it is kept in
 // fp32 (in registers), and K^ enters the product as three bf16 parts
 // (8 + 8 + 8 bits, exactly the fp32 product a^e k): V is exact in bf16, so
-// the update has fp32 accuracy.  Powers of the decay come from repeated
+// the update has fp32 accuracy.  Where the state is not an output two parts
+// do.  Powers of the decay come from repeated
 // squaring in two fp32 (decay_attn.cuh).
 //
 // Bound.  Q, K, V in and O out are 128 KB a chunk at K = V = 128, 2.9 us at
@@ -143,7 +144,9 @@ __device__ __forceinline__ uint32_t top2(float a, float b) {   // the upper 16 b
 }
 __device__ __forceinline__ float top(float a) { return __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
 
-template <int K, int V, bool STATE_ONLY>
+// PARTS: the parts of K^.  Three where the state is an output; two (16 bits) where it only enters
+// Q S^T, as bf16.
+template <int K, int V, bool STATE_ONLY, int PARTS>
 __global__ void __launch_bounds__(threads(STATE_ONLY), 1)
 attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, Args a) {
@@ -316,7 +319,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     if (!(ok = poll(bars.kq_full[h], j))) break;
                     ptx::tc_fence_after();
 #pragma unroll 1
-                    for (int part = 2; part >= 0; --part) {
+                    for (int part = PARTS - 1; part >= 0; --part) {
                         const uint64_t da = dmn0(v, C * 128) + mnoff(kStep / 16 * h);
                         const uint32_t at = STATE_ONLY ? parts + part * LY::kK : part ? parts + (part - 1) * LY::kK : ptx::smem_u32(sK(j));
                         const uint64_t db = dmn0(at, C * 128) + mnoff(kStep / 16 * h);
@@ -324,7 +327,7 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         for (int ks = 0; ks < kStep / 16; ++ks)
                             ptx::umma_bf16(tmem + (STATE_ONLY ? group_col(j / kGroup, part > 0) : kColD), da + mnoff(ks),
                                            db + mnoff(ks), id_d,
-                                           STATE_ONLY ? j % kGroup || h || part == 1 || ks : h || part < 2 || ks);
+                                           STATE_ONLY ? j % kGroup || h || part == 1 || ks : h || part < PARTS - 1 || ks);
                     }
                     if (STATE_ONLY) ptx::umma_commit(&bars.kq_free[h]);
                 }
@@ -547,15 +550,18 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     for (int e = 0; e < 4; ++e) {
                         const float2 x = __fmul2_rn(make_float2(__uint_as_float(in[e] << 16), __uint_as_float(in[e] & 0xffff0000u)), ww);
                         const float2 m = __ffma2_rn(make_float2(top(x.x), top(x.y)), minus, x);
-                        const float2 l = __ffma2_rn(make_float2(top(m.x), top(m.y)), minus, m);
                         ph[e] = top2(x.x, x.y);
                         pm[e] = top2(m.x, m.y);
-                        pl[e] = top2(l.x, l.y);
+                        if (PARTS == 3) {
+                            const float2 l = __ffma2_rn(make_float2(top(m.x), top(m.y)), minus, m);
+                            pl[e] = top2(l.x, l.y);
+                        }
                     }
                     uint8_t *dst = smem + LY::oP + at + (STATE_ONLY ? LY::kK : 0);
                     *reinterpret_cast<uint4 *>(STATE_ONLY ? smem + LY::oP + at : sK(j) + at) = make_uint4(ph[0], ph[1], ph[2], ph[3]);
                     *reinterpret_cast<uint4 *>(dst) = make_uint4(pm[0], pm[1], pm[2], pm[3]);
-                    *reinterpret_cast<uint4 *>(dst + LY::kK) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                    if (PARTS == 3)
+                        *reinterpret_cast<uint4 *>(dst + LY::kK) = make_uint4(pl[0], pl[1], pl[2], pl[3]);
                 }
                 ptx::fence_proxy_async_smem();
                 arrive(bars.kq_full[h]);
@@ -610,15 +616,15 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp == 1) ptx::tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int K, int V, bool STATE_ONLY>
+template <int K, int V, bool STATE_ONLY, int PARTS>
 cudaError_t launch(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Args &a,
                    cudaStream_t stream) {
     constexpr int smem = Lay<K, V, STATE_ONLY>::kAlloc;
     static std::atomic<unsigned long long> attr_done{0};
-    cudaError_t e = smem_attr_once((const void *)attend_tc_kernel<K, V, STATE_ONLY>, smem, attr_done);
+    cudaError_t e = smem_attr_once((const void *)attend_tc_kernel<K, V, STATE_ONLY, PARTS>, smem, attr_done);
     if (e != cudaSuccess) return e;
     // no range follows the last one, so nothing needs its state
-    return launch_overlapped(!STATE_ONLY && a.states && !a.p.given, attend_tc_kernel<K, V, STATE_ONLY>,
+    return launch_overlapped(!STATE_ONLY && a.states && !a.p.given, attend_tc_kernel<K, V, STATE_ONLY, PARTS>,
                              dim3(a.s.G - (STATE_ONLY ? 1 : 0)), threads(STATE_ONLY), smem, stream, mq, mk, mv, a);
 }
 
@@ -626,11 +632,12 @@ template <int K, int V>
 cudaError_t run(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const Args &a,
                 cudaStream_t stream) {
     if (a.states && !a.p.given) {
-        cudaError_t e = launch<K, V, true>(mq, mk, mv, a, stream);
+        cudaError_t e = launch<K, V, true, 3>(mq, mk, mv, a, stream);
         if (e == cudaSuccess) e = chain_states(a.p, a.s, a.states, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch<K, V, false>(mq, mk, mv, a, stream);
+    if (a.p.ST) return launch<K, V, false, 3>(mq, mk, mv, a, stream);
+    return launch<K, V, false, 2>(mq, mk, mv, a, stream);
 }
 
 }  // namespace
