@@ -54,39 +54,38 @@ struct Raw {
 #pragma unroll
         for (int i = 0; i < (int)sizeof(io_t) / 2; ++i) u[i] = reinterpret_cast<const uint4 *>(p)[i];
     }
-    __device__ __forceinline__ void wide(float (&x)[8]) const {
+    // in pairs: the arithmetic below is packed (two fp32 an instruction), since with an activation
+    // the gradients issue more instructions than the loads take time
+    __device__ __forceinline__ void wide(float2 (&x)[4]) const {
         if constexpr (sizeof(io_t) == 4) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                x[4 * i] = __uint_as_float(u[i].x);
-                x[4 * i + 1] = __uint_as_float(u[i].y);
-                x[4 * i + 2] = __uint_as_float(u[i].z);
-                x[4 * i + 3] = __uint_as_float(u[i].w);
+                x[2 * i] = make_float2(__uint_as_float(u[i].x), __uint_as_float(u[i].y));
+                x[2 * i + 1] = make_float2(__uint_as_float(u[i].z), __uint_as_float(u[i].w));
             }
         } else {
             const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[2 * i] = __uint_as_float(w[i] << 16);
-                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
+            for (int i = 0; i < 4; ++i)
+                x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
         }
     }
 };
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ void load8(const float *p, float2 (&x)[4]) {
     Raw<float> r;
     r.load(p);
     r.wide(x);
 }
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void store8(float *p, const float2 (&x)[4]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float2 (&x)[4]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[i].x, x[i].y);
         w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
     *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -100,34 +99,37 @@ __device__ __forceinline__ float group_sum(float v) {
 }
 
 // 1 / (1 + e^-u) from the hardware's base-2 exponential and reciprocal (2 ulp each; e^-u = inf: 0).
-__device__ __forceinline__ float sigmoid(float u) {
-    float e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * u));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+__device__ __forceinline__ float2 sigmoid(float2 u) {
+    float2 e = __fmul2_rn(u, both(-1.4426950408889634f)), s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(e.y));
+    e = __fadd2_rn(e, both(1.0f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
     return s;
 }
 // act(u) for eight values, and with DER its derivative; the choice is made once for all eight.
 template <bool DER>
-__device__ __forceinline__ void act8(int act, const float (&u)[8], float (&f)[8], float (&d)[8]) {
+__device__ __forceinline__ void act8(int act, const float2 (&u)[4], float2 (&f)[4], float2 (&d)[4]) {
     if (act == kNone) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 4; ++e) {
             f[e] = u[e];
-            if (DER) d[e] = 1.0f;
+            if (DER) d[e] = both(1.0f);
         }
     } else if (act == kSilu) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float s = sigmoid(u[e]);
-            f[e] = u[e] * s;
-            if (DER) d[e] = fmaf(f[e], 1.0f - s, s);
+        for (int e = 0; e < 4; ++e) {
+            const float2 s = sigmoid(u[e]);
+            f[e] = __fmul2_rn(u[e], s);
+            if (DER) d[e] = __ffma2_rn(f[e], __ffma2_rn(s, both(-1.0f), both(1.0f)), s);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float s = sigmoid(u[e]);
+        for (int e = 0; e < 4; ++e) {
+            const float2 s = sigmoid(u[e]);
             f[e] = s;
-            if (DER) d[e] = fmaf(-s, s, s);
+            if (DER) d[e] = __fmul2_rn(s, __ffma2_rn(s, both(-1.0f), both(1.0f)));
         }
     }
 }
@@ -175,30 +177,30 @@ struct Walk {
 // 1 / sqrt(var + eps) of a group; v leaves as x - mean.  The mean is taken of x less the group's
 // first value, so that rounding it is relative to the spread.
 template <int L, int N>
-__device__ __forceinline__ float normalise(const Params &p, int l, float (&v)[N][8]) {
+__device__ __forceinline__ float normalise(const Params &p, int l, float2 (&v)[N][4]) {
     const float inv = 1.0f / (float)p.D;
-    const float x0 = __shfl_sync(kFullMask, v[0][0], 0, L);
-    float sum = 0.0f, sq = 0.0f;
+    const float x0 = __shfl_sync(kFullMask, v[0][0].x, 0, L);
+    float2 sum = both(0.0f), sq = both(0.0f);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const bool in = (n * L + l) * 8 < p.D;
+    for (int n = 0; n < N; ++n) {   // (channels past D hold zeros, and keep them)
+        const float2 m = both((n * L + l) * 8 < p.D ? -x0 : 0.0f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[n][e] = in ? v[n][e] - x0 : 0.0f;
-            sum += v[n][e];
+        for (int e = 0; e < 4; ++e) {
+            v[n][e] = __fadd2_rn(v[n][e], m);
+            sum = __fadd2_rn(sum, v[n][e]);
         }
     }
-    const float mean = group_sum<L>(sum) * inv;
+    const float mean = group_sum<L>(sum.x + sum.y) * inv;
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-        const bool in = (n * L + l) * 8 < p.D;
+        const float2 m = both((n * L + l) * 8 < p.D ? -mean : 0.0f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[n][e] = in ? v[n][e] - mean : 0.0f;
-            sq = fmaf(v[n][e], v[n][e], sq);
+        for (int e = 0; e < 4; ++e) {
+            v[n][e] = __fadd2_rn(v[n][e], m);
+            sq = __ffma2_rn(v[n][e], v[n][e], sq);
         }
     }
-    return rsqrtf(fmaf(group_sum<L>(sq), inv, p.eps));
+    return rsqrtf(fmaf(group_sum<L>(sq.x + sq.y), inv, p.eps));
 }
 
 // A lane's N pieces of eight channels: piece n starts at channel (n L + l) 8.
@@ -206,7 +208,7 @@ template <typename io_t, int L, int N>
 __global__ void __launch_bounds__(kThreads) group_norm_kernel(Params p) {
     Walk<L> w(p);
     const int l = w.l;
-    float wt[N][8], bs[N][8];
+    float2 wt[N][4], bs[N][4];
     Raw<io_t> rx[N], rg[N];
     auto fetch = [&] {
         const bool live = w.live();
@@ -228,15 +230,15 @@ __global__ void __launch_bounds__(kThreads) group_norm_kernel(Params p) {
     for (int n = 0; n < N; ++n) {
         const int c = (n * L + l) * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            wt[n][e] = 1.0f;
-            bs[n][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) {
+            wt[n][e] = both(1.0f);
+            bs[n][e] = both(0.0f);
         }
         if (w.in_range && c < p.D && p.weight) load8(p.weight + (size_t)w.g * p.D + c, wt[n]);
         if (w.in_range && c < p.D && p.bias) load8(p.bias + (size_t)w.g * p.D + c, bs[n]);
     }
     for (int i = Walk<L>::rounds(p); i > 0; --i) {
-        float v[N][8], gt[N][8];
+        float2 v[N][4], gt[N][4];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             rx[n].wide(v[n]);
@@ -251,13 +253,13 @@ __global__ void __launch_bounds__(kThreads) group_norm_kernel(Params p) {
         for (int n = 0; n < N; ++n) {
             const int c = (n * L + l) * 8;
             if (!live || c >= p.D) continue;
-            float z[8], o[8], none[8];
+            float2 z[4], o[4], none[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = fmaf(v[n][e] * r, wt[n][e], bs[n][e]);
+            for (int e = 0; e < 4; ++e) z[e] = __ffma2_rn(__fmul2_rn(v[n][e], both(r)), wt[n][e], bs[n][e]);
             if (p.gate) {
                 act8<false>(p.act, gt[n], o, none);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] *= z[e];
+                for (int e = 0; e < 4; ++e) o[e] = __fmul2_rn(o[e], z[e]);
             } else {
                 act8<false>(p.act, z, o, none);
             }
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(kThreads) group_norm_backward_kernel(Params p)
     Walk<L> w(p);
     const int l = w.l;
     const float inv = 1.0f / (float)p.D;
-    float wt[N][8], bs[N][8], aw[N][8], ab[N][8];
+    float2 wt[N][4], bs[N][4], aw[N][4], ab[N][4];
     Raw<io_t> rx[N], rd[N], rg[N];
     auto fetch = [&] {
         const bool live = w.live();
@@ -296,15 +298,15 @@ __global__ void __launch_bounds__(kThreads) group_norm_backward_kernel(Params p)
     for (int n = 0; n < N; ++n) {
         const int c = (n * L + l) * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            wt[n][e] = 1.0f;
-            bs[n][e] = aw[n][e] = ab[n][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) {
+            wt[n][e] = both(1.0f);
+            bs[n][e] = aw[n][e] = ab[n][e] = both(0.0f);
         }
         if (w.in_range && c < p.D && p.weight) load8(p.weight + (size_t)w.g * p.D + c, wt[n]);
         if (w.in_range && c < p.D && p.bias) load8(p.bias + (size_t)w.g * p.D + c, bs[n]);
     }
     for (int i = Walk<L>::rounds(p); i > 0; --i) {
-        float v[N][8], d[N][8], gt[N][8];
+        float2 v[N][4], d[N][4], gt[N][4];
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             rx[n].wide(v[n]);
@@ -316,45 +318,45 @@ __global__ void __launch_bounds__(kThreads) group_norm_backward_kernel(Params p)
         w.next(p);
         if (i > 1) fetch();   // on its way while this token is computed
         const float r = normalise<L, N>(p, l, v);
-        float hs = 0.0f, hx = 0.0f;
+        float2 h1 = both(0.0f), h2 = both(0.0f);
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-            float z[8], f[8], df[8];
+            float2 z[4], f[4], df[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v[n][e] *= r;
-                z[e] = fmaf(v[n][e], wt[n][e], bs[n][e]);
+            for (int e = 0; e < 4; ++e) {
+                v[n][e] = __fmul2_rn(v[n][e], both(r));
+                z[e] = __ffma2_rn(v[n][e], wt[n][e], bs[n][e]);
             }
             if (p.gate) {
                 act8<true>(p.act, gt[n], f, df);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    gt[n][e] = d[n][e] * z[e] * df[e];
-                    d[n][e] *= f[e];
+                for (int e = 0; e < 4; ++e) {
+                    gt[n][e] = __fmul2_rn(__fmul2_rn(d[n][e], z[e]), df[e]);
+                    d[n][e] = __fmul2_rn(d[n][e], f[e]);
                 }
             } else {
                 act8<true>(p.act, z, f, df);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[n][e] *= df[e];
+                for (int e = 0; e < 4; ++e) d[n][e] = __fmul2_rn(d[n][e], df[e]);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {   // d is dz here, then h
-                aw[n][e] = fmaf(d[n][e], v[n][e], aw[n][e]);
-                ab[n][e] += d[n][e];
-                d[n][e] *= wt[n][e];
-                hs += d[n][e];
-                hx = fmaf(d[n][e], v[n][e], hx);
+            for (int e = 0; e < 4; ++e) {   // d is dz here, then h
+                aw[n][e] = __ffma2_rn(d[n][e], v[n][e], aw[n][e]);
+                ab[n][e] = __fadd2_rn(ab[n][e], d[n][e]);
+                d[n][e] = __fmul2_rn(d[n][e], wt[n][e]);
+                h1 = __fadd2_rn(h1, d[n][e]);
+                h2 = __ffma2_rn(d[n][e], v[n][e], h2);
             }
         }
-        hs = group_sum<L>(hs) * inv;
-        hx = group_sum<L>(hx) * inv;
+        const float hs = group_sum<L>(h1.x + h1.y) * -inv, hx = group_sum<L>(h2.x + h2.y) * -inv;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int c = (n * L + l) * 8;
             if (!live || c >= p.D) continue;
-            float dx[8];
+            float2 dx[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dx[e] = r * fmaf(-v[n][e], hx, d[n][e] - hs);
+            for (int e = 0; e < 4; ++e)
+                dx[e] = __fmul2_rn(both(r), __ffma2_rn(v[n][e], both(hx), __fadd2_rn(d[n][e], both(hs))));
             store8(static_cast<io_t *>(p.dx) + xa + c, dx);
             if (p.gate) store8(static_cast<io_t *>(p.dgate) + ya + c, gt[n]);
         }
