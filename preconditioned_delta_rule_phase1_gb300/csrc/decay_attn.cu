@@ -5,13 +5,21 @@
 // accuracy.
 //
 // The rows of S evolve independently, so a CTA of 128 threads takes 64 rows
-// of one range of the time axis: a thread holds two rows' columns 16m + 4p +
-// {0..3} (p = lane & 3), so that k and q come from shared memory as
-// broadcast 16-byte reads that serve two rows, and a row's dot product needs
-// two shuffles.  The decay costs no multiplication a token: over groups of
-// eight tokens the state is kept as S~ = a^-n S (v is scaled instead) and
-// multiplied by a^8 once a group; heads whose a^-8 would grow too large
-// (a < 1/16) decay token by token.
+// of one range of the time axis: a thread holds four rows' columns 32m + 4p +
+// {0..3} (p = lane & 7), so that k and q come from shared memory as 16-byte
+// reads that serve four rows, and the four dot products are summed over the
+// eight lanes together, four shuffles.  With two rows a thread those reads,
+// four cycles a warp each, took twice the arithmetic's time (2x16x8192x128:
+// 1153 -> 997 us; 1024 sequences of 256 tokens: 802 -> 643 us).
+// The decay costs no multiplication a token: over groups of eight tokens the
+// state is kept as S~ = a^-n S (v is scaled instead) and multiplied by a^8
+// once a group; heads whose a^-8 would grow too large (a < 1/16) decay token
+// by token.
+//
+// Bound: 2 K V multiply-adds a token (a third of that more where the time
+// axis is cut), 232 us at 2x16x8192x128; the kernel reaches 0.36 of that rate
+// there, with twelve warps a SM (160 registers a thread) that do not hide
+// all of the latency of a token's reads and sums.
 #include "decay_attn.cuh"
 
 #include <algorithm>
@@ -23,9 +31,9 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kRows = 64;
-constexpr int kStage = 16;   // tokens staged at a time
+constexpr int kStage = 8;    // tokens staged at a time
 constexpr int kGroup = 8;    // tokens between rescalings
-constexpr int kUnit = kStage;   // tokens a unit of the split
+constexpr int kUnit = 16;    // tokens a unit of the split
 
 struct Args {
     Pass p;
@@ -36,14 +44,14 @@ struct Args {
 
 template <int K, bool STATE_ONLY>
 __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
-    constexpr int M = K / 16;
+    constexpr int M = K / 32, R = 4;   // 32s of columns, rows a thread
     __shared__ __align__(16) float ks[kStage][K], qs[STATE_ONLY ? 1 : kStage][K];
-    __shared__ __align__(8) float vs[kStage][kRows];
+    __shared__ __align__(16) float vs[kStage][kRows];
     __shared__ Pow pows[kGroup + 1];     // a^n
     __shared__ float2 updown[kGroup];   // a^-x and a^x after a group's n-th token
     const Pass &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int pc = lane & 3, row = warp * 16 + (lane >> 2) * 2, row0 = blockIdx.x * kRows;
+    const int pc = lane & 7, row = warp * 16 + (lane >> 3) * R, row0 = blockIdx.x * kRows;
     const int g = blockIdx.y + gridDim.y * blockIdx.z;
     if (g >= a.s.G) return;
     int lo = a.s.lo(g);
@@ -92,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
                 if (t < tend) load4(v + r, rv[n]);
             }
         };
-        float2 S[2][M][2];
+        float2 S[R][M][2];
         {
             const size_t sb = (size_t)p.K * p.V;
             const float *src = nullptr;
@@ -105,11 +113,11 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
                 tr = p.S0.transposed;
             }
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
                     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    const int c = 16 * m + 4 * pc, i = row0 + row + r;
+                    const int c = 32 * m + 4 * pc, i = row0 + row + r;
                     if (src && !tr) load4(src + (size_t)i * K + c, x);
                     if (src && tr) {
 #pragma unroll
@@ -122,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
         auto scale = [&](Pow f) {
             const float2 h = make_float2(f.hi, f.hi), l = make_float2(f.lo, f.lo);
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -155,37 +163,45 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
                 const int in = tt & (kGroup - 1);
                 const float up = updown[in].x, down = updown[in].y;
                 if (!grouped && !p.rev) scale(pows[1]);
-                const float2 vv = *reinterpret_cast<const float2 *>(&vs[tt][row]);
-                const float2 w0 = make_float2(up * vv.x, up * vv.x), w1 = make_float2(up * vv.y, up * vv.y);
-                float2 o0 = make_float2(0.0f, 0.0f), o1 = o0, o2 = o0, o3 = o0;
+                float2 w[R], dot[R];
+                {
+                    float vv[R];
+                    load4(&vs[tt][row], vv);
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        w[r] = make_float2(up * vv[r], up * vv[r]);
+                        dot[r] = make_float2(0.0f, 0.0f);
+                    }
+                }
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
-                    const float4 kk = *reinterpret_cast<const float4 *>(&ks[tt][16 * m + 4 * pc]);
+                    const float4 kk = *reinterpret_cast<const float4 *>(&ks[tt][32 * m + 4 * pc]);
                     const float2 ka = make_float2(kk.x, kk.y), kc = make_float2(kk.z, kk.w);
-                    S[0][m][0] = __ffma2_rn(w0, ka, S[0][m][0]);
-                    S[0][m][1] = __ffma2_rn(w0, kc, S[0][m][1]);
-                    S[1][m][0] = __ffma2_rn(w1, ka, S[1][m][0]);
-                    S[1][m][1] = __ffma2_rn(w1, kc, S[1][m][1]);
+                    float2 qa, qc;
                     if (!STATE_ONLY) {
-                        const float4 qq = *reinterpret_cast<const float4 *>(&qs[tt][16 * m + 4 * pc]);
-                        const float2 qa = make_float2(qq.x, qq.y), qc = make_float2(qq.z, qq.w);
-                        o0 = __ffma2_rn(S[0][m][0], qa, o0);
-                        o1 = __ffma2_rn(S[0][m][1], qc, o1);
-                        o2 = __ffma2_rn(S[1][m][0], qa, o2);
-                        o3 = __ffma2_rn(S[1][m][1], qc, o3);
+                        const float4 qq = *reinterpret_cast<const float4 *>(&qs[tt][32 * m + 4 * pc]);
+                        qa = make_float2(qq.x, qq.y);
+                        qc = make_float2(qq.z, qq.w);
+                    }
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        S[r][m][0] = __ffma2_rn(w[r], ka, S[r][m][0]);
+                        S[r][m][1] = __ffma2_rn(w[r], kc, S[r][m][1]);
+                        if (!STATE_ONLY) dot[r] = __ffma2_rn(S[r][m][1], qc, __ffma2_rn(S[r][m][0], qa, dot[r]));
                     }
                 }
                 if (!STATE_ONLY) {
-                    float s0 = (o0.x + o0.y) + (o1.x + o1.y), s1 = (o2.x + o2.y) + (o3.x + o3.y);
-                    s0 += __shfl_xor_sync(kFullMask, s0, 1);
-                    s1 += __shfl_xor_sync(kFullMask, s1, 1);
-                    s0 += __shfl_xor_sync(kFullMask, s0, 2);
-                    s1 += __shfl_xor_sync(kFullMask, s1, 2);
+                    // four sums over eight lanes: each exchange halves the rows a lane still carries
+                    float s[R];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) s[r] = dot[r].x + dot[r].y;
+                    const bool b0 = pc & 1, b1 = pc & 2;
+                    float s0 = (b0 ? s[2] : s[0]) + __shfl_xor_sync(kFullMask, b0 ? s[0] : s[2], 1);
+                    float s1 = (b0 ? s[3] : s[1]) + __shfl_xor_sync(kFullMask, b0 ? s[1] : s[3], 1);
+                    s0 = (b1 ? s1 : s0) + __shfl_xor_sync(kFullMask, b1 ? s0 : s1, 2);
+                    s0 += __shfl_xor_sync(kFullMask, s0, 4);
                     const int t = t0 + tt;
-                    if (pc == 0) {
-                        const float y[2] = {down * s0, down * s1};
-                        store2(o + vb + (size_t)(p.rev ? p.T - 1 - t : t) * p.V + row, y);
-                    }
+                    if (pc < 4) o[vb + (size_t)(p.rev ? p.T - 1 - t : t) * p.V + row + 2 * (pc & 1) + (pc >> 1)] = down * s0;
                 }
                 if (!grouped && p.rev) scale(pows[1]);
                 if (grouped && (in == kGroup - 1 || tt == tn - 1)) scale(pows[in + 1]);
@@ -200,10 +216,10 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
         }
         if (dst) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int m = 0; m < M; ++m) {
-                    const int c = 16 * m + 4 * pc, i = row0 + row + r;
+                    const int c = 32 * m + 4 * pc, i = row0 + row + r;
                     const float x[4] = {S[r][m][0].x, S[r][m][0].y, S[r][m][1].x, S[r][m][1].y};
                     store4(dst + (size_t)i * K + c, x);
                 }
