@@ -71,8 +71,9 @@
  *  first call (osdn_workspace_init does that on a stream); the status word is
  *  sticky until the caller zeroes it again.  The header's second word is a
  *  test word: while it is nonzero, the bf16 osdn_chunk_fwd's state recurrence
- *  loads nothing and shortens its bounded waits, so that they run out and the
- *  status word reads OSDN_ERR_TIMEOUT -- the way the timeout path is
+ *  and the bf16 osdn_decay_attn and its gradients load nothing and shorten
+ *  their bounded waits, so that they run out and the status word reads
+ *  OSDN_ERR_TIMEOUT -- the way the timeout path is
  *  exercised without a fault.  Keep it zero otherwise.
  */
 #ifndef OSDN_H
@@ -460,8 +461,12 @@ size_t osdn_decay_attn_workspace_bytes(int io, int B, int H, int T, int K, int V
  *   ST    out [B][H][V][K] fp32, or NULL (not written)
  * The state layout is that of osdn_chunk_fwd.  Inputs must be finite: inside
  * a block of tokens a later token's infinity or NaN can reach earlier rows.
+ * io == OSDN_BF16 runs on the tensor cores in chunks of 128 tokens, the state
+ * with fp32 accuracy; io == OSDN_F32 runs in fp32 FFMA.  With few sequences
+ * the time axis is cut into ranges that run side by side (K and V are then
+ * read twice).
  * With T == 0 the call writes ST = S0 and nothing else.  T may be at most
- * 1,073,741,760.  Outputs must not overlap inputs, each other or the
+ * 1,073,741,760 and B*H*ceil(T/16) below 2^31.  Outputs must not overlap inputs, each other or the
  * workspace (OSDN_ERR_ALIAS).  Results are the same on every run.
  */
 int osdn_decay_attn(int io, int B, int H, int T, int K, int V, const void *q, const void *k,

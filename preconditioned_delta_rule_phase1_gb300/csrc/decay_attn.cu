@@ -18,8 +18,9 @@
 //
 // Bound: 2 K V multiply-adds a token (a third of that more where the time
 // axis is cut), 232 us at 2x16x8192x128; the kernel reaches 0.36 of that rate
-// there, with twelve warps a SM (160 registers a thread) that do not hide
-// all of the latency of a token's reads and sums.
+// there.  Twelve warps a SM (160 registers a thread) issue in 0.54 of the
+// slots, half of them multiply-adds: the rest is reads, sums over lanes and
+// their latency.
 #include "decay_attn.cuh"
 
 #include <algorithm>

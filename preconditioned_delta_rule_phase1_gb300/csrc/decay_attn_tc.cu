@@ -13,36 +13,46 @@
 // is an output and is carried over thousands of tokens, so it is kept in
 // fp32 (in registers), and K^ enters the product as three bf16 parts
 // (8 + 8 + 8 bits, exactly the fp32 product a^e k): V is exact in bf16, so
-// the update has fp32 accuracy.  Where the state is not an output two parts
-// do.  Powers of the decay come from repeated
-// squaring in two fp32 (decay_attn.cuh).
-//
-// Bound.  Q, K, V in and O out are 128 KB a chunk at K = V = 128, 2.9 us at
-// an SM's share of HBM; the six 128^3 products take about 1.6 us of the
-// tensor pipe.  So the kernel is HBM-bound if everything overlaps, and the
-// chain of chunks needs few steps: only the register update of S and the
-// product Q S^T wait for the chunk before.
+// the update has fp32 accuracy (S_T within 4e-7 of 64 bits; a plain bf16 K^
+// would leave 2e-3).  Where the state is not an output two parts do.  The
+// chunk's decay a^L, which a state meets hundreds of times, comes from
+// repeated squaring in two fp32 (decay_attn.cuh).
 //
 // Time axis.  Every CTA takes a range of the chunks of all sequences (one
 // CTA a SM, nearly equal ranges).  A range that starts inside a sequence
 // needs the state there: a first launch (STATE_ONLY: K, V and the state
 // update alone) forms each range's addition to the state, chain_states joins
-// them, the second launch does the work.  That reads K and V once more, so
-// ranges that hold whole sequences are preferred where they fill the GPU.
+// them, the second launch does the work.  That reads K and V once more (1.5
+// times the unsplit bytes), so ranges that hold whole sequences are preferred
+// where they fill the GPU.  The launches overlap: the second one's CTAs start
+// as the first one's leave and form K^, Q K^T and P before they need a state
+// (8x8x2048x128 75 -> 63 us with the cheaper numbering of ranges).
 //
 // Roles (15 warps): 0 TMA; 1 MMA issue for the outputs; 2-5 P out of TMEM,
-// weighted, back as a TMEM operand, and O, turned in shared memory so that
-// whole rows are stored; 6-13 the state: K^ in two steps of 64 tokens, each multiplied while
-// the next is formed, and, behind the first step of the chunk after it, the
-// update of S; 14 MMA issue for the state.
-// Buffers are single (224 KB hold one chunk's K, V, Q, S and three parts of
-// K^): the next chunk's tiles wait in L2, brought there a chunk ahead, and
-// are loaded as their places fall free, K by halves.
-// STATE_ONLY takes its chunks last to first with weights up to the range's
-// end, so that they add up in TMEM, four at a time; it also leaves in L2 what
-// the second launch reads first.  The roles' loops are kept short
-// (little unrolling): each runs once a chunk, and unrolled they miss the
-// instruction cache (2x16x8192x128: 124 -> 80 us for the second launch).
+// weighted, back as a TMEM operand, and O out of TMEM to global memory, a
+// row a lane in whole sectors; 6-13 the state: K^ in two steps of 64 tokens
+// (its first part in K's place), each multiplied while the next is formed,
+// then the update of S and its bf16 copy; 14 MMA issue for the state.
+// STATE_ONLY: 16 warps form K^; it takes its chunks last to first with
+// weights up to the range's end, so that they add up in TMEM, four at a time
+// (see kGroup), and leaves in L2 what the second launch reads first.
+// 224 KB hold two tiles of K, one of V and Q, S and two parts of K^; the next
+// V and Q are brought to L2 meanwhile.
+//
+// Bound.  At K = V = 128 a chunk is 128 KB in and out, 2.9 us at an SM's
+// share of HBM; its products take 3100 cycles of the tensor pipe and, as
+// their operands come from shared memory at 128 bytes a cycle, most of the
+// 4700 cycles of shared-memory traffic that a chunk cannot do without (352 KB
+// for the products, 160 KB for forming K^ and S, 96 KB arriving).  A chunk
+// takes about 6000 cycles (3.2 us): the second launch 60 us at 2x16x8192x128,
+// DRAM at 0.54 and the tensor pipe at 0.42 of their peaks, the first 33 us.
+// What was measured on the way there, second launch at 2x16x8192x128: short
+// role loops instead of unrolled ones, which miss the instruction cache, 124
+// -> 80 us; the tile's transposition for whole-row stores of O 78 -> 68 us; K
+// a chunk ahead 68 -> 60 us.  26 warps (16 for the state, 8 for P and O)
+// were slower (108 us), and so were steps of 32 tokens (64 -> 70 us), P V
+// ahead of Q S^T (+4 us for the three launches) and straight-line issue of
+// the state's products (+5 us: they crowd K^'s traffic out).
 // Every wait is bounded: one that runs out records OSDN_ERR_TIMEOUT and all
 // roles leave their loops; no role waits for another in any other way.
 #include <algorithm>
