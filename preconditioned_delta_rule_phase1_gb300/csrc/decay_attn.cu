@@ -231,8 +231,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
 // One thread per four state elements of a sequence: the states entering the
 // sequence's ranges, one after another.  Up to kAhead ranges' states are
 // loaded before the first is used, and the powers between them (thread i's
-// the i-th) come first, so that the chain itself is fused multiply-adds
-//.
+// the i-th) come first, so that the chain itself is fused multiply-adds.
 constexpr int kAhead = 8;
 __global__ void __launch_bounds__(256) chain_states_kernel(Pass p, Split s, float *states) {
     __shared__ Pow pows[kAhead];
