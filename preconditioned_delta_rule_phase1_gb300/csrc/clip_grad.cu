@@ -216,16 +216,18 @@ scale_kernel(const __grid_constant__ Table<N> t, const double *part, int parts, 
 
 constexpr int kTable = 1024;   // 28 KB of the 32 KB that a kernel's parameters may take
 
-// Tensors [at, n) into the table, as many as fit; returns the first left out.
-// A launch numbers its chunks in 32 bits (2^45 elements).
+// Tensors [at, n) into the table, as many as fit; returns the first left out that is not empty
+// (n: none), so that only a call without any element meets an empty table.  A launch numbers its
+// chunks in 32 bits (2^45 elements).
 template <int N>
 int fill(Table<N> &t, int at, int n, const void *const *g, void *const *o, const long long *size,
          const int *io) {
     t.n = 0;
     t.first[0] = 0;
     unsigned long long c = 0;
-    for (; at < n && t.n < N; ++at) {
+    for (; at < n; ++at) {
         if (size[at] == 0) continue;
+        if (t.n == N) break;
         c += (unsigned long long)((size[at] + kChunk - 1) / kChunk);
         t.g[t.n] = g[at];
         t.o[t.n] = o ? o[at] : const_cast<void *>(g[at]);
