@@ -13,8 +13,12 @@
 // 1153 -> 997 us; 1024 sequences of 256 tokens: 802 -> 643 us).
 // The decay costs no multiplication a token: over groups of eight tokens the
 // state is kept as S~ = a^-n S (v is scaled instead) and multiplied by a^8
-// once a group; heads whose a^-8 would grow too large (a < 1/16) decay token
-// by token.
+// once a group, as long as a^-8 <= 2, so that S~ leaves fp32's range only where
+// S is within a factor of 2 of doing so.  Heads that forget faster (a < 0.917,
+// a memory of 12 tokens) decay token by token, which takes a tenth longer
+// (2x16x4096x128: 520 us with a = 0.95, 569 us with 0.9).  Groups of four and
+// two tokens for those between, chosen at run time, would cost the others 6%,
+// and noticing an overflow to do the tokens over 15%.
 //
 // Bound: 2 K V multiply-adds a token (a third of that more where the time
 // axis is cut), 232 us at 2x16x8192x128; the kernel reaches 0.36 of that rate
@@ -34,6 +38,7 @@ constexpr int kThreads = 128;
 constexpr int kRows = 64;
 constexpr int kStage = 8;    // tokens staged at a time
 constexpr int kGroup = 8;    // tokens between rescalings
+constexpr float kGrouped = 0.917005f;   // the least decay with a^-kGroup <= 2
 constexpr int kUnit = 16;    // tokens a unit of the split
 
 struct Args {
@@ -76,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
         at += u1 - u0;
         const float dec = p.decay[seq % p.H];
         if (!decay_ok(dec) && tid == 0) report_status(a.status, OSDN_ERR_DEVICE);
-        const bool grouped = dec >= 0.0625f;
+        const bool grouped = dec >= kGrouped;
         const size_t kb = (size_t)seq * p.T * K, vb = (size_t)seq * p.T * p.V + row0;
         auto fetch = [&](int t0) {   // the stage's tokens, in the pass's direction
 #pragma unroll
@@ -138,6 +143,15 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
                     for (int e = 0; e < 2; ++e)
                         S[r][m][e] = __ffma2_rn(h, S[r][m][e], __fmul2_rn(l, S[r][m][e]));
         };
+        auto forget = [&] {   // one token's decay
+            const float2 h = make_float2(dec, dec);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int m = 0; m < M; ++m)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) S[r][m][e] = __fmul2_rn(h, S[r][m][e]);
+        };
         __syncthreads();   // the last sequence's powers have been read
         if (tid <= kGroup) pows[tid] = decay_pow(dec, tid);
         if (tid < kGroup) {
@@ -163,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
             for (int tt = 0; tt < tn; ++tt) {
                 const int in = tt & (kGroup - 1);
                 const float up = updown[in].x, down = updown[in].y;
-                if (!grouped && !p.rev) scale(pows[1]);
+                if (!grouped && !p.rev) forget();
                 float2 w[R], dot[R];
                 {
                     float vv[R];
@@ -204,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 3) attend_simt_kernel(Args a) {
                     const int t = t0 + tt;
                     if (pc < 4) o[vb + (size_t)(p.rev ? p.T - 1 - t : t) * p.V + row + 2 * (pc & 1) + (pc >> 1)] = down * s0;
                 }
-                if (!grouped && p.rev) scale(pows[1]);
+                if (!grouped && p.rev) forget();
                 if (grouped && (in == kGroup - 1 || tt == tn - 1)) scale(pows[in + 1]);
             }
         }

@@ -1,0 +1,63 @@
+"""Linear attention with a decay per head where one head's, one row's or one
+operand's size would hide another's: each head against its own size, values
+whose scaled forms leave fp32, scores that overflow where the mask hides them.
+
+Tolerances, normwise over the part that is compared.  fp32: 2e-5, as for whole
+tensors (sums of a few hundred products).  bf16: the score, the copy of the
+state and the output each round by up to 2^-9 of their own terms, which sum to
+the output with mixed signs: 3 * 2^-9 = 6e-3, and 1e-2 with the terms that sum
+to a little more.  The fp32 states: 2e-5 in both.
+"""
+import itertools
+
+import pytest
+import torch
+
+from preconditioned_delta_rule_phase1_gb300 import build as osdn_build
+from preconditioned_delta_rule_phase1_gb300 import ops
+from tests._util import rel_err
+from tests.test_decay_attn_gpu import STATE_TOL, TOL, autograd, backward, forward, inputs, recurrence
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    osdn_build.build()
+    ops.lib()
+
+
+def each_head(got, ref, tol, what, rows=(0,)):
+    """Every head by itself, over all tokens and over those from each of `rows` on (the
+    first tokens' share of S0 would set the scale of a head that forgets at once)."""
+    for h, t in itertools.product(range(ref.shape[1]), rows):
+        if ref.dim() == 4 and t < ref.shape[2]:
+            assert rel_err(got[:, h, t:], ref[:, h, t:].cpu()) < tol, (what, h, t)
+
+
+LARGE = {"v": 1e33, "k": 1e33, "q": 1e35, "S0": 1e35, "do": 1e33, "dST": 1e35, "one token": 1e33}
+
+
+@pytest.mark.parametrize("what", sorted(LARGE))
+@pytest.mark.parametrize("B,H,T", [(2, 4, 150), (1, 4, 700)])
+def test_large_values_in_fp32(what, B, H, T):
+    # the recurrence is finite, so no scaled form of it may leave fp32's range
+    x = inputs(B, H, T, 64, 128, "f32", seed=T, decay=torch.tensor([0.07, 0.3, 0.9, 0.999]))
+    if what == "one token":
+        x["v"][:, :, T // 2] *= LARGE[what]
+    else:
+        x[what] *= LARGE[what]
+    if what in ("do", "dST"):
+        x["S0"] *= 0.0
+    else:
+        o, ST = forward(x)
+        ro, rS = recurrence(x["q"], x["k"], x["v"], x["decay"], x["S0"])
+        each_head(o, ro, TOL["f32"], "o", rows=(0, T // 2))
+        each_head(ST, rS, STATE_TOL, "ST")
+        x["dST"] *= 0.0
+    got, ref = backward(x), autograd(x)
+    for n in ("q", "k", "v"):
+        each_head(got[n], ref[n], TOL["f32"], n)
+    each_head(got["S0"], ref["S0"], STATE_TOL, "S0")
