@@ -459,8 +459,10 @@ size_t osdn_decay_attn_workspace_bytes(int io, int B, int H, int T, int K, int V
  *   S0    in  [B][H][V][K] fp32, or NULL (zeros)
  *   o     out [B][H][T][V] io
  *   ST    out [B][H][V][K] fp32, or NULL (not written)
- * The state layout is that of osdn_chunk_fwd.  Inputs must be finite: inside
- * a block of tokens a later token's infinity or NaN can reach earlier rows.
+ * The state layout is that of osdn_chunk_fwd.  Inputs must be finite: with
+ * bf16 I/O, inside a block of 128 tokens, a later token's infinity or NaN in
+ * v can reach earlier rows.  A score q_t . k_s that overflows where s > t is
+ * never read.
  * io == OSDN_BF16 runs on the tensor cores in chunks of 128 tokens, the state
  * with fp32 accuracy; io == OSDN_F32 runs in fp32 FFMA.  With few sequences
  * the time axis is cut into ranges that run side by side (K and V are then

@@ -356,10 +356,11 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int r = 32 * q4 + lane;   // row of the chunk
             // Key block b (32 columns) against the row's own block, d blocks away: the weight of
             // column m is far[d-1] col[m], far from the row to the near end of the block and col
-            // from there on; on the diagonal it is a^gap, read from the same table, which holds
-            // zeros where the gap is negative.
+            // from there on; on the diagonal it is a^gap, read from the same table.  Scores that the
+            // mask hides are put to zero, not multiplied by it: they may have overflowed.
             float *col = s_pow[warp - 2] + 32;
             const float *diag = col + (p.rev ? -lane : 31 - lane);
+            const uint32_t seen = p.rev ? kFullMask << lane : kFullMask >> (31 - lane);   // columns of the diagonal block
             const bool wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
             float wq = 0.0f, far[3] = {0.0f, 0.0f, 0.0f};
             int have = -1;
@@ -393,6 +394,8 @@ attend_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         float x[32];
                         tc::tmem_ld32(tmem + lane_off + kColP + 32 * b, x);
                         if (d == 0) {
+#pragma unroll
+                            for (int m = 0; m < 32; ++m) x[m] = seen >> m & 1 ? x[m] : 0.0f;
 #pragma unroll
                             for (int m = 0; m < 16; ++m)
                                 pk[m] = __uint_as_float(tc::pack_bf16x2(x[2 * m] * diag[2 * m], x[2 * m + 1] * diag[2 * m + 1]));

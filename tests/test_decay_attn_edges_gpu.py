@@ -61,3 +61,21 @@ def test_large_values_in_fp32(what, B, H, T):
     for n in ("q", "k", "v"):
         each_head(got[n], ref[n], TOL["f32"], n)
     each_head(got["S0"], ref["S0"], STATE_TOL, "S0")
+
+
+@pytest.mark.parametrize("T", [100, 300, 2100])
+def test_scores_that_overflow_behind_the_mask(T):
+    # early queries times late keys exceed fp32, but no token reads a later key
+    at = 71
+    x = inputs(1, 3, T, 128, 64, "bf16", seed=T, decay=torch.tensor([0.9, 0.99, 1.0]))
+    x["q"][:, :, :at] *= 1e25
+    x["k"][:, :, at:] *= 1e25
+    o, ST = forward(x)
+    ro, rS = recurrence(x["q"], x["k"], x["v"], x["decay"], x["S0"])
+    got, ref = backward(x), autograd(x)
+    for part in (slice(0, at), slice(at, T)):
+        each_head(o[:, :, part], ro[:, :, part], TOL["bf16"], ("o", part))
+        for n in ("q", "k", "v"):
+            each_head(got[n][:, :, part], ref[n][:, :, part], TOL["bf16"], (n, part))
+    each_head(ST, rS, STATE_TOL, "ST")
+    each_head(got["S0"], ref["S0"], STATE_TOL, "S0")
