@@ -10,12 +10,19 @@ the binding checks them (every tensor's shape, dtype and device against the
 call's layout) before any pointer leaves Python, and runs the call with the
 tensors' device current and, by default, on its current stream.  A tensor
 of the wrong type would otherwise be read or written out of its bounds.
+
+Every call takes ``stream`` (None: torch's current stream).  A call with a
+stream is the call under ``torch.cuda.stream(stream)``: its kernels run there
+and what it allocates belongs to that stream.  As with any tensor, the caller
+orders the inputs, and a workspace used on several streams, with it.
 """
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import functools
+import inspect
 import operator
 import os
 import threading
@@ -138,8 +145,35 @@ def _ptr(t):
 
 
 def _stream(stream, device=None):
+    _same_device(stream, device)
     s = torch.cuda.current_stream(device) if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _same_device(stream, device):
+    if stream is not None and device is not None and stream.device != device:
+        raise ValueError("stream is on %s; the call runs on %s" % (stream.device, device))
+
+
+def _current(stream):
+    """The context in which `stream` (None: no change) is torch's current stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _on_stream(fn):
+    """`fn` with ``stream=s`` as if called under ``torch.cuda.stream(s)``: what it allocates (its
+    outputs, a workspace of its own or a grown one) belongs to that stream too, so that nothing is
+    filled, or handed on to another tensor, on a stream that the kernels are not ordered with."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        with _current(stream):
+            return fn(*args, **kw)
+    return call
 
 
 F32 = torch.float32
@@ -190,12 +224,16 @@ class Workspace:
         self.ensure(max(nbytes, STATUS_BYTES), stream)
 
     def ensure(self, nbytes: int, stream=None):
+        """At least `nbytes` bytes, allocated and zeroed on `stream` (None: the current one)."""
         if self.buf.numel() < nbytes:
             old = self.buf
-            self.buf = torch.zeros(((nbytes + 255) // 256) * 256, dtype=torch.uint8,
-                                   device=self.device)
-            if old.numel() >= STATUS_BYTES:  # keep a sticky status already raised
-                self.buf[:STATUS_BYTES].copy_(old[:STATUS_BYTES])
+            with _current(stream):
+                self.buf = torch.zeros(((nbytes + 255) // 256) * 256, dtype=torch.uint8,
+                                       device=self.device)
+                if old.numel() >= STATUS_BYTES:  # keep a sticky status already raised
+                    self.buf[:STATUS_BYTES].copy_(old[:STATUS_BYTES])
+                    if old.is_cuda:  # it may belong to another stream, and is in use on this one
+                        old.record_stream(torch.cuda.current_stream(old.device))
         return self
 
     @property
@@ -233,6 +271,7 @@ def backward_kda_workspace_bytes(B, H, T, K, V) -> int:
     return int(lib().osdn_backward_kda_workspace_bytes(B, H, T, K, V))
 
 
+@_on_stream
 def precond_scan(k, beta, r=None, eta=0.1, d0=None, ktilde=None, dT=None, workspace=None,
                  stream=None, log_ratio=None):
     """Phase 1 (osdn_precond_scan): returns (ktilde, dT).
@@ -274,6 +313,7 @@ def precond_scan(k, beta, r=None, eta=0.1, d0=None, ktilde=None, dT=None, worksp
     return ktilde, dT, log_ratio
 
 
+@_on_stream
 def precond_scan_noalloc(k, beta, r=None, eta=0.1, d0=None, ktilde=None, dT=None, stream=None):
     """Phase 1 through osdn_precond_scan_noalloc: no workspace, no device
     allocation inside the call (outputs are allocated here only when not given)."""
@@ -296,6 +336,7 @@ def precond_scan_noalloc(k, beta, r=None, eta=0.1, d0=None, ktilde=None, dT=None
     return ktilde, dT
 
 
+@_on_stream
 def chunk_fwd(q, k, ktilde, v, beta, alpha=None, S0=None, o=None, ST=None, workspace=None,
               stream=None):
     """Phase 2 (osdn_chunk_fwd): returns (o, ST)."""
@@ -324,6 +365,7 @@ def chunk_fwd(q, k, ktilde, v, beta, alpha=None, S0=None, o=None, ST=None, works
     return o, ST
 
 
+@_on_stream
 def forward(q, k, v, beta, r=None, eta=0.1, d0=None, alpha=None, S0=None, workspace=None,
             stream=None):
     """Both phases: returns (ktilde, dT, o, ST)."""
@@ -333,6 +375,7 @@ def forward(q, k, v, beta, r=None, eta=0.1, d0=None, alpha=None, S0=None, worksp
     return ktilde, dT, o, ST
 
 
+@_on_stream
 def forward_fused(q, k, v, beta, r=None, eta=0.1, d0=None, alpha=None, S0=None, o=None, dT=None,
                   ST=None, workspace=None, stream=None):
     """Both phases in one call (osdn_forward), ktilde kept off global memory
@@ -366,6 +409,7 @@ def forward_fused(q, k, v, beta, r=None, eta=0.1, d0=None, alpha=None, S0=None, 
     return dT, o, ST
 
 
+@_on_stream
 def decode_step(q, k, v, beta, d, S, r=None, eta=0.1, alpha=None, o=None, ktilde=None,
                 workspace=None, stream=None):
     """One recurrent step (osdn_decode_step): updates d [B,H,K] and S [B,H,V,K]
@@ -374,6 +418,7 @@ def decode_step(q, k, v, beta, d, S, r=None, eta=0.1, alpha=None, o=None, ktilde
     return _decode(False, q, k, v, beta, d, S, r, eta, alpha, o, ktilde, workspace, stream)
 
 
+@_on_stream
 def decode_step_kda(q, k, v, beta, d, S, r=None, eta=0.1, alpha_k=None, o=None, ktilde=None,
                     workspace=None, stream=None):
     """One recurrent step with a decay per key channel (osdn_decode_step_kda):
@@ -408,6 +453,7 @@ def _decode(per_channel, q, k, v, beta, d, S, r, eta, alpha, o, ktilde, workspac
     return o, ktilde
 
 
+@_on_stream
 def backward(q, k, ktilde, v, beta, r=None, eta=0.1, d0=None, alpha=None, S0=None, *, do=None,
              dST=None, ddT=None, dktilde=None, workspace=None, stream=None):
     """Gradients of both phases (osdn_backward).
@@ -422,6 +468,7 @@ def backward(q, k, ktilde, v, beta, r=None, eta=0.1, d0=None, alpha=None, S0=Non
                      workspace, stream)
 
 
+@_on_stream
 def backward_kda(q, k, ktilde, v, beta, r=None, eta=0.1, d0=None, alpha_k=None, S0=None, *,
                  do=None, dST=None, ddT=None, dktilde=None, workspace=None, stream=None):
     """Gradients of both phases with a decay per key channel
@@ -473,6 +520,7 @@ def _backward(per_channel, q, k, ktilde, v, beta, r, eta, d0, alpha, S0, do, dST
     return g
 
 
+@_on_stream
 def chunk_fwd_kda(q, k, ktilde, v, beta, alpha_k=None, S0=None, o=None, ST=None, workspace=None,
                   stream=None):
     """Phase 2 with a decay per key channel (osdn_chunk_fwd_kda), alpha_k
@@ -502,6 +550,7 @@ def chunk_fwd_kda(q, k, ktilde, v, beta, alpha_k=None, S0=None, o=None, ST=None,
     return o, ST
 
 
+@_on_stream
 def forward_kda(q, k, v, beta, r=None, eta=0.1, d0=None, alpha_k=None, S0=None, workspace=None,
                 stream=None):
     """Both phases with a decay per key channel in Phase 2: returns
@@ -536,6 +585,7 @@ def _run(name, device, stream, args, workspace=None, nbytes=0):
     """Call `name` with `args`, then the workspace (if given) and the stream, on `device`."""
     if device.type != "cuda":
         raise ValueError("OSDN operates on CUDA tensors only")
+    _same_device(stream, device)
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
             return _run(name, device, stream, args, workspace, nbytes)
@@ -570,6 +620,7 @@ def clip_grad_norm_workspace_bytes(n) -> int:
     return _bytes("osdn_clip_grad_norm_workspace_bytes", n)
 
 
+@_on_stream
 def decay_attn(q, k, v, decay, S0=None, o=None, ST=None, workspace=None, stream=None):
     """Linear attention with a decay per head (osdn_decay_attn), q, k [B,H,T,K],
     v [B,H,T,V] (io), decay [H] fp32 in [0, 1], S0 [B,H,V,K] fp32 or None:
@@ -591,6 +642,7 @@ def decay_attn(q, k, v, decay, S0=None, o=None, ST=None, workspace=None, stream=
     return o, ST
 
 
+@_on_stream
 def decay_attn_step(q, k, v, decay, S, o=None, workspace=None, stream=None):
     """One token of ``decay_attn`` (osdn_decay_attn_step): updates S [B,H,V,K]
     (fp32) in place for the token q, k [B,H,K], v [B,H,V] (io); returns o."""
@@ -607,6 +659,7 @@ def decay_attn_step(q, k, v, decay, S, o=None, workspace=None, stream=None):
     return o
 
 
+@_on_stream
 def decay_attn_backward(q, k, v, decay, S0=None, *, do, dST=None, workspace=None, stream=None):
     """Gradients through ``decay_attn`` (osdn_decay_attn_backward) given the
     cotangents do [B,H,T,V] (io) of o and dST [B,H,V,K] fp32 of ST (None: zero).
@@ -652,6 +705,7 @@ def _act(act):
     return ACTS[act]
 
 
+@_on_stream
 def group_norm(x, weight=None, bias=None, gate=None, groups=None, act="none", eps=1e-5, y=None,
                stream=None):
     """Group norm of every token with an activation (osdn_group_norm).
@@ -672,6 +726,7 @@ def group_norm(x, weight=None, bias=None, gate=None, groups=None, act="none", ep
     return y
 
 
+@_on_stream
 def group_norm_backward(x, dy, weight=None, bias=None, gate=None, groups=None, act="none",
                         eps=1e-5, workspace=None, stream=None):
     """Gradients of ``group_norm`` (osdn_group_norm_backward) given dy [B,T,C]:
@@ -709,6 +764,7 @@ def _tensor_table(what, tensors, dev):
             array.array("q", map(torch.Tensor.numel, tensors)), ios)
 
 
+@_on_stream
 def clip_grad_norm(grads, max_norm, outs=None, norm=None, workspace=None, stream=None):
     """Clip tensors by their global 2-norm (osdn_clip_grad_norm): every g becomes
     g min(1, max_norm / norm), in place, or in `outs` (as many elements of the
@@ -742,6 +798,7 @@ def clip_grad_norm(grads, max_norm, outs=None, norm=None, workspace=None, stream
     return norm
 
 
+@_on_stream
 def grad_norm(grads, norm=None, workspace=None, stream=None):
     """The global 2-norm of the tensors, [1] fp32 on the device."""
     return clip_grad_norm(grads, float("inf"), norm=norm, workspace=workspace, stream=stream)
