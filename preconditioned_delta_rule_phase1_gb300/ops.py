@@ -581,17 +581,20 @@ def _arg(name, t, shape, dtype, device):
     raise ValueError("%s does not fit the call" % name)
 
 
-def _run(name, device, stream, args, workspace=None, nbytes=0):
-    """Call `name` with `args`, then the workspace (if given) and the stream, on `device`."""
+def _run(name, device, stream, args, workspace=None, size=None):
+    """Call `name` with `args`, then the workspace (if given) and the stream, on `device`.
+    `size`: the C call, and its arguments, that says how large the workspace has to be."""
     if device.type != "cuda":
         raise ValueError("OSDN operates on CUDA tensors only")
     _same_device(stream, device)
     if device.index != torch.cuda.current_device():
         with torch.cuda.device(device):
-            return _run(name, device, stream, args, workspace, nbytes)
+            return _run(name, device, stream, args, workspace, size)
     if workspace is not None:
-        if workspace.buf.numel() < nbytes:
-            workspace.ensure(nbytes)
+        if size is not None:
+            nbytes = _bytes(device.index, *size)
+            if workspace.buf.numel() < nbytes:
+                workspace.ensure(nbytes)
         args += (workspace.buf.data_ptr(), workspace.buf.numel())
     s = torch.cuda.current_stream(device) if stream is None else stream
     code = getattr(_lib or lib(), name)(*args, s.cuda_stream)
@@ -600,24 +603,26 @@ def _run(name, device, stream, args, workspace=None, nbytes=0):
 
 
 @functools.lru_cache(maxsize=1024)
-def _bytes(name, *shape) -> int:
+def _bytes(device, name, *shape) -> int:
+    """What `name` answers on the device numbered `device`, the current one: it may depend on its
+    number of SMs."""
     return int(getattr(lib(), name)(*shape))
 
 
 def decay_attn_workspace_bytes(io, B, H, T, K, V) -> int:
-    return _bytes("osdn_decay_attn_workspace_bytes", io, B, H, T, K, V)
+    return int(lib().osdn_decay_attn_workspace_bytes(io, B, H, T, K, V))
 
 
 def decay_attn_backward_workspace_bytes(io, B, H, T, K, V) -> int:
-    return _bytes("osdn_decay_attn_backward_workspace_bytes", io, B, H, T, K, V)
+    return int(lib().osdn_decay_attn_backward_workspace_bytes(io, B, H, T, K, V))
 
 
 def group_norm_backward_workspace_bytes(B, G, T, D) -> int:
-    return _bytes("osdn_group_norm_backward_workspace_bytes", B, G, T, D)
+    return int(lib().osdn_group_norm_backward_workspace_bytes(B, G, T, D))
 
 
 def clip_grad_norm_workspace_bytes(n) -> int:
-    return _bytes("osdn_clip_grad_norm_workspace_bytes", n)
+    return int(lib().osdn_clip_grad_norm_workspace_bytes(n))
 
 
 @_on_stream
@@ -638,7 +643,7 @@ def decay_attn(q, k, v, decay, S0=None, o=None, ST=None, workspace=None, stream=
             _arg("v", v, vo, dt, dev), _arg("decay", decay, (H,), F32, dev),
             _arg("S0", S0, st, F32, dev), _arg("o", o, vo, dt, dev), _arg("ST", ST, st, F32, dev))
     _run("osdn_decay_attn", dev, stream, args, _workspace(workspace, dev),
-         decay_attn_workspace_bytes(io, B, H, T, K, V))
+         ("osdn_decay_attn_workspace_bytes", io, B, H, T, K, V))
     return o, ST
 
 
@@ -679,7 +684,7 @@ def decay_attn_backward(q, k, v, decay, S0=None, *, do, dST=None, workspace=None
     args += (g["q"].data_ptr(), g["k"].data_ptr(), g["v"].data_ptr(),
              None if S0 is None else g["S0"].data_ptr())
     _run("osdn_decay_attn_backward", dev, stream, args, _workspace(workspace, dev),
-         decay_attn_backward_workspace_bytes(io, B, H, T, K, V))
+         ("osdn_decay_attn_backward_workspace_bytes", io, B, H, T, K, V))
     return g
 
 
@@ -744,7 +749,7 @@ def group_norm_backward(x, dy, weight=None, bias=None, gate=None, groups=None, a
     at = lambda name: g[name].data_ptr() if name in g else None  # noqa: E731
     args += (at("x"), at("gate"), at("weight"), at("bias"))
     _run("osdn_group_norm_backward", dev, stream, args, _workspace(workspace, dev),
-         group_norm_backward_workspace_bytes(B, G, T, D))
+         ("osdn_group_norm_backward_workspace_bytes", B, G, T, D))
     return g
 
 
@@ -794,7 +799,7 @@ def clip_grad_norm(grads, max_norm, outs=None, norm=None, workspace=None, stream
     args = (n, at(gp), None if outs is None else at(op), at(sizes), at(ios), float(max_norm),
             _arg("norm", norm, (1,), F32, dev))
     _run("osdn_clip_grad_norm", dev, stream, args, _workspace(workspace, dev),
-         clip_grad_norm_workspace_bytes(n))
+         ("osdn_clip_grad_norm_workspace_bytes", n))
     return norm
 
 
