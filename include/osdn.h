@@ -552,9 +552,8 @@ int osdn_group_norm_backward(int io, int B, int G, int T, int D, int heads_first
  *          max_norm)
  *   max_norm >= 0; infinity computes the norm alone (in place)
  *   norm   out [1] fp32 on the device, or NULL
- * A written tensor must not overlap any other tensor of the call; the call
- * itself checks each outs[i] against its own grads[i], norm and the
- * workspace.  An infinity or NaN in any gradient makes the norm infinite or
+ * A written tensor must not overlap any other tensor of the call, norm or the
+ * workspace (OSDN_ERR_ALIAS); tensors that are only read may.  An infinity or NaN in any gradient makes the norm infinite or
  * NaN, and the scale 0 or NaN, as the formula says (0 times infinity is
  * NaN).  The pointer arrays are read before the call returns.
  */

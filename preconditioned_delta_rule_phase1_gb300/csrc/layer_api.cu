@@ -1,6 +1,7 @@
 // layer_api.cu -- the extern "C" boundary of the decayed linear-attention
 // layer (include/osdn.h): attention over prompts, its single-token step and
 // its gradients, the group norm behind it, and gradient clipping.
+#include <algorithm>
 #include <cmath>
 #include <stdint.h>
 
@@ -75,6 +76,41 @@ int check_bufs(const Buf (&b)[N]) {
             if (x < y + b[j].n && y < x + b[i].n) return OSDN_ERR_ALIAS;
         }
     return OSDN_OK;
+}
+
+// An address range, and whether the call writes it; in a sorted list `any`
+// and `written` are the furthest ends up to there of all and of written ones.
+struct Span {
+    uintptr_t lo, any, written;
+};
+// True if, of the spans at(0) .. at(n - 1) (empty ones: lo == any; read ones:
+// written == 0), a written one overlaps another.  The library allocates no
+// host memory, so they are sorted kSpans at a time on the stack, and the later
+// ones looked up in each such list.
+constexpr long long kSpans = 1024;
+template <typename At>
+bool overlap(long long n, const At &at) {
+    Span s[kSpans];
+    for (long long from = 0; from < n; from += kSpans) {
+        const long long to = std::min(n, from + kSpans);
+        int m = 0;
+        for (long long i = from; i < to; ++i) {
+            s[m] = at(i);
+            m += s[m].lo != s[m].any;
+        }
+        std::sort(s, s + m, [](const Span &a, const Span &b) { return a.lo < b.lo; });
+        for (int i = 1; i < m; ++i) {
+            if (s[i].lo < (s[i].written ? s[i - 1].any : s[i - 1].written)) return true;
+            s[i].any = std::max(s[i].any, s[i - 1].any);
+            s[i].written = std::max(s[i].written, s[i - 1].written);
+        }
+        for (long long i = to; i < n; ++i) {
+            const Span x = at(i);
+            const int before = (int)(std::lower_bound(s, s + m, x.any, [](const Span &a, uintptr_t end) { return a.lo < end; }) - s);
+            if (x.lo != x.any && before && x.lo < (x.written ? s[before - 1].any : s[before - 1].written)) return true;
+        }
+    }
+    return false;
 }
 
 int done(cudaError_t e) { return e == cudaSuccess ? OSDN_OK : OSDN_ERR_CUDA; }
@@ -279,17 +315,23 @@ int osdn_clip_grad_norm(int n, const void *const *grads, void *const *outs,
         if (sizes[i] == 0) continue;
         if (!grads[i] || (outs && !outs[i])) return OSDN_ERR_NULL;
         if (misaligned(grads[i]) || (outs && misaligned(outs[i]))) return OSDN_ERR_ALIGN;
-        const size_t b = (size_t)sizes[i] * io_bytes(ios[i]);
-        const Buf mine[] = {{grads[i], b, !outs || outs[i] == grads[i]},
-                            {outs && outs[i] != grads[i] ? outs[i] : nullptr, b, true},
-                            {workspace, workspace_bytes, true}, {norm, 4, true}};
-        for (int x = 0; x < 4; ++x)
-            for (int y = 0; y < x; ++y) {
-                if (!mine[x].p || !mine[y].p) continue;
-                const uintptr_t p = reinterpret_cast<uintptr_t>(mine[x].p), q = reinterpret_cast<uintptr_t>(mine[y].p);
-                if (p < q + mine[y].n && q < p + mine[x].n) return OSDN_ERR_ALIAS;
-            }
     }
+    const bool scale = outs || !std::isinf(max_norm);
+    const auto span = [&](long long k) {   // the workspace, the norm, the gradients, the outputs
+        const void *p = k == 0 ? workspace : norm;
+        size_t b = k == 0 ? workspace_bytes : norm ? 4 : 0;
+        bool out = true;
+        if (k >= 2) {
+            const long long i = k - 2 < n ? k - 2 : k - 2 - n;
+            const bool in_place = !outs || outs[i] == grads[i];
+            p = k - 2 < n ? grads[i] : outs[i];
+            b = k - 2 < n || !in_place ? (size_t)sizes[i] * io_bytes(ios[i]) : 0;
+            out = k - 2 < n ? in_place && scale : true;
+        }
+        const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+        return Span{lo, lo + b, out ? lo + b : 0};
+    };
+    if (overlap(2 + (long long)n * (outs ? 2 : 1), span)) return OSDN_ERR_ALIAS;
     if (int c = check_device()) return c;
     return done(osdn::clip_launch(n, grads, outs, sizes, ios, max_norm, norm,
                                   static_cast<char *>(workspace) + kStatusBytes, (cudaStream_t)stream));
