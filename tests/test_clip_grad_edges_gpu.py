@@ -43,3 +43,14 @@ def test_full_tables_and_empty_tensors(sizes):
     ops.clip_grad_norm(inplace, 0.25 * n, norm=norm)
     assert abs(float(norm) - n) < 2e-7 * n
     assert all(torch.equal(a, b) for a, b in zip(inplace, outs))
+
+
+def test_a_tensor_counted_twice():
+    # tied weights: the norm alone writes nothing
+    gs = tensors([5000, 300], seed=9)
+    n = norm64([gs[0], *gs])
+    assert abs(float(ops.grad_norm([gs[0], *gs])) - n) < 2e-7 * n
+    # two outputs that share elements
+    out = torch.empty_like(gs[0])
+    with pytest.raises(ops.OsdnError, match="overlaps"):
+        ops.clip_grad_norm(gs, 1.0, outs=[out, out.view(torch.bfloat16)[8:308]])

@@ -67,3 +67,13 @@ def test_workspace_sizes_are_those_of_the_tensors_device(monkeypatch, device):
         q, k, v, o = (Fake(d, 1, 1, 77777, 64) for _ in range(4))
         ops.decay_attn(q, k, v, Fake(d, 1), o=o, ST=Fake(d, 1, 1, 64, 64), workspace=FakeWorkspace(d))
     assert given == [(d, need[d]) for d in (0, 1, 2, 0, 1)]
+
+
+def test_a_tensor_may_be_counted_twice_but_not_written_twice():
+    g = torch.zeros(40)
+    with pytest.raises(ValueError, match="CUDA tensors only"):   # no argument was refused
+        ops.grad_norm([g, g])
+    with pytest.raises(ValueError, match="written twice"):
+        ops.clip_grad_norm([g, g], 1.0)
+    with pytest.raises(ValueError, match="written twice"):
+        ops.clip_grad_norm([g, torch.zeros(40)], float("inf"), outs=[g, g])
