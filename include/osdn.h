@@ -546,7 +546,8 @@ int osdn_group_norm_backward(int io, int B, int G, int T, int D, int heads_first
  *     out_i = g_i min(1, max_norm / norm)
  *
  *   grads  host array of n device pointers; tensor i has sizes[i] elements
- *          (up to 2^40, zero allowed) of type ios[i] (OSDN_F32 / OSDN_BF16)
+ *          (up to 2^40, 2^44 in all, zero allowed) of type ios[i] (OSDN_F32 or
+ *          OSDN_BF16)
  *   outs   host array of n device pointers, of the same types; outs[i] may be
  *          grads[i].  NULL: in place (nothing is written where norm <=
  *          max_norm)

@@ -218,7 +218,7 @@ constexpr int kTable = 1024;   // 28 KB of the 32 KB that a kernel's parameters 
 
 // Tensors [at, n) into the table, as many as fit; returns the first left out that is not empty
 // (n: none), so that only a call without any element meets an empty table.  A launch numbers its
-// chunks in 32 bits (2^45 elements).
+// chunks in 32 bits (a call has at most 2^44 elements, and 2^31 tensors).
 template <int N>
 int fill(Table<N> &t, int at, int n, const void *const *g, void *const *o, const long long *size,
          const int *io) {

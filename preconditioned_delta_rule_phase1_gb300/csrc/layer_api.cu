@@ -309,9 +309,11 @@ int osdn_clip_grad_norm(int n, const void *const *grads, void *const *outs,
     if (!workspace || workspace_bytes < osdn_clip_grad_norm_workspace_bytes(n)) return OSDN_ERR_WORKSPACE;
     if (n > 0 && (!grads || !sizes || !ios)) return OSDN_ERR_NULL;
     if (misaligned(workspace) || (reinterpret_cast<uintptr_t>(norm) & 3u)) return OSDN_ERR_ALIGN;
+    long long elements = 0;   // a launch numbers chunks of 2^13 in 32 bits
     for (int i = 0; i < n; ++i) {
         if (!io_ok(ios[i])) return OSDN_ERR_DTYPE;
         if (sizes[i] < 0 || sizes[i] > (1LL << 40)) return OSDN_ERR_DIMS;
+        if ((elements += sizes[i]) > (1LL << 44)) return OSDN_ERR_DIMS;
         if (sizes[i] == 0) continue;
         if (!grads[i] || (outs && !outs[i])) return OSDN_ERR_NULL;
         if (misaligned(grads[i]) || (outs && misaligned(outs[i]))) return OSDN_ERR_ALIGN;

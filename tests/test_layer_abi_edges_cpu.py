@@ -51,6 +51,14 @@ def test_gradients_scaled_in_place(L):
     assert clip(L, [F, 0], sizes=[16, 0]) in FINE
 
 
+def test_elements_of_all_tensors(L):
+    # chunks of 8192 elements are numbered in 32 bits over a launch's tensors
+    big, at = 1 << 40, [(i + 1) << 44 for i in range(40)]
+    assert clip(L, at[:16], sizes=[big] * 16, norm=F, ws=2 * F) in FINE
+    assert clip(L, at[:17], sizes=[big] * 16 + [1], norm=F, ws=2 * F) == -2
+    assert clip(L, at[:33], sizes=[big] * 33, norm=F, ws=2 * F) == -2
+
+
 def test_against_pairs(L):
     # more tensors than are sorted at once, in any order; overlaps of a few bytes
     rng = random.Random(1)
