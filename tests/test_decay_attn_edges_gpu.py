@@ -16,7 +16,7 @@ import torch
 from preconditioned_delta_rule_phase1_gb300 import build as osdn_build
 from preconditioned_delta_rule_phase1_gb300 import ops
 from tests._util import rel_err
-from tests.test_decay_attn_gpu import STATE_TOL, TOL, autograd, backward, forward, inputs, recurrence
+from tests.test_decay_attn_gpu import STATE_TOL, TOL, WIDTHS, autograd, backward, forward, inputs, recurrence
 
 pytestmark = pytest.mark.gpu
 
@@ -35,6 +35,42 @@ def each_head(got, ref, tol, what, rows=(0,)):
     for h, t in itertools.product(range(ref.shape[1]), rows):
         if ref.dim() == 4 and t < ref.shape[2]:
             assert rel_err(got[:, h, t:], ref[:, h, t:].cpu()) < tol, (what, h, t)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("K,V", WIDTHS)
+def test_each_head_of_the_outputs(io, K, V):
+    for T, s0 in itertools.product([1, 2, 33, 64, 129, 257, 385], [False, True]):
+        x = inputs(2, 7, T, K, V, io, seed=3 * T + K, s0=s0)
+        o, ST = forward(x)
+        ro, rS = recurrence(x["q"], x["k"], x["v"], x["decay"], x["S0"])
+        each_head(o, ro, TOL[io], ("o", T, s0), rows=(0, 2, 128))
+        each_head(ST, rS, STATE_TOL, ("ST", T, s0))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,T,K,V", [(1, 7, 3001, 128, 128), (1, 7, 2050, 64, 128), (40, 7, 130, 64, 64),
+                                       (3, 7, 1111, 128, 64)])
+def test_each_head_of_cut_sequences(io, B, H, T, K, V):
+    x = inputs(B, H, T, K, V, io, seed=T)
+    o, ST = forward(x)
+    ro, rS = recurrence(x["q"], x["k"], x["v"], x["decay"], x["S0"])
+    each_head(o, ro, TOL[io], "o", rows=(0, 2, 128, T // 2))
+    each_head(ST, rS, STATE_TOL, "ST")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("K,V", WIDTHS)
+def test_each_head_of_the_gradients(io, K, V):
+    for (B, T), s0 in itertools.product([(2, 33), (2, 129), (1, 1030), (20, 70)], [False, True]):
+        x = inputs(B, 7, T, K, V, io, seed=T + V + 1, s0=s0)
+        got, ref = backward(x), autograd(x)
+        for n in ("q", "k", "v"):
+            each_head(got[n], ref[n], TOL[io], (n, B, T, s0), rows=(0, 2))
+            if T > 2:   # the last tokens' share of dS_T
+                each_head(got[n][:, :, :-2], ref[n][:, :, :-2], TOL[io], (n, B, T, s0, "but the last"))
+        if s0:
+            each_head(got["S0"], ref["S0"], STATE_TOL, ("S0", B, T))
 
 
 LARGE = {"v": 1e33, "k": 1e33, "q": 1e35, "S0": 1e35, "do": 1e33, "dST": 1e35, "one token": 1e33}
@@ -79,3 +115,29 @@ def test_scores_that_overflow_behind_the_mask(T):
             each_head(got[n][:, :, part], ref[n][:, :, part], TOL["bf16"], (n, part))
     each_head(ST, rS, STATE_TOL, "ST")
     each_head(got["S0"], ref["S0"], STATE_TOL, "S0")
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_step_and_gradients_in_a_graph(io):
+    x = inputs(1, 4, 700, 128, 128, io, seed=8, decay=torch.tensor([0.99, 0.999, 1.0, 0.9]))
+    one = {n: x[n][:, :, 0].contiguous() for n in "qkv"}
+    S, o = x["S0"].clone(), torch.empty_like(one["v"])
+    ws = ops.Workspace()
+    step = lambda: ops.decay_attn_step(one["q"], one["k"], one["v"], x["decay"], S, o=o, workspace=ws)  # noqa: E731
+    step()
+    backward(x, ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+        g = backward(x, ws)
+    for t in (one["v"], x["v"], x["S0"]):
+        t.mul_(-1.0)
+    S.copy_(x["S0"])
+    graph.replay()
+    torch.cuda.synchronize()
+    S2 = x["S0"].clone()
+    o2 = ops.decay_attn_step(one["q"], one["k"], one["v"], x["decay"], S2)
+    want = backward(x)
+    assert torch.equal(o, o2) and torch.equal(S, S2)
+    assert all(torch.equal(g[n], want[n]) for n in want)
+    assert ws.status() == 0
