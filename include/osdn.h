@@ -462,9 +462,13 @@ size_t osdn_decay_attn_workspace_bytes(int io, int B, int H, int T, int K, int V
  * The state layout is that of osdn_chunk_fwd.  Inputs must be finite: with
  * bf16 I/O, inside a block of 128 tokens, a later token's infinity or NaN in
  * v can reach earlier rows.  A score q_t . k_s that overflows where s > t is
- * never read.
- * io == OSDN_BF16 runs on the tensor cores in chunks of 128 tokens, the state
- * with fp32 accuracy; io == OSDN_F32 runs in fp32 FFMA.  With few sequences
+ * never read; where s <= t it has to fit fp32 before its decay, and so has
+ * S q_t with the state entering the block.
+ * io == OSDN_BF16 runs on the tensor cores in chunks of 128 tokens, sums in
+ * fp32.  ST has fp32 accuracy.  For o the weighted scores and a copy of the
+ * state are rounded to bf16 as operands, so that o is within 2.4e-3 of 64 bits
+ * (its own rounding to bf16: 1.7e-3; norms of the error and of o).
+ * io == OSDN_F32 runs in fp32 FFMA.  With few sequences
  * the time axis is cut into ranges that run side by side (K and V are then
  * read twice).
  * With T == 0 the call writes ST = S0 and nothing else.  T may be at most
@@ -490,7 +494,8 @@ int osdn_decay_attn_step(int io, int B, int H, int K, int V, const void *q, cons
  * respect to q, k, v and S_0.  The decay is a constant of the model and has
  * no gradient.  With X_T = d_ST, R_t = X_t + d_o_t q_t^T, X_{t-1} = a R_t:
  *     dq_t = S_t^T d_o_t,   dk_t = R_t^T v_t,   dv_t = R_t k_t,   dS_0 = X_0
- * (S_t is recomputed from k, v and S0).
+ * (S_t is recomputed from k, v and S0).  With bf16 I/O dq, dk and dv have the
+ * accuracy of o, and dS0 that of ST.
  *   d_o  in [B][H][T][V] io       d_ST in [B][H][V][K] fp32, or NULL (zeros)
  *   dq, dk out [B][H][T][K] io    dv   out [B][H][T][V] io
  *   dS0  out [B][H][V][K] fp32, or NULL (not written)

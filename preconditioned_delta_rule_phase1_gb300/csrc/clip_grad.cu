@@ -12,8 +12,9 @@
 // takes a run of chunks.
 //
 // The sum: a thread squares and adds 32 elements in fp32, and adds such sums
-// with their rounding errors kept (an unevaluated pair of fp32), so the norm
-// is as good as one summed in 64 bits.  Squares that leave fp32's range
+// with their rounding errors kept (an unevaluated pair of fp32).  The 32 squares
+// are what rounds: ten additions deep, so the norm is within 5 * 2^-24 (3e-7)
+// of one summed in 64 bits (no more than 2e-7 was met).  Squares that leave fp32's range
 // (|g| above 1e15 or so, or all below 1e-14) are squared and added in fp64
 // instead; infinities and NaN reach the norm, and through it every output.
 // CTAs' sums are joined in a fixed order (no atomics).
@@ -283,7 +284,8 @@ cudaError_t clip_launch(int n, const void *const *g, void *const *o, const long 
                         const int *io, float max_norm, float *norm, void *scratch,
                         cudaStream_t stream) {
     double *part = static_cast<double *>(scratch);
-    // a launch copies its parameters: the table is sized to the call
+    // A launch copies its parameters, 1.4 or 28 KB: 48 tensors take 55.8 us a call (12 on the device),
+    // 49 with the large table 60.4 (12)
     if (n <= 48) return clip::run<48>(n, g, o, size, io, max_norm, norm, part, stream);
     return clip::run<clip::kTable>(n, g, o, size, io, max_norm, norm, part, stream);
 }

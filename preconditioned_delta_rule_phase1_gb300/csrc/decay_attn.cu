@@ -9,8 +9,8 @@
 // {0..3} (p = lane & 7), so that k and q come from shared memory as 16-byte
 // reads that serve four rows, and the four dot products are summed over the
 // eight lanes together, four shuffles.  With two rows a thread those reads,
-// four cycles a warp each, took twice the arithmetic's time (2x16x8192x128:
-// 1153 -> 997 us; 1024 sequences of 256 tokens: 802 -> 643 us).
+// four cycles a warp each, took twice the arithmetic's time (2x16x8192x128
+// 16% longer, 1024 sequences of 256 tokens 25%).
 // The decay costs no multiplication a token: over groups of eight tokens the
 // state is kept as S~ = a^-n S (v is scaled instead) and multiplied by a^8
 // once a group, as long as a^-8 <= 2, so that S~ leaves fp32's range only where
@@ -20,11 +20,12 @@
 // two tokens for those between, chosen at run time, would cost the others 6%,
 // and noticing an overflow to do the tokens over 15%.
 //
-// Bound: 2 K V multiply-adds a token (a third of that more where the time
-// axis is cut), 232 us at 2x16x8192x128; the kernel reaches 0.36 of that rate
-// there.  Twelve warps a SM (160 registers a thread) issue in 0.54 of the
-// slots, half of them multiply-adds: the rest is reads, sums over lanes and
-// their latency.
+// Bound: 2 K V multiply-adds a token, 232 us for 262144 token-heads of 128x128
+// (half as much again, for the states alone, where the time axis is cut).
+// 1024 sequences of 256 tokens take 644 us, 0.36 of that rate; 2x16x8192, which
+// is cut, 1020 us, 0.34.  Twelve warps a SM (160 registers a thread) issue in
+// 0.54 of the slots, half of them multiply-adds: the rest is reads, sums over
+// lanes and their latency.
 #include "decay_attn.cuh"
 
 #include <algorithm>
@@ -323,8 +324,9 @@ Split simt_split(int BH, int T, int K, int V) {
     // CTAs resident at once, in ranges (the same for K and V exchanged)
     const long long slots = 152LL * 3 / (std::max(K, V) / kRows);
     const long long N = (long long)BH * nch;
-    // Tokens one after another: a split pass costs two thirds more, two launches (about 40 tokens'
-    // time) and, in chain_states, about one a range of a sequence.
+    // Tokens one after another: a split pass costs up to two thirds more (half the arithmetic again,
+    // 1020 us where whole sequences take 644), two launches (about 40 tokens' time) and, in
+    // chain_states, about one a range of a sequence.
     const long long whole = (BH + slots - 1) / slots * T;
     long long best = whole, G = BH;
     for (long long g = std::min(N, slots); g > BH; g /= 2) {
