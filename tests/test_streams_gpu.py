@@ -53,8 +53,8 @@ def test_a_busy_current_stream_is_no_part_of_the_call(io, grow):
             call()
         ws = ops.Workspace(stream=side) if grow else None
         torch.cuda.synchronize()
-        for _ in range(12):
-            a @ a   # some hundred milliseconds of the current stream
+        for _ in range(30):
+            a @ a   # half a second of the current stream or so
         busy = torch.cuda.Event()
         busy.record()
         got = flat(call(stream=side, workspace=ws))
