@@ -29,6 +29,13 @@
  * gradient norm of a training step, and clipping by it).  These follow their
  * formulas as stated at each call; the paper has no counterpart to them.
  *
+ * And the recurrent layer without a matrix state, for the same models:
+ * osdn_gated_scan, osdn_gated_scan_step and osdn_gated_scan_backward (a
+ * recurrence with a gate for every token and channel: prompts, single tokens,
+ * gradients), and osdn_layer_norm and osdn_layer_norm_backward (the norm in
+ * front of any of the layers, with the residual stream's addition).  Their
+ * formulas, too, are stated at each call.
+ *
  * Conventions shared by every call
  * --------------------------------
  *  - All tensor pointers are DEVICE pointers owned by the caller; the
@@ -105,11 +112,14 @@ typedef enum {
     OSDN_ERR_SCRATCH = -11,  /* osdn_precond_scan_noalloc: shape needs more
                                 scratch than its static buffer holds         */
     OSDN_ERR_ARG = -12       /* a scalar argument is out of its range (eps, act,
-                                max_norm)                                     */
+                                max_norm, mix)                                */
 } osdn_status;
 
 /* Activations of osdn_group_norm. */
 typedef enum { OSDN_ACT_NONE = 0, OSDN_ACT_SILU = 1, OSDN_ACT_SIGMOID = 2 } osdn_act;
+
+/* How osdn_gated_scan weighs its input. */
+typedef enum { OSDN_MIX_SUM = 0, OSDN_MIX_MEAN = 1, OSDN_MIX_UNIT = 2 } osdn_mix;
 
 /* Bytes of workspace osdn_precond_scan needs for this shape (>= 256). */
 size_t osdn_precond_scan_workspace_bytes(int B, int H, int T, int K);
@@ -567,6 +577,107 @@ size_t osdn_clip_grad_norm_workspace_bytes(int n);
 int osdn_clip_grad_norm(int n, const void *const *grads, void *const *outs,
                         const long long *sizes, const int *ios, float max_norm, float *norm,
                         void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Bytes of workspace osdn_gated_scan needs for this shape (>= 256): one fp32
+ * state a few hundred to a few thousand tokens of a long sequence.
+ */
+size_t osdn_gated_scan_workspace_bytes(int io, int B, int T, int C);
+
+/*
+ * A linear recurrence with a gate for every token and channel.  For each
+ * sequence b and channel c, with a_t = sigmoid(gate_t), from h_0 (h0, or zeros
+ * if h0 is NULL), for t = 1 .. T:
+ *     h_t = a_t h_{t-1} + w(a_t) x_t
+ * with, by mix,
+ *     OSDN_MIX_SUM   w = 1
+ *     OSDN_MIX_MEAN  w = 1 - a           (a weighted mean of what was read)
+ *     OSDN_MIX_UNIT  w = sqrt(1 - a^2)   (independent x of unit variance: so is h)
+ * The gate is read as its logit, so that 1 - a has all its digits whatever
+ * the I/O type: in bf16 a itself could not come closer to 1 than 2^-8.
+ *
+ *   x, gate in  [B][T][C] io
+ *   h0      in  [B][C] fp32, or NULL (zeros)
+ *   h       out [B][T][C] io
+ *   hT      out [B][C] fp32, or NULL (not written)
+ * A factor that is exactly zero hides what it multiplies, an infinity or NaN
+ * included: a token whose gate is -infinity forgets the state before it (a new
+ * document in a packed sequence), and with OSDN_MIX_MEAN or OSDN_MIX_UNIT one
+ * whose gate is +infinity leaves the state as it is and does not read x (a
+ * padded batch: hT is then the state after the last token that counts).
+ * Otherwise an infinity or NaN reaches the later tokens of its channel, at
+ * least until the product of the gates behind it leaves fp32's range.
+ * The state is carried in fp32 and only rounded where it is stored in h.  The
+ * time axis is cut into ranges that run side by side, joined in a fixed order:
+ * results are the same on every run.
+ * With T == 0 the call writes hT = h0 and nothing else.  C is any number of
+ * channels; T may be at most 1,073,741,760 and B ceil(C/32) ceil(T/16) below
+ * 2^31.  Outputs must not overlap inputs, each other or the workspace
+ * (OSDN_ERR_ALIAS).
+ */
+int osdn_gated_scan(int io, int B, int T, int C, int mix, const void *x, const void *gate, const float *h0,
+                    void *h, float *hT, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * One token of osdn_gated_scan, in place: h <- a h + w(a) x, y = h.
+ *   x, gate in [B][C] io     h in/out [B][C] fp32     y out [B][C] io
+ */
+int osdn_gated_scan_step(int io, int B, int C, int mix, const void *x, const void *gate, float *h, void *y,
+                         void *stream);
+
+/*
+ * Gradients of L = <h, d_h> + <h_T, d_hT> through osdn_gated_scan with respect
+ * to x, gate and h_0.  With R_T = d_h_T + d_hT, R_t = d_h_t + a_{t+1} R_{t+1}:
+ *     dx_t = w(a_t) R_t,   dgate_t = R_t (a_t (1 - a_t) h_{t-1} + w'_t x_t),
+ *     dh_0 = a_1 R_1
+ * where w'_t, the derivative of w by the gate, is 0, -a (1 - a) or
+ * -a^2 sqrt((1 - a) / (1 + a)) by mix.  Factors that are zero hide as above
+ * (d_h is read at every token: a padded place has to hold zeros).
+ *   h    in  [B][T][C] io: what osdn_gated_scan wrote for these inputs.  The
+ *            states are recomputed in fp32 from rows of it some tens to
+ *            hundreds of tokens apart
+ *   d_h  in  [B][T][C] io       d_hT in [B][C] fp32, or NULL (zeros)
+ *   dx, dgate out [B][T][C] io  dh0 out [B][C] fp32, or NULL (not written)
+ * The rest, and the limits, as osdn_gated_scan; with T == 0 the call writes
+ * dh0 = d_hT and nothing else.
+ */
+size_t osdn_gated_scan_backward_workspace_bytes(int io, int B, int T, int C);
+int osdn_gated_scan_backward(int io, int B, int T, int C, int mix, const void *x, const void *gate, const void *h,
+                             const float *h0, const void *d_h, const float *d_hT, void *dx, void *dgate,
+                             float *dh0, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Layer norm of rows of C values, with the addition of a residual stream in
+ * front of it.  Per row, with m and v the mean and (biased) variance of s:
+ *     s = x + residual  (s = x without one),
+ *     y = weight (s - m) / sqrt(v + eps) + bias
+ * The norm is taken of the sum in fp32, before it is rounded to be stored.
+ *   x        in  [rows][C] io      residual in [rows][C] io, or NULL
+ *   weight, bias in [C] fp32, each or both NULL (ones, zeros)
+ *   y        out [rows][C] io
+ *   sum      out [rows][C] io: s; given exactly if residual is
+ * C is from 1 to 16384, rows below 2^31; eps > 0 and finite.
+ */
+int osdn_layer_norm(int io, long long rows, int C, const void *x, const void *residual, const float *weight,
+                    const float *bias, float eps, void *y, void *sum, void *stream);
+
+/*
+ * Gradients of osdn_layer_norm given dy [rows][C] io and, or NULL, the
+ * cotangent d_sum [rows][C] io that reaches s by the residual stream; x is
+ * what was normed (sum, with a residual).  With x^ the normed row and
+ * u = dy weight:
+ *     dx = (u - mean(u) - x^ mean(u x^)) / sqrt(v + eps) + d_sum
+ *     dweight = sum over rows of dy x^,    dbias = sum over rows of dy
+ * dx is the gradient of x and of residual alike.
+ *   dx out [rows][C] io
+ *   dweight, dbias out [C] fp32, each or both NULL (not written)
+ * The workspace holds shares of dweight and dbias, joined in a fixed order.
+ * With rows == 0 dweight and dbias are zeroed.
+ */
+size_t osdn_layer_norm_backward_workspace_bytes(long long rows, int C);
+int osdn_layer_norm_backward(int io, long long rows, int C, const void *x, const void *dy, const float *weight,
+                             const void *d_sum, float eps, void *dx, float *dweight, float *dbias,
+                             void *workspace, size_t workspace_bytes, void *stream);
 
 /* Zero the 256-byte status area at the start of a workspace (async). */
 int osdn_workspace_init(void *workspace, size_t workspace_bytes, void *stream);

@@ -5,6 +5,7 @@
 #include <cmath>
 #include <stdint.h>
 
+#include "api_checks.cuh"
 #include "decay_attn.cuh"
 
 namespace osdn {
@@ -32,14 +33,11 @@ cudaError_t clip_launch(int n, const void *const *g, void *const *o, const long 
 
 namespace {
 
-constexpr size_t kStatusBytes = 256;
-constexpr size_t kMaxSeqs = size_t(1) << 24;
-constexpr int kMaxTokens = 1073741760;   // chunk starts stay 32-bit TMA coordinates
+using namespace osdn::api;
 
-bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+constexpr size_t kMaxSeqs = size_t(1) << 24;
+
 bool width_ok(int x) { return x == 64 || x == 128; }
-bool io_ok(int io) { return io == OSDN_F32 || io == OSDN_BF16; }
-size_t io_bytes(int io) { return io == OSDN_BF16 ? 2 : 4; }
 bool dims_ok(int B, int H, int T) {
     return B >= 0 && H >= 0 && T >= 0 && T <= kMaxTokens && (size_t)B * (size_t)H <= kMaxSeqs;
 }
@@ -47,36 +45,6 @@ bool dims_ok(int B, int H, int T) {
 // Units of the attention's time axis over all sequences, numbered in 31 bits (2^31 of the smallest
 // ones are 8 TB of K).
 size_t units(size_t BH, int T) { return BH * (((size_t)T + 15) / 16); }
-
-int check_device() {
-    int dev = 0, major = 0, minor = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
-        return OSDN_ERR_CUDA;
-    return major == 10 && minor == 3 ? OSDN_OK : OSDN_ERR_ARCH;
-}
-
-// A buffer of a call: its address, its bytes and whether the call writes it.
-struct Buf {
-    const void *p;
-    size_t n;
-    bool out;
-};
-// OSDN_ERR_ALIGN or OSDN_ERR_ALIAS if a buffer is not 16-byte aligned or a
-// written one overlaps another, else OSDN_OK.
-template <int N>
-int check_bufs(const Buf (&b)[N]) {
-    for (int i = 0; i < N; ++i)
-        if (misaligned(b[i].p)) return OSDN_ERR_ALIGN;
-    for (int i = 0; i < N; ++i)
-        for (int j = 0; j < i; ++j) {
-            if (!(b[i].out || b[j].out) || !b[i].p || !b[j].p || !b[i].n || !b[j].n) continue;
-            const uintptr_t x = reinterpret_cast<uintptr_t>(b[i].p), y = reinterpret_cast<uintptr_t>(b[j].p);
-            if (x < y + b[j].n && y < x + b[i].n) return OSDN_ERR_ALIAS;
-        }
-    return OSDN_OK;
-}
 
 // An address range, and whether the call writes it; in a sorted list `any`
 // and `written` are the furthest ends up to there of all and of written ones.
@@ -112,8 +80,6 @@ bool overlap(long long n, const At &at) {
     }
     return false;
 }
-
-int done(cudaError_t e) { return e == cudaSuccess ? OSDN_OK : OSDN_ERR_CUDA; }
 
 osdn::da::Pass make_pass(int BH, int H, int T, int K, int V, const void *q, const void *k,
                          const void *v, const float *decay, osdn::da::State S0, void *o,

@@ -33,6 +33,7 @@ from . import build as _build
 
 OSDN_F32, OSDN_BF16 = 0, 1
 ACTS = {"none": 0, "silu": 1, "sigmoid": 2}
+MIXES = {"sum": 0, "mean": 1, "unit": 2}
 STATUS_BYTES = 256
 _lock = threading.Lock()
 _lib = None
@@ -92,6 +93,19 @@ _SIGS = {
     "osdn_clip_grad_norm": (ctypes.c_int, [ctypes.c_int] + [ctypes.c_void_p] * 4 +
                             [ctypes.c_float] + [ctypes.c_void_p] * 2 +
                             [ctypes.c_size_t, ctypes.c_void_p]),
+    "osdn_gated_scan_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 4),
+    "osdn_gated_scan": (ctypes.c_int, [ctypes.c_int] * 5 + [ctypes.c_void_p] * 6 +
+                        [ctypes.c_size_t, ctypes.c_void_p]),
+    "osdn_gated_scan_step": (ctypes.c_int, [ctypes.c_int] * 4 + [ctypes.c_void_p] * 5),
+    "osdn_gated_scan_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 4),
+    "osdn_gated_scan_backward": (ctypes.c_int, [ctypes.c_int] * 5 + [ctypes.c_void_p] * 10 +
+                                 [ctypes.c_size_t, ctypes.c_void_p]),
+    "osdn_layer_norm": (ctypes.c_int, [ctypes.c_int, ctypes.c_longlong, ctypes.c_int] +
+                        [ctypes.c_void_p] * 4 + [ctypes.c_float] + [ctypes.c_void_p] * 3),
+    "osdn_layer_norm_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_longlong, ctypes.c_int]),
+    "osdn_layer_norm_backward": (ctypes.c_int, [ctypes.c_int, ctypes.c_longlong, ctypes.c_int] +
+                                 [ctypes.c_void_p] * 4 + [ctypes.c_float] + [ctypes.c_void_p] * 4 +
+                                 [ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 
@@ -808,3 +822,128 @@ def clip_grad_norm(grads, max_norm, outs=None, norm=None, workspace=None, stream
 def grad_norm(grads, norm=None, workspace=None, stream=None):
     """The global 2-norm of the tensors, [1] fp32 on the device."""
     return clip_grad_norm(grads, float("inf"), norm=norm, workspace=workspace, stream=stream)
+
+
+# The gated recurrent layer's calls.
+
+def gated_scan_workspace_bytes(io, B, T, C) -> int:
+    return int(lib().osdn_gated_scan_workspace_bytes(io, B, T, C))
+
+
+def gated_scan_backward_workspace_bytes(io, B, T, C) -> int:
+    return int(lib().osdn_gated_scan_backward_workspace_bytes(io, B, T, C))
+
+
+def layer_norm_backward_workspace_bytes(rows, C) -> int:
+    return int(lib().osdn_layer_norm_backward_workspace_bytes(rows, C))
+
+
+def _mix(mix):
+    if mix not in MIXES:
+        raise ValueError("mix must be one of %s, got %r" % (sorted(MIXES), mix))
+    return MIXES[mix]
+
+
+@_on_stream
+def gated_scan(x, gate, h0=None, mix="mean", h=None, hT=None, workspace=None, stream=None):
+    """The recurrence h_t = a_t h_{t-1} + w(a_t) x_t with a = sigmoid(gate), channel by channel
+    (osdn_gated_scan): x, gate [B,T,C] (io), h0 [B,C] fp32 or None; w is 1 (mix "sum"), 1 - a
+    ("mean") or sqrt(1 - a^2) ("unit").  Returns (h [B,T,C] (io), hT [B,C] fp32).
+
+    A gate of -inf forgets what was before the token; with "mean" and "unit" one of +inf passes over
+    the token, whatever x holds there."""
+    m = _mix(mix)
+    B, T, C = x.shape
+    io, dt, dev = _io(x), x.dtype, x.device
+    if h is None:
+        h = torch.empty((B, T, C), dtype=dt, device=dev)
+    if hT is None:
+        hT = torch.empty((B, C), dtype=F32, device=dev)
+    args = (io, B, T, C, m, _arg("x", x, (B, T, C), dt, dev), _arg("gate", gate, (B, T, C), dt, dev),
+            _arg("h0", h0, (B, C), F32, dev), _arg("h", h, (B, T, C), dt, dev), _arg("hT", hT, (B, C), F32, dev))
+    _run("osdn_gated_scan", dev, stream, args, _workspace(workspace, dev),
+         ("osdn_gated_scan_workspace_bytes", io, B, T, C))
+    return h, hT
+
+
+@_on_stream
+def gated_scan_step(x, gate, h, mix="mean", y=None, stream=None):
+    """One token of ``gated_scan`` (osdn_gated_scan_step): updates h [B,C] (fp32) in place for the
+    token x, gate [B,C] (io); returns y [B,C] (io), the state rounded."""
+    m = _mix(mix)
+    B, C = x.shape
+    io, dt, dev = _io(x), x.dtype, x.device
+    if y is None:
+        y = torch.empty((B, C), dtype=dt, device=dev)
+    args = (io, B, C, m, _arg("x", x, (B, C), dt, dev), _arg("gate", gate, (B, C), dt, dev),
+            _arg("h", h, (B, C), F32, dev), _arg("y", y, (B, C), dt, dev))
+    _run("osdn_gated_scan_step", dev, stream, args)
+    return y
+
+
+@_on_stream
+def gated_scan_backward(x, gate, h, h0=None, *, dh, dhT=None, mix="mean", workspace=None, stream=None):
+    """Gradients through ``gated_scan`` (osdn_gated_scan_backward) given h, which it returned, and the
+    cotangents dh [B,T,C] (io) of h and dhT [B,C] fp32 of hT (None: zero).  Returns a dict with x,
+    gate (io) and, if h0 is given, h0 (fp32)."""
+    m = _mix(mix)
+    B, T, C = x.shape
+    io, dt, dev = _io(x), x.dtype, x.device
+    full = (B, T, C)
+    args = (io, B, T, C, m, _arg("x", x, full, dt, dev), _arg("gate", gate, full, dt, dev),
+            _arg("h", h, full, dt, dev), _arg("h0", h0, (B, C), F32, dev), _arg("dh", dh, full, dt, dev),
+            _arg("dhT", dhT, (B, C), F32, dev))
+    g = {"x": torch.empty_like(x), "gate": torch.empty_like(x)}
+    if h0 is not None:
+        g["h0"] = torch.empty_like(h0)
+    args += (g["x"].data_ptr(), g["gate"].data_ptr(), None if h0 is None else g["h0"].data_ptr())
+    _run("osdn_gated_scan_backward", dev, stream, args, _workspace(workspace, dev),
+         ("osdn_gated_scan_backward_workspace_bytes", io, B, T, C))
+    return g
+
+
+@_on_stream
+def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, y=None, s=None, stream=None):
+    """Layer norm over the last dimension (osdn_layer_norm): x [...,C] (io), weight, bias [C] fp32.
+    Returns y, like x.  With `residual` (like x) the norm is of s = x + residual, and the call
+    returns (y, s), s rounded to x's type."""
+    if x.dim() == 0:
+        raise ValueError("x must have a last dimension to norm over")
+    C = x.shape[-1]
+    rows = x.numel() // C if C else 0
+    io, dt, dev = _io(x), x.dtype, x.device
+    if s is not None and residual is None:
+        raise ValueError("s is the sum with a residual; there is none")
+    if y is None:
+        y = torch.empty_like(x)
+    if s is None and residual is not None:
+        s = torch.empty_like(x)
+    args = (io, rows, C, _arg("x", x, x.shape, dt, dev), _arg("residual", residual, x.shape, dt, dev),
+            _arg("weight", weight, (C,), F32, dev), _arg("bias", bias, (C,), F32, dev), float(eps),
+            _arg("y", y, x.shape, dt, dev), _arg("s", s, x.shape, dt, dev))
+    _run("osdn_layer_norm", dev, stream, args)
+    return y if residual is None else (y, s)
+
+
+@_on_stream
+def layer_norm_backward(x, dy, weight=None, bias=None, ds=None, eps=1e-5, workspace=None, stream=None):
+    """Gradients of ``layer_norm`` (osdn_layer_norm_backward) given dy, like x, and the cotangent ds
+    of the residual stream (like x, or None).  x is what was normed: s, where a residual was added.
+    Returns a dict with x (the residual's gradient too) and weight, bias for those given."""
+    if x.dim() == 0:
+        raise ValueError("x must have a last dimension to norm over")
+    C = x.shape[-1]
+    rows = x.numel() // C if C else 0
+    io, dt, dev = _io(x), x.dtype, x.device
+    args = (io, rows, C, _arg("x", x, x.shape, dt, dev), _arg("dy", dy, x.shape, dt, dev),
+            _arg("weight", weight, (C,), F32, dev), _arg("ds", ds, x.shape, dt, dev), float(eps))
+    _arg("bias", bias, (C,), F32, dev)
+    g = {"x": torch.empty_like(x)}
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            g[name] = torch.empty_like(t)
+    at = lambda name: g[name].data_ptr() if name in g else None  # noqa: E731
+    args += (at("x"), at("weight"), at("bias"))
+    _run("osdn_layer_norm_backward", dev, stream, args, _workspace(workspace, dev),
+         ("osdn_layer_norm_backward_workspace_bytes", rows, C))
+    return g
