@@ -579,12 +579,6 @@ int osdn_clip_grad_norm(int n, const void *const *grads, void *const *outs,
                         void *workspace, size_t workspace_bytes, void *stream);
 
 /*
- * Bytes of workspace osdn_gated_scan needs for this shape (>= 256): one fp32
- * state a few hundred to a few thousand tokens of a long sequence.
- */
-size_t osdn_gated_scan_workspace_bytes(int io, int B, int T, int C);
-
-/*
  * A linear recurrence with a gate for every token and channel.  For each
  * sequence b and channel c, with a_t = sigmoid(gate_t), from h_0 (h0, or zeros
  * if h0 is NULL), for t = 1 .. T:
@@ -607,16 +601,17 @@ size_t osdn_gated_scan_workspace_bytes(int io, int B, int T, int C);
  * padded batch: hT is then the state after the last token that counts).
  * Otherwise an infinity or NaN reaches the later tokens of its channel, at
  * least until the product of the gates behind it leaves fp32's range.
- * The state is carried in fp32 and only rounded where it is stored in h.  The
- * time axis is cut into ranges that run side by side, joined in a fixed order:
- * results are the same on every run.
- * With T == 0 the call writes hT = h0 and nothing else.  C is any number of
- * channels; T may be at most 1,073,741,760 and B ceil(C/32) ceil(T/16) below
- * 2^31.  Outputs must not overlap inputs, each other or the workspace
- * (OSDN_ERR_ALIAS).
+ * The state is carried in fp32 and only rounded where it is stored in h.  With
+ * fp32 I/O 1 - a enters the state with all its digits; with bf16 I/O a is
+ * rounded to fp32 (the gate's own rounding to bf16 moves 1 - a far more).  The
+ * time axis is cut into runs that are worked on side by side and joined in a
+ * fixed order: results are the same on every run.  The call needs no workspace.
+ * With T == 0 it writes hT = h0 and nothing else.  C is any number of channels
+ * up to 2^24; T may be at most 1,073,741,760 and B ceil(C/32) ceil(T/16) below
+ * 2^31.  Outputs must not overlap inputs or each other (OSDN_ERR_ALIAS).
  */
 int osdn_gated_scan(int io, int B, int T, int C, int mix, const void *x, const void *gate, const float *h0,
-                    void *h, float *hT, void *workspace, size_t workspace_bytes, void *stream);
+                    void *h, float *hT, void *stream);
 
 /*
  * One token of osdn_gated_scan, in place: h <- a h + w(a) x, y = h.
@@ -641,10 +636,9 @@ int osdn_gated_scan_step(int io, int B, int C, int mix, const void *x, const voi
  * The rest, and the limits, as osdn_gated_scan; with T == 0 the call writes
  * dh0 = d_hT and nothing else.
  */
-size_t osdn_gated_scan_backward_workspace_bytes(int io, int B, int T, int C);
 int osdn_gated_scan_backward(int io, int B, int T, int C, int mix, const void *x, const void *gate, const void *h,
                              const float *h0, const void *d_h, const float *d_hT, void *dx, void *dgate,
-                             float *dh0, void *workspace, size_t workspace_bytes, void *stream);
+                             float *dh0, void *stream);
 
 /*
  * Layer norm of rows of C values, with the addition of a residual stream in

@@ -1,13 +1,20 @@
 // gated_scan.cuh -- the arithmetic of the recurrence in gated_scan.cu.
 //
-// A gate g is held as one signed number c: its smaller sigmoid s = 1 / (1 +
-// e^|g|), negative where the state is kept rather than dropped (g >= 0):
+// Two forms.  The exact one holds a gate g as one signed number c: its smaller
+// sigmoid s = 1 / (1 + e^|g|), negative where the state is kept rather than
+// dropped (g >= 0):
 //     g >= 0:  1 - a = s = -c,  a v = v + c v
 //     g <  0:      a = s =  c,  a v = c v
 // Both a and 1 - a then have all their digits: a itself, rounded to fp32, says
-// too little of 1 - a for memories of thousands of tokens (2^-25 an error of
+// too little of 1 - a for memories of thousands of tokens (2^-25, an error of
 // the same sign at every token of a constant gate).  g = -inf is c = +0, g =
-// +inf is c = -0.
+// +inf is c = -0; a factor that is exactly zero hides what it multiplies.
+//
+// The short one, for bf16 I/O and |g| <= kPlainGate, holds a rounded to fp32:
+// a bf16 gate knows its own 1 - a to 2^-9 g of itself, far less than that
+// rounding takes away (at g = 7, 1 - a = 9e-4 to 1.4%, and 2^-25 is 0.003% of
+// it), and instructions are what bounds bf16.  1 - a is e^-g a, and keeps its
+// digits in both forms.
 #pragma once
 
 #include "osdn_device.cuh"
@@ -20,35 +27,103 @@ struct Mix {
     static constexpr int value = M;
 };
 
-__device__ __forceinline__ float gate_coefficient(float g) {
-    float e, r;
-    // the hardware's base-2 exponential and reciprocal (2 ulp each); e = 0 from |g| = 87.4
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(g) * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return __uint_as_float(__float_as_uint(e * r) | (~__float_as_uint(g) & 0x80000000u));
+// V channels of a thread; two go through packed instructions.
+template <int V>
+struct Vec {
+    float v[V];
+};
+template <int V>
+__device__ __forceinline__ Vec<V> fill(float x) {
+    Vec<V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = x;
+    return r;
 }
-__device__ __forceinline__ bool keeps(float c) { return (int)__float_as_uint(c) < 0; }
-__device__ __forceinline__ bool forgets(float c) { return __float_as_uint(c) == 0u; }        // a = 0
-__device__ __forceinline__ bool passes(float c) { return __float_as_uint(c) == 0x80000000u; }  // 1 - a = 0
+template <int V>
+__device__ __forceinline__ Vec<V> mul(const Vec<V> &a, const Vec<V> &b) {
+    Vec<V> r;
+    if constexpr (V == 2) {
+        const float2 x = __fmul2_rn(make_float2(a.v[0], a.v[1]), make_float2(b.v[0], b.v[1]));
+        r.v[0] = x.x;
+        r.v[1] = x.y;
+    } else {
+        r.v[0] = a.v[0] * b.v[0];
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> add(const Vec<V> &a, const Vec<V> &b) {
+    Vec<V> r;
+    if constexpr (V == 2) {
+        const float2 x = __fadd2_rn(make_float2(a.v[0], a.v[1]), make_float2(b.v[0], b.v[1]));
+        r.v[0] = x.x;
+        r.v[1] = x.y;
+    } else {
+        r.v[0] = a.v[0] + b.v[0];
+    }
+    return r;
+}
+template <int V>
+__device__ __forceinline__ Vec<V> fma(const Vec<V> &a, const Vec<V> &b, const Vec<V> &c) {
+    Vec<V> r;
+    if constexpr (V == 2) {
+        const float2 x = __ffma2_rn(make_float2(a.v[0], a.v[1]), make_float2(b.v[0], b.v[1]),
+                                    make_float2(c.v[0], c.v[1]));
+        r.v[0] = x.x;
+        r.v[1] = x.y;
+    } else {
+        r.v[0] = fmaf(a.v[0], b.v[0], c.v[0]);
+    }
+    return r;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {   // the hardware's, 2 ulp, zero below 2^-126
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+    return e;
+}
+__device__ __forceinline__ float rcp_fast(float x) {    // 1 ulp
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float sqrt_fast(float x) {   // 3 ulp
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rsqrt_fast(float x) {
+    float r;
+    asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 // c v, where a factor that is exactly zero hides v whatever it holds.
 __device__ __forceinline__ float hide(float c, float v) { return c == 0.0f ? 0.0f : c * v; }
 
-// Z: some factor may be exactly zero, and then hides what it multiplies.  Without Z there is none
-// (the callers look), and the selections are saved.
+// ------------------------------------------------------------- the exact form
+__device__ __forceinline__ float gate_coefficient(float g) {
+    const float e = exp2_fast(fabsf(g) * -kLog2e);
+    return __uint_as_float(__float_as_uint(e * rcp_fast(1.0f + e)) | (~__float_as_uint(g) & 0x80000000u));
+}
+__device__ __forceinline__ bool keeps(float c) { return (int)__float_as_uint(c) < 0; }
+__device__ __forceinline__ bool forgets(float c) { return __float_as_uint(c) == 0u; }          // a = 0
+__device__ __forceinline__ bool passes(float c) { return __float_as_uint(c) == 0x80000000u; }  // 1 - a = 0
+
+// a v.  Z: the factor may be exactly zero (without Z the callers have looked that none is).
 template <bool Z>
 __device__ __forceinline__ float decay(float c, float v) {
     if (Z && forgets(c)) return 0.0f;
     return fmaf(c, v, keeps(c) ? v : 0.0f);
 }
+// w(a)^2 = 1 - a^2 = s (2 - s), or 1 - s^2
+__device__ __forceinline__ float unit_square(float c) { return fmaf(-c, c, keeps(c) ? -2.0f * c : 1.0f); }
 template <int MIX>
 __device__ __forceinline__ float weight(float c) {
     if (MIX == OSDN_MIX_SUM) return 1.0f;
     if (MIX == OSDN_MIX_MEAN) return keeps(c) ? -c : 1.0f - c;
-    // 1 - a^2 = s (2 - s), or 1 - s^2
-    float w;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(w) : "f"(fmaf(-c, c, keeps(c) ? -2.0f * c : 1.0f)));
-    return w;
+    return sqrt_fast(unit_square(c));
 }
 // w(a) x
 template <int MIX, bool Z>
@@ -57,26 +132,60 @@ __device__ __forceinline__ float weighted(float c, float x) {
     if (Z && passes(c)) return 0.0f;
     return weight<MIX>(c) * x;
 }
-// With r the cotangent of the state after a token and v the state before it: the gradients w r of x
-// and r (a b v + w' x) = r a b (v - k x) of g, where k is 0, 1 or a / w.  (w' = -a / w times a b,
-// and k a b = a^2 sqrt((1 - a) / (1 + a)) goes to zero where w does.)
+// With v the state before a token: the factors that turn R into the gradients, w for x and
+// a b v + w' x = a b (v - k x) for g, where k is 0, 1 or a / w.  (w' = -a / w times a b, and k a b =
+// a^2 sqrt((1 - a) / (1 + a)) goes to zero where w does.)
 template <int MIX, bool Z>
-__device__ __forceinline__ void gradients(float c, float r, float v, float x, float &dx, float &dg) {
+__device__ __forceinline__ void slopes(float c, float v, float x, float &w, float &slope) {
     const float s = fabsf(c), ab = fmaf(-s, s, s);
-    float d = v;
-    if (MIX == OSDN_MIX_SUM) dx = r;
-    if (MIX == OSDN_MIX_MEAN) {
-        dx = weight<MIX>(c) * r;
-        d -= x;
+    w = weight<MIX>(c);
+    if (MIX == OSDN_MIX_MEAN) v -= x;
+    if (MIX == OSDN_MIX_UNIT)
+        v = fmaf(-(keeps(c) ? 1.0f + c : c) * rsqrt_fast(fmaxf(unit_square(c), 1e-37f)), x, v);
+    slope = Z && ab == 0.0f ? 0.0f : ab * v;
+}
+
+// ------------------------------------------------------------- the short form
+constexpr float kPlainGate = 80.0f;   // e^80 and its reciprocal are normal numbers
+// a and b = 1 - a
+template <int V>
+__device__ __forceinline__ void sigmoids(const Vec<V> &g, Vec<V> &a, Vec<V> &b) {
+    Vec<V> e = mul(g, fill<V>(-kLog2e));
+#pragma unroll
+    for (int i = 0; i < V; ++i) e.v[i] = exp2_fast(e.v[i]);
+    a = add(e, fill<V>(1.0f));
+#pragma unroll
+    for (int i = 0; i < V; ++i) a.v[i] = rcp_fast(a.v[i]);
+    b = mul(e, a);
+}
+template <int MIX, int V>
+__device__ __forceinline__ Vec<V> weight(const Vec<V> &a, const Vec<V> &b) {
+    if (MIX == OSDN_MIX_SUM) return fill<V>(1.0f);
+    if (MIX == OSDN_MIX_MEAN) return b;
+    Vec<V> w = fma(a, b, b);   // 1 - a^2
+#pragma unroll
+    for (int i = 0; i < V; ++i) w.v[i] = sqrt_fast(w.v[i]);
+    return w;
+}
+template <int MIX, int V>
+__device__ __forceinline__ void slopes(const Vec<V> &a, const Vec<V> &b, const Vec<V> &v, const Vec<V> &x, Vec<V> &w,
+                                       Vec<V> &slope) {
+    const Vec<V> ab = mul(a, b);
+    if (MIX == OSDN_MIX_SUM) {
+        w = fill<V>(1.0f);
+        slope = mul(ab, v);
+    } else if (MIX == OSDN_MIX_MEAN) {
+        w = b;
+        slope = mul(ab, fma(x, fill<V>(-1.0f), v));
+    } else {
+        const Vec<V> q = add(ab, b);
+        Vec<V> k;
+#pragma unroll
+        for (int i = 0; i < V; ++i) k.v[i] = rsqrt_fast(q.v[i]);
+        w = mul(q, k);
+        k = mul(mul(a, k), x);
+        slope = mul(ab, fma(k, fill<V>(-1.0f), v));
     }
-    if (MIX == OSDN_MIX_UNIT) {
-        const float q = fmaf(-c, c, keeps(c) ? -2.0f * c : 1.0f);   // w^2
-        float inv;
-        asm("rsqrt.approx.f32 %0, %1;" : "=f"(inv) : "f"(fmaxf(q, 1e-37f)));
-        dx = q * inv * r;
-        d = fmaf(-(keeps(c) ? 1.0f + c : c) * inv, x, d);
-    }
-    dg = Z && ab == 0.0f ? 0.0f : r * ab * d;
 }
 
 }  // namespace gs

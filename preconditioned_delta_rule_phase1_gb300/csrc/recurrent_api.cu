@@ -7,15 +7,13 @@
 
 namespace osdn {
 namespace gs {
-size_t scan_scratch_bytes(int io, int B, int T, int C);
-size_t backward_scratch_bytes(int io, int B, int T, int C);
 cudaError_t scan_launch(int io, int B, int T, int C, int mix, const void *x, const void *gate, const float *h0,
-                        void *h, float *hT, void *scratch, int *status, cudaStream_t stream);
+                        void *h, float *hT, cudaStream_t stream);
 cudaError_t step_launch(int io, int B, int C, int mix, const void *x, const void *gate, float *h, void *y,
                         cudaStream_t stream);
 cudaError_t backward_launch(int io, int B, int T, int C, int mix, const void *x, const void *gate, const void *h,
                             const float *h0, const void *dh, const float *dhT, void *dx, void *dgate, float *dh0,
-                            void *scratch, int *status, cudaStream_t stream);
+                            cudaStream_t stream);
 }  // namespace gs
 namespace ln {
 size_t backward_scratch_bytes(long long rows, int C);
@@ -34,12 +32,13 @@ using namespace osdn::api;
 
 constexpr int kMaxWidth = 16384;   // layer norm: a row stays in one CTA's registers
 constexpr long long kMaxRows = 0x7fffffff;
+constexpr int kMaxChannels = 1 << 24;   // the recurrence: 16 rows are addressed in 32 bits
 
 bool mix_ok(int mix) { return mix >= OSDN_MIX_SUM && mix <= OSDN_MIX_UNIT; }
 
 // Tiles of the recurrence (at least 16 tokens of 32 channels of a sequence) are numbered in 31 bits.
 bool scan_dims_ok(int B, int T, int C) {
-    if (B < 0 || T < 0 || C < 0 || T > kMaxTokens) return false;
+    if (B < 0 || T < 0 || C < 0 || T > kMaxTokens || C > kMaxChannels) return false;
     const double strips = (double)B * (((double)C + 31) / 32), chunks = ((double)T + 15) / 16;
     return strips <= 2147483647.0 && strips * chunks <= 2147483647.0;
 }
@@ -50,29 +49,21 @@ bool eps_ok(float eps) { return eps > 0.0f && !std::isinf(eps); }
 
 extern "C" {
 
-size_t osdn_gated_scan_workspace_bytes(int io, int B, int T, int C) {
-    if (!io_ok(io) || !scan_dims_ok(B, T, C) || B == 0 || T == 0 || C == 0) return kStatusBytes;
-    return kStatusBytes + osdn::gs::scan_scratch_bytes(io, B, T, C);
-}
-
 int osdn_gated_scan(int io, int B, int T, int C, int mix, const void *x, const void *gate, const float *h0,
-                    void *h, float *hT, void *workspace, size_t workspace_bytes, void *stream) {
+                    void *h, float *hT, void *stream) {
     if (!io_ok(io)) return OSDN_ERR_DTYPE;
     if (!scan_dims_ok(B, T, C)) return OSDN_ERR_DIMS;
     if (!mix_ok(mix)) return OSDN_ERR_ARG;
-    if (!workspace || workspace_bytes < osdn_gated_scan_workspace_bytes(io, B, T, C)) return OSDN_ERR_WORKSPACE;
     const size_t states = (size_t)B * C, n = states * T * io_bytes(io);
     if (states == 0) return OSDN_OK;
     if (n && (!x || !gate || !h)) return OSDN_ERR_NULL;
     const Buf bufs[] = {{x, n, false}, {gate, n, false}, {h0, states * 4, false}, {h, n, true},
-                        {hT, states * 4, true}, {workspace, workspace_bytes, true}};
+                        {hT, states * 4, true}};
     if (int c = check_bufs(bufs)) return c;
     if (int c = check_device()) return c;
     cudaStream_t st = (cudaStream_t)stream;
     if (T == 0) return done(osdn::fill_state_launch(hT ? states : 0, h0, 0.0f, hT, st));
-    return done(osdn::gs::scan_launch(io, B, T, C, mix, x, gate, h0, h, hT,
-                                      static_cast<char *>(workspace) + kStatusBytes,
-                                      static_cast<int *>(workspace), st));
+    return done(osdn::gs::scan_launch(io, B, T, C, mix, x, gate, h0, h, hT, st));
 }
 
 int osdn_gated_scan_step(int io, int B, int C, int mix, const void *x, const void *gate, float *h, void *y,
@@ -89,32 +80,22 @@ int osdn_gated_scan_step(int io, int B, int C, int mix, const void *x, const voi
     return done(osdn::gs::step_launch(io, B, C, mix, x, gate, h, y, (cudaStream_t)stream));
 }
 
-size_t osdn_gated_scan_backward_workspace_bytes(int io, int B, int T, int C) {
-    if (!io_ok(io) || !scan_dims_ok(B, T, C) || B == 0 || T == 0 || C == 0) return kStatusBytes;
-    return kStatusBytes + osdn::gs::backward_scratch_bytes(io, B, T, C);
-}
-
 int osdn_gated_scan_backward(int io, int B, int T, int C, int mix, const void *x, const void *gate, const void *h,
                              const float *h0, const void *d_h, const float *d_hT, void *dx, void *dgate,
-                             float *dh0, void *workspace, size_t workspace_bytes, void *stream) {
+                             float *dh0, void *stream) {
     if (!io_ok(io)) return OSDN_ERR_DTYPE;
     if (!scan_dims_ok(B, T, C)) return OSDN_ERR_DIMS;
     if (!mix_ok(mix)) return OSDN_ERR_ARG;
-    if (!workspace || workspace_bytes < osdn_gated_scan_backward_workspace_bytes(io, B, T, C))
-        return OSDN_ERR_WORKSPACE;
     const size_t states = (size_t)B * C, n = states * T * io_bytes(io);
     if (states == 0) return OSDN_OK;
     if (n && (!x || !gate || !h || !d_h || !dx || !dgate)) return OSDN_ERR_NULL;
     const Buf bufs[] = {{x, n, false}, {gate, n, false}, {h, n, false}, {h0, states * 4, false}, {d_h, n, false},
-                        {d_hT, states * 4, false}, {dx, n, true}, {dgate, n, true}, {dh0, states * 4, true},
-                        {workspace, workspace_bytes, true}};
+                        {d_hT, states * 4, false}, {dx, n, true}, {dgate, n, true}, {dh0, states * 4, true}};
     if (int c = check_bufs(bufs)) return c;
     if (int c = check_device()) return c;
     cudaStream_t st = (cudaStream_t)stream;
     if (T == 0) return done(osdn::fill_state_launch(dh0 ? states : 0, d_hT, 0.0f, dh0, st));
-    return done(osdn::gs::backward_launch(io, B, T, C, mix, x, gate, h, h0, d_h, d_hT, dx, dgate, dh0,
-                                          static_cast<char *>(workspace) + kStatusBytes,
-                                          static_cast<int *>(workspace), st));
+    return done(osdn::gs::backward_launch(io, B, T, C, mix, x, gate, h, h0, d_h, d_hT, dx, dgate, dh0, st));
 }
 
 int osdn_layer_norm(int io, long long rows, int C, const void *x, const void *residual, const float *weight,

@@ -93,13 +93,9 @@ _SIGS = {
     "osdn_clip_grad_norm": (ctypes.c_int, [ctypes.c_int] + [ctypes.c_void_p] * 4 +
                             [ctypes.c_float] + [ctypes.c_void_p] * 2 +
                             [ctypes.c_size_t, ctypes.c_void_p]),
-    "osdn_gated_scan_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 4),
-    "osdn_gated_scan": (ctypes.c_int, [ctypes.c_int] * 5 + [ctypes.c_void_p] * 6 +
-                        [ctypes.c_size_t, ctypes.c_void_p]),
+    "osdn_gated_scan": (ctypes.c_int, [ctypes.c_int] * 5 + [ctypes.c_void_p] * 6),
     "osdn_gated_scan_step": (ctypes.c_int, [ctypes.c_int] * 4 + [ctypes.c_void_p] * 5),
-    "osdn_gated_scan_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int] * 4),
-    "osdn_gated_scan_backward": (ctypes.c_int, [ctypes.c_int] * 5 + [ctypes.c_void_p] * 10 +
-                                 [ctypes.c_size_t, ctypes.c_void_p]),
+    "osdn_gated_scan_backward": (ctypes.c_int, [ctypes.c_int] * 5 + [ctypes.c_void_p] * 10),
     "osdn_layer_norm": (ctypes.c_int, [ctypes.c_int, ctypes.c_longlong, ctypes.c_int] +
                         [ctypes.c_void_p] * 4 + [ctypes.c_float] + [ctypes.c_void_p] * 3),
     "osdn_layer_norm_backward_workspace_bytes": (ctypes.c_size_t, [ctypes.c_longlong, ctypes.c_int]),
@@ -826,14 +822,6 @@ def grad_norm(grads, norm=None, workspace=None, stream=None):
 
 # The gated recurrent layer's calls.
 
-def gated_scan_workspace_bytes(io, B, T, C) -> int:
-    return int(lib().osdn_gated_scan_workspace_bytes(io, B, T, C))
-
-
-def gated_scan_backward_workspace_bytes(io, B, T, C) -> int:
-    return int(lib().osdn_gated_scan_backward_workspace_bytes(io, B, T, C))
-
-
 def layer_norm_backward_workspace_bytes(rows, C) -> int:
     return int(lib().osdn_layer_norm_backward_workspace_bytes(rows, C))
 
@@ -851,7 +839,8 @@ def gated_scan(x, gate, h0=None, mix="mean", h=None, hT=None, workspace=None, st
     ("mean") or sqrt(1 - a^2) ("unit").  Returns (h [B,T,C] (io), hT [B,C] fp32).
 
     A gate of -inf forgets what was before the token; with "mean" and "unit" one of +inf passes over
-    the token, whatever x holds there."""
+    the token, whatever x holds there.  `workspace` is taken as by the other layers' calls; this one
+    needs none."""
     m = _mix(mix)
     B, T, C = x.shape
     io, dt, dev = _io(x), x.dtype, x.device
@@ -861,8 +850,7 @@ def gated_scan(x, gate, h0=None, mix="mean", h=None, hT=None, workspace=None, st
         hT = torch.empty((B, C), dtype=F32, device=dev)
     args = (io, B, T, C, m, _arg("x", x, (B, T, C), dt, dev), _arg("gate", gate, (B, T, C), dt, dev),
             _arg("h0", h0, (B, C), F32, dev), _arg("h", h, (B, T, C), dt, dev), _arg("hT", hT, (B, C), F32, dev))
-    _run("osdn_gated_scan", dev, stream, args, _workspace(workspace, dev),
-         ("osdn_gated_scan_workspace_bytes", io, B, T, C))
+    _run("osdn_gated_scan", dev, stream, args)
     return h, hT
 
 
@@ -885,7 +873,7 @@ def gated_scan_step(x, gate, h, mix="mean", y=None, stream=None):
 def gated_scan_backward(x, gate, h, h0=None, *, dh, dhT=None, mix="mean", workspace=None, stream=None):
     """Gradients through ``gated_scan`` (osdn_gated_scan_backward) given h, which it returned, and the
     cotangents dh [B,T,C] (io) of h and dhT [B,C] fp32 of hT (None: zero).  Returns a dict with x,
-    gate (io) and, if h0 is given, h0 (fp32)."""
+    gate (io) and, if h0 is given, h0 (fp32).  `workspace` as in ``gated_scan``."""
     m = _mix(mix)
     B, T, C = x.shape
     io, dt, dev = _io(x), x.dtype, x.device
@@ -897,8 +885,7 @@ def gated_scan_backward(x, gate, h, h0=None, *, dh, dhT=None, mix="mean", worksp
     if h0 is not None:
         g["h0"] = torch.empty_like(h0)
     args += (g["x"].data_ptr(), g["gate"].data_ptr(), None if h0 is None else g["h0"].data_ptr())
-    _run("osdn_gated_scan_backward", dev, stream, args, _workspace(workspace, dev),
-         ("osdn_gated_scan_backward_workspace_bytes", io, B, T, C))
+    _run("osdn_gated_scan_backward", dev, stream, args)
     return g
 
 

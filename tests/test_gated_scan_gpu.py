@@ -231,9 +231,9 @@ def test_extreme_gates(T):
         g = ops.gated_scan_backward(t["x"], t["gate"], h, t["h0"], dh=t["dh"], dhT=t["dhT"], mix=mix)
         assert all(torch.isfinite(v).all() for v in g.values())
         # a sigmoid below fp32's normal range (2^-126) may be zero, and the root of twice it with it
-        R = (dx / gates64(d["gate"], mix)[2]).abs()
-        close(g["x"], dx, 2.0 ** -24, R * 2.0 ** (-62 if mix == "unit" else -126), what=mix)
-        close(g["gate"], dg, 2.0 ** -24, 1e-30, what=mix)
+        R = (dx / gates64(d["gate"], mix)[2]).abs() * 2.0 ** (-62 if mix == "unit" else -126)
+        close(g["x"], dx, 2.0 ** -24, R, what=mix)
+        close(g["gate"], dg, 2.0 ** -24, R * d["x"].abs() + lever * 2.0 ** -126 + 1e-30, what=mix)
 
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
