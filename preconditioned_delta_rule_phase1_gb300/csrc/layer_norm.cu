@@ -6,11 +6,12 @@
 //     dweight = sum over rows of dy x^,   dbias = sum over rows of dy
 // Rows are read and written once, so HBM bounds both directions.  A row is
 // held in registers, N pieces of E neighbouring channels a thread (16 bytes
-// where rows keep 16-byte boundaries, else one word or one element), by one
+// where rows keep 16-byte boundaries, else one word), by one
 // warp where it is short and by up to 32 otherwise.  Statistics are taken in
 // two steps, the mean of the values less the row's first, so that a large mean
 // costs no accuracy, and then the variance; all arithmetic is fp32.
 #include <algorithm>
+#include <type_traits>
 
 #include "decay_attn.cuh"
 #include "ptx.cuh"
@@ -20,70 +21,158 @@ namespace ln {
 
 namespace {
 
-// E neighbouring channels as they lie in memory.
-template <int BYTES> struct Word;
-template <> struct Word<16> { typedef uint4 type; };
-template <> struct Word<4> { typedef unsigned type; };
-template <> struct Word<2> { typedef unsigned short type; };
+// Zeros, or the bytes at p where `there`.  Predicated rather than branched around: the compiler would
+// move the first use into the branch, and wait there for one load after the other.
+__device__ __forceinline__ void load_if(const void *p, bool there, uint4 &u) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+                 "mov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t@q ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p), "r"((int)there));
+}
+__device__ __forceinline__ void load_if(const void *p, bool there, unsigned &u) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\tmov.b32 %0, 0;\n\t@q ld.global.nc.b32 %0, [%1];\n\t}"
+                 : "=r"(u) : "l"(p), "r"((int)there));
+}
+__device__ __forceinline__ void load_half(const void *p, unsigned &u) {
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(u) : "l"(p));
+}
 
-template <typename io_t, int E>
-struct Piece {
-    typedef typename Word<E * (int)sizeof(io_t)>::type raw_t;
-    raw_t u;
-    __device__ __forceinline__ void zero() { u = raw_t(); }
-    __device__ __forceinline__ void load(const io_t *p) { u = *reinterpret_cast<const raw_t *>(p); }
-    __device__ __forceinline__ void wide(float (&x)[E]) const {
-        if constexpr (sizeof(raw_t) == 16) {
-            const unsigned w[4] = {u.x, u.y, u.z, u.w};
+// How a row of C channels lies in its threads' pieces: kFull, it fills them all; kTail, some threads
+// have fewer or none; kOdd (rows of an odd number of bf16, E = 2), also the row may begin in the middle
+// of a word, and its first and last pieces may hold one channel.
+enum { kFull, kTail, kOdd };
+// A thread's N pieces of E neighbouring channels: piece n begins at channel (n width + tid) E - odd.
+template <typename io_t, int E, int N, int KIND>
+struct Pieces {
+    static constexpr bool ODD = KIND == kOdd;
+    static constexpr bool FULL = KIND == kFull;
+    static constexpr int M = N * E;
+    typedef typename std::conditional<E * sizeof(io_t) == 16, uint4, unsigned>::type raw_t;
+    int first, step, count, last;   // channel of piece 0, from piece to piece, pieces, and (ODD) of second channels
+    __device__ __forceinline__ Pieces(int C, int width, int tid, int odd) {
+        first = tid * E - (ODD ? odd : 0);
+        step = width * E;
+        count = (C - first + step - 1) / step;   // (first is less than 32 M; C may be less)
+        last = ODD ? (C - first + step - 2) / step : count;
+        count = C > first ? count : 0;
+        last = ODD && C <= first + 1 ? 0 : last;
+    }
+    // pieces n, n + 1, .. of a thread that has more
+    template <int N2>
+    __device__ __forceinline__ Pieces(const Pieces<io_t, E, N2, KIND> &all, int n)
+        : first(all.first + n * all.step), step(all.step), count(all.count - n), last(all.last - n) {}
+    __device__ __forceinline__ int at(int n) const { return n * step + first; }
+    // whether element i (of M) is a channel of the row
+    __device__ __forceinline__ bool has(int i) const {
+        if (FULL) return true;
+        if (!ODD) return i / E < count;
+        return i % E ? i / E < last : i / E < count && (i || first >= 0);
+    }
+    __device__ __forceinline__ float pick(int i, float v) const { return has(i) ? v : 0.0f; }
+    __device__ __forceinline__ void load(const io_t *row, raw_t (&u)[N]) const {
+        const io_t *p = row + first;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (sizeof(io_t) == 4) {
-                    x[i] = __uint_as_float(w[i]);
-                } else {
-                    x[2 * i] = __uint_as_float(w[i] << 16);
-                    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-                }
+        for (int n = 0; n < N; ++n) {
+            if constexpr (FULL) u[n] = *reinterpret_cast<const raw_t *>(p + n * step);
+            else load_if(p + n * step, n < last, u[n]);
+            if constexpr (ODD) {
+                if (n == 0 && first < 0) u[n] &= 0xffff0000u;
+                if (n == last && n < count) load_half(p + n * step, u[n]);
             }
-        } else if constexpr (sizeof(io_t) == 4) {
-            x[0] = __uint_as_float(u);
-        } else {
-            x[0] = __uint_as_float((unsigned)u << 16);
-            if constexpr (E == 2) x[1] = __uint_as_float(u & 0xffff0000u);
         }
     }
-    __device__ __forceinline__ static void store(io_t *p, const float (&x)[E]) {
-        if constexpr (sizeof(io_t) == 4) {
-            if constexpr (E == 4) store4(p, x); else *p = x[0];
-        } else if constexpr (E == 1) {
-            *p = __float2bfloat16_rn(x[0]);
-        } else {
-            unsigned w[E / 2];
+    __device__ __forceinline__ static void wide(const raw_t (&u)[N], float (&x)[M]) {
 #pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-                w[i] = *reinterpret_cast<const unsigned *>(&h);
+        for (int n = 0; n < N; ++n) {
+            unsigned w[E * sizeof(io_t) / 4];
+            if constexpr (sizeof(raw_t) == 16) {
+                w[0] = u[n].x; w[1] = u[n].y; w[2] = u[n].z; w[3] = u[n].w;
+            } else {
+                w[0] = u[n];
             }
-            if constexpr (E == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-            else *reinterpret_cast<unsigned *>(p) = w[0];
+#pragma unroll
+            for (int i = 0; i < (int)(E * sizeof(io_t) / 4); ++i) {
+                if constexpr (sizeof(io_t) == 4) {
+                    x[n * E + i] = __uint_as_float(w[i]);
+                } else {
+                    x[n * E + 2 * i] = __uint_as_float(w[i] << 16);
+                    x[n * E + 2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ void store(io_t *row, const float (&x)[M]) const {
+        io_t *p = row + first;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            io_t *q = p + n * step;
+            if constexpr (sizeof(io_t) == 4) {
+                if (FULL || n < count) {
+                    if constexpr (E == 4)
+                        *reinterpret_cast<float4 *>(q) = make_float4(x[n * E], x[n * E + 1], x[n * E + 2], x[n * E + 3]);
+                    else
+                        *q = x[n];
+                }
+            } else {
+                unsigned w[E / 2];
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[n * E + 2 * i], x[n * E + 2 * i + 1]);
+                    w[i] = *reinterpret_cast<const unsigned *>(&h);
+                }
+                if constexpr (E == 8) {
+                    if (FULL || n < count) *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else if constexpr (!ODD) {
+                    if (n < count) *reinterpret_cast<unsigned *>(q) = w[0];
+                } else {
+                    if (n < last && (n || first >= 0)) *reinterpret_cast<unsigned *>(q) = w[0];
+                    else if (n < last) reinterpret_cast<unsigned short *>(q)[1] = (unsigned short)(w[0] >> 16);
+                    else if (n < count && (n || first >= 0)) *reinterpret_cast<unsigned short *>(q) = (unsigned short)w[0];
+                }
+            }
+        }
+    }
+    // of a weight or bias [C] fp32, or `other` without one
+    __device__ __forceinline__ void affine(const float *p, float other, float (&x)[M]) const {
+        const float *q = p + first;
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            if constexpr (E % 4 == 0) {
+#pragma unroll
+                for (int e = 0; e < E; e += 4) {
+                    float4 v = make_float4(other, other, other, other);
+                    if (p && (FULL || n < count)) v = *reinterpret_cast<const float4 *>(q + n * step + e);
+                    x[n * E + e] = v.x; x[n * E + e + 1] = v.y; x[n * E + e + 2] = v.z; x[n * E + e + 3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[n * E + e] = p && has(n * E + e) ? q[n * step + e] : other;
+            }
         }
     }
 };
-// E values of a weight or bias [C] fp32 at c, or `other` without one
-template <int E>
-__device__ __forceinline__ void affine(const float *p, int c, float other, float (&x)[E]) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = other;
-    if (!p) return;
-    if constexpr (E % 4 == 0) {
-#pragma unroll
-        for (int e = 0; e < E; e += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(p + c + e);
-            x[e] = v.x; x[e + 1] = v.y; x[e + 2] = v.z; x[e + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = p[c + e];
-    }
+
+// `bytes` of the W bytes at src (the rest: zeros) into shared memory, asynchronously.
+template <int W>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int bytes) {
+    if constexpr (W == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {   // all but the last N groups
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two values an instruction.
+__device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
+template <int M>
+__device__ __forceinline__ float2 get2(const float (&x)[M], int i) { return make_float2(x[i], x[i + 1]); }
+template <int M>
+__device__ __forceinline__ void put2(float (&x)[M], int i, float2 v) {
+    x[i] = v.x;
+    x[i + 1] = v.y;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -91,23 +180,36 @@ __device__ __forceinline__ float warp_sum(float v) {
     for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(kFullMask, v, m);
     return v;
 }
-// Sums of K values over the `warps` warps of a row, in a fixed order; `part` is the row's, of
-// [warps][K], and `bar` its barrier.
-template <int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], int warps, int warp, float *part, int bar) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = warp_sum(v[k]);
-    if (warps == 1) return;
-    if (threadIdx.x % 32 == 0) {
-#pragma unroll
-        for (int k = 0; k < K; ++k) part[warp * K + k] = v[k];
-    }
+// Sums over the `warps` warps of a row, in a fixed order; `part` is the row's, and `bar` its barrier.
+__device__ __forceinline__ float row_sum(float v, int warps, int warp, float *part, int bar) {
+    v = warp_sum(v);
+    if (warps == 1) return v;
+    if (threadIdx.x % 32 == 0) part[warp] = v;
     ptx::named_bar(bar, warps * 32);
+    v = 0.0f;
+    for (int w = 0; w < warps; ++w) v += part[w];
+    return v;
+}
+// Three at once: the first two exchanges halve what a lane carries (of four, one zero), so that six
+// shuffles do instead of fifteen; lanes 0 to 3 then hold one sum each.
+__device__ __forceinline__ float3 row_sum(float3 v, int warps, int warp, float4 *part, int bar) {
+    const int lane = threadIdx.x & 31;
+    const bool a = lane & 1, b = lane & 2;
+    const float x = a ? v.y : v.x, gx = a ? v.x : v.y, y = a ? 0.0f : v.z, gy = a ? v.z : 0.0f;
+    const float p = x + __shfl_xor_sync(kFullMask, gx, 1), q = y + __shfl_xor_sync(kFullMask, gy, 1);
+    float s = (b ? q : p) + __shfl_xor_sync(kFullMask, b ? p : q, 2);   // lane 0: x, 1: y, 2: z
 #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = 0.0f;
-    for (int w = 0; w < warps; ++w)
-#pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += part[w * K + k];
+    for (int m = 4; m < 32; m <<= 1) s += __shfl_xor_sync(kFullMask, s, m);
+    if (warps == 1)
+        return make_float3(__shfl_sync(kFullMask, s, 0), __shfl_sync(kFullMask, s, 1), __shfl_sync(kFullMask, s, 2));
+    if (lane < 4) reinterpret_cast<float *>(part + warp)[lane] = s;
+    ptx::named_bar(bar, warps * 32);
+    float3 t = make_float3(0.0f, 0.0f, 0.0f);
+    for (int w = 0; w < warps; ++w) {
+        const float4 u = part[w];
+        t = make_float3(t.x + u.x, t.y + u.y, t.z + u.z);
+    }
+    return t;
 }
 
 struct Params {
@@ -124,176 +226,217 @@ struct Params {
 constexpr int kMaxWarps = 32;
 
 // A row a group of p.warps warps; several groups a CTA where that is one warp.
-template <typename io_t, int E, int N, bool RES>
-__global__ void __launch_bounds__(N * E > 16 ? 512 : 1024) norm_kernel(Params p) {
+template <typename io_t, int E, int N, int KIND, bool RES>
+__global__ void __launch_bounds__(N * E == 8 ? 1024 : N * E == 16 ? 128 : 512) norm_kernel(Params p) {
+    typedef Pieces<io_t, E, N, KIND> P;
+    constexpr int M = P::M;
     __shared__ float part[2][kMaxWarps];
     const int width = p.warps * 32, tid = threadIdx.x % width;
     const long long row = (long long)blockIdx.x * (blockDim.x / width) + threadIdx.x / width;
     if (row >= p.rows) return;   // (a whole warp, and then a group of one)
     const size_t at = (size_t)row * p.C;
     const io_t *x = static_cast<const io_t *>(p.x) + at, *res = static_cast<const io_t *>(p.residual) + at;
-    Piece<io_t, E> px[N], pr[N];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const int c = (n * width + tid) * E;
-        px[n].zero();
-        pr[n].zero();
-        if (c < p.C) {
-            px[n].load(x + c);
-            if (RES) pr[n].load(res + c);
-        }
-    }
+    const P g(p.C, width, tid, (int)(at & 1));
+    typename P::raw_t rx[N], rr[N];
+    g.load(x, rx);
+    if (RES) g.load(res, rr);
     const float x0 = to_f32(x[0]) + (RES ? to_f32(res[0]) : 0.0f);
-    float v[N][E], k[1] = {0.0f};
+    float v[M];
+    float2 sum = two(0.0f);
+    P::wide(rx, v);
+    if (RES) {
+        float b[M];
+        P::wide(rr, b);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const int c = (n * width + tid) * E;
-        px[n].wide(v[n]);
-        if (RES) {
-            float b[E];
-            pr[n].wide(b);
+        for (int i = 0; i < M; i += 2) put2(v, i, __fadd2_rn(get2(v, i), get2(b, i)));
+        g.store(static_cast<io_t *>(p.sum) + at, v);
+    }
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[n][e] += b[e];
-            if (c < p.C) Piece<io_t, E>::store(static_cast<io_t *>(p.sum) + at + c, v[n]);
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            v[n][e] = c < p.C ? v[n][e] - x0 : 0.0f;
-            k[0] += v[n][e];
-        }
+    for (int i = 0; i < M; i += 2) {
+        put2(v, i, __fadd2_rn(get2(v, i), make_float2(g.pick(i, -x0), g.pick(i + 1, -x0))));
+        sum = __fadd2_rn(sum, get2(v, i));
     }
     const float inv = 1.0f / (float)p.C;
-    row_sum(k, p.warps, tid / 32, part[0], 1);
-    const float m = k[0] * inv;
-    k[0] = 0.0f;
+    const float m = row_sum(sum.x + sum.y, p.warps, tid / 32, part[0], 1) * inv;
+    sum = two(0.0f);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const int c = (n * width + tid) * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            v[n][e] = c < p.C ? v[n][e] - m : 0.0f;
-            k[0] = fmaf(v[n][e], v[n][e], k[0]);
-        }
+    for (int i = 0; i < M; i += 2) {
+        put2(v, i, __fadd2_rn(get2(v, i), make_float2(g.pick(i, -m), g.pick(i + 1, -m))));
+        sum = __ffma2_rn(get2(v, i), get2(v, i), sum);
     }
-    row_sum(k, p.warps, tid / 32, part[1], 1);
-    const float r = rsqrtf(fmaf(k[0], inv, p.eps));
+    const float r = rsqrtf(fmaf(row_sum(sum.x + sum.y, p.warps, tid / 32, part[1], 1), inv, p.eps));
+    float w[M], b[M];
+    g.affine(p.weight, 1.0f, w);
+    g.affine(p.bias, 0.0f, b);
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const int c = (n * width + tid) * E;
-        if (c >= p.C) continue;
-        float w[E], b[E];
-        affine<E>(p.weight, c, 1.0f, w);
-        affine<E>(p.bias, c, 0.0f, b);
-#pragma unroll
-        for (int e = 0; e < E; ++e) v[n][e] = fmaf(v[n][e] * r, w[e], b[e]);
-        Piece<io_t, E>::store(static_cast<io_t *>(p.y) + at + c, v[n]);
-    }
+    for (int i = 0; i < M; i += 2)
+        put2(v, i, __ffma2_rn(__fmul2_rn(get2(v, i), two(r)), get2(w, i), get2(b, i)));
+    g.store(static_cast<io_t *>(p.y) + at, v);
 }
 
 // Groups of p.warps warps walk rows; the sums over rows stay with the threads that own the columns,
-// in registers or (SMEM, wide rows) in shared memory, and end as one share a CTA.
-template <typename io_t, int E, int N, bool SMEM>
+// in registers or (SMEM, wide rows) in shared memory, and end as one share a CTA.  The next S rows are
+// on their way into shared memory meanwhile; a thread reads only what it copied itself.  With kOdd a
+// group keeps to rows of one parity, which begin in the same place of a word, so that its columns stay
+// its own.
+// Rows ahead, by what 227 KB of shared memory hold beside the sums (none: 16384 channels of fp32, which
+// are read when they are needed).
+template <typename io_t, int M>
+struct Ahead {
+    static constexpr bool kSmem = M == 32;
+    static constexpr int S = sizeof(io_t) * M <= 32 ? 3 : sizeof(io_t) * M <= 64 ? 1 : 0;
+    static constexpr int bytes(int threads) { return threads * M * (int)sizeof(io_t) * 3 * S; }   // of copies
+};
+template <typename io_t, int E, int N, int KIND>
 __global__ void __launch_bounds__(512) backward_kernel(Params p) {
-    extern __shared__ float sums[];   // [2][C]
-    __shared__ float part[2][3 * 16];
+    typedef Pieces<io_t, E, N, KIND> P;
+    typedef typename P::raw_t raw_t;
+    constexpr int M = P::M, S = Ahead<io_t, M>::S;
+    constexpr bool ODD = P::ODD, SMEM = Ahead<io_t, M>::kSmem;
+    constexpr int Q = E == 1 ? 2 : 1, EE = Q * E;   // pieces and values at a time
+    extern __shared__ __align__(16) char sm[];      // [S][3][N][threads] pieces, [2][C] sums
+    __shared__ float part0[16];
+    __shared__ float4 part1[16];
     const int width = p.warps * 32, groups = blockDim.x / width;
     const int group = threadIdx.x / width, tid = threadIdx.x % width, warp = tid / 32;
-    float *const part0 = part[0] + group * p.warps, *const part1 = part[1] + group * p.warps * 3;
     const float inv = 1.0f / (float)p.C;
-    float aw[N][E], ab[N][E];
+    const long long first = (long long)blockIdx.x * groups + group, all = (long long)gridDim.x * groups;
+    // an even number of groups with kOdd (a last one too many idles; alone it has one row)
+    const long long step = !ODD ? all : all > 1 ? all & ~1ll : 2;
+    const long long rows = ODD && all > 1 && first >= step ? 0 : p.rows;
+    const P g(p.C, width, tid, (int)(first & 1));
+    raw_t *const slot = reinterpret_cast<raw_t *>(sm) + threadIdx.x;
+    float *const sums = reinterpret_cast<float *>(sm + Ahead<io_t, M>::bytes(blockDim.x));
+    // tensor k (x, dy, ds) of a row into its place of stage s
+    const auto place = [&](int s, int k, int n) { return slot + ((s * 3 + k) * N + n) * (int)blockDim.x; };
+    const auto fetch = [&](const void *base, int s, int k, long long row) {
+        const io_t *q = static_cast<const io_t *>(base) + (size_t)row * p.C + g.first;
 #pragma unroll
-    for (int n = 0; n < N; ++n)
+        for (int n = 0; n < N; ++n) {
+            const int bytes = P::FULL || n < g.last ? (int)sizeof(raw_t) : ODD && n < g.count ? 2 : 0;
+            copy_async<sizeof(raw_t)>(ptx::smem_u32(place(s, k, n)), bytes ? q + n * g.step : base, bytes);
+        }
+    };
+    const auto fetch_x = [&](int s, long long row) {
+        if (S && row < rows) fetch(p.x, s, 0, row);
+        copies_commit();   // (a group even of nothing, so that waiting counts them)
+    };
+    const auto fetch_d = [&](int s, long long row) {
+        if (S && row < rows) {
+            fetch(p.dy, s, 1, row);
+            if (p.ds) fetch(p.ds, s, 2, row);
+        }
+        copies_commit();
+    };
+    const auto read = [&](int s, int k, int n, long long row, float (&v)[EE]) {
+        raw_t u[Q];
+        if constexpr (S == 0) {
+            const void *base = k == 0 ? p.x : k == 1 ? p.dy : p.ds;
+            Pieces<io_t, E, Q, KIND>(g, n).load(static_cast<const io_t *>(base) + (size_t)row * p.C, u);
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) aw[n][e] = ab[n][e] = 0.0f;
+            for (int i = 0; i < Q; ++i) u[i] = *place(s, k, n + i);
+            if constexpr (ODD)
+                if (n == 0 && g.first < 0) u[0] &= 0xffff0000u;
+        }
+        Pieces<io_t, E, Q, KIND>::wide(u, v);
+    };
+    float aw[M], ab[M], w[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) aw[i] = ab[i] = 0.0f;
+    if (!SMEM) g.affine(p.weight, 1.0f, w);
     for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) sums[c] = 0.0f;
     __syncthreads();
-    const long long step = (long long)gridDim.x * groups;
-    for (long long row = (long long)blockIdx.x * groups + group; row < p.rows; row += step) {
-        const size_t at = (size_t)row * p.C;
-        const io_t *x = static_cast<const io_t *>(p.x) + at, *dy = static_cast<const io_t *>(p.dy) + at;
-        const io_t *ds = static_cast<const io_t *>(p.ds) + at;
-        Piece<io_t, E> px[N], pd[N], ps[N];
+    float x0 = first < rows ? to_f32(static_cast<const io_t *>(p.x)[(size_t)first * p.C]) : 0.0f;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int c = (n * width + tid) * E;
-            px[n].zero();
-            pd[n].zero();
-            ps[n].zero();
-            if (c < p.C) {
-                px[n].load(x + c);
-                pd[n].load(dy + c);
-                if (p.ds) ps[n].load(ds + c);
+    for (int i = 0; i < S; ++i) {
+        fetch_x(i, first + i * step);
+        fetch_d(i, first + i * step);
+    }
+    int s = 0;
+    for (long long row = first; row < rows; row += step) {
+        float v[M];
+        float2 sum = two(0.0f);
+        copies_wait<S ? 2 * S - 1 : 0>();
+#pragma unroll
+        for (int n = 0; n < N; n += Q) {
+            float t[EE];
+            read(s, 0, n, row, t);
+#pragma unroll
+            for (int i = 0; i < EE; i += 2) {
+                const int o = n * E + i;
+                put2(v, o, __fadd2_rn(get2(t, i), make_float2(g.pick(o, -x0), g.pick(o + 1, -x0))));
+                sum = __fadd2_rn(sum, get2(v, o));
             }
         }
-        const float x0 = to_f32(x[0]);
-        float v[N][E], k[1] = {0.0f};
+        fetch_x(s, row + S * step);
+        if (row + step < rows) x0 = to_f32(static_cast<const io_t *>(p.x)[(size_t)(row + step) * p.C]);
+        const float m = row_sum(sum.x + sum.y, p.warps, warp, part0 + group * p.warps, 1 + group) * inv;
+        copies_wait<S ? 2 * S - 1 : 0>();
+        float2 q[3] = {two(0.0f), two(0.0f), two(0.0f)};   // sums of v^2, u and u v
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int c = (n * width + tid) * E;
-            px[n].wide(v[n]);
+        for (int n = 0; n < N; n += Q) {
+            float d[EE];
+            read(s, 1, n, row, d);
+            if (SMEM) Pieces<io_t, E, Q, KIND>(g, n).affine(p.weight, 1.0f, reinterpret_cast<float (&)[EE]>(w[n * E]));
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                v[n][e] = c < p.C ? v[n][e] - x0 : 0.0f;
-                k[0] += v[n][e];
+            for (int i = 0; i < EE; i += 2) {
+                const int o = n * E + i;
+                put2(v, o, __fadd2_rn(get2(v, o), make_float2(g.pick(o, -m), g.pick(o + 1, -m))));
+                const float2 u = __fmul2_rn(get2(d, i), get2(w, o));
+                q[0] = __ffma2_rn(get2(v, o), get2(v, o), q[0]);
+                q[1] = __fadd2_rn(q[1], u);
+                q[2] = __ffma2_rn(u, get2(v, o), q[2]);
             }
         }
-        row_sum(k, p.warps, warp, part0, 1 + group);
-        const float m = k[0] * inv;
-        float q[3] = {0.0f, 0.0f, 0.0f};   // sums of v^2, u and u v
+        const float3 t = row_sum(make_float3(q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y), p.warps, warp,
+                                 part1 + group * p.warps, 1 + group);
+        const float r = rsqrtf(fmaf(t.x, inv, p.eps)), mu = t.y * inv, mx = t.z * inv * r * r;
+        io_t *out = static_cast<io_t *>(p.dx) + (size_t)row * p.C;
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int c = (n * width + tid) * E;
-            float d[E], w[E];
-            pd[n].wide(d);
-            if (c < p.C) affine<E>(p.weight, c, 1.0f, w);
+        for (int n = 0; n < N; n += Q) {
+            float d[EE], e[EE];
+            read(s, 1, n, row, d);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                v[n][e] = c < p.C ? v[n][e] - m : 0.0f;
-                const float u = c < p.C ? __fmul_rn(d[e], w[e]) : 0.0f;
-                q[0] = fmaf(v[n][e], v[n][e], q[0]);
-                q[1] += u;
-                q[2] = fmaf(u, v[n][e], q[2]);
-            }
-        }
-        row_sum(q, p.warps, warp, part1, 1 + group);
-        const float r = rsqrtf(fmaf(q[0], inv, p.eps)), mu = q[1] * inv, mx = q[2] * inv * r * r;
+            for (int i = 0; i < EE; ++i) e[i] = 0.0f;
+            if (p.ds) read(s, 2, n, row, e);
+            if (SMEM) Pieces<io_t, E, Q, KIND>(g, n).affine(p.weight, 1.0f, reinterpret_cast<float (&)[EE]>(w[n * E]));
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-            const int c = (n * width + tid) * E;
-            if (c >= p.C) continue;
-            float d[E], w[E], s[E];
-            pd[n].wide(d);
-            ps[n].wide(s);
-            affine<E>(p.weight, c, 1.0f, w);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                // u rounded as in its mean, so that they cancel where they have to
-                s[e] = fmaf(r, fmaf(-v[n][e], mx, __fmul_rn(d[e], w[e]) - mu), s[e]);
+            for (int i = 0; i < EE; i += 2) {
+                const int o = n * E + i;
+                const float2 u = __fadd2_rn(__fmul2_rn(get2(d, i), get2(w, o)), two(-mu));
+                put2(e, i, __ffma2_rn(two(r), __ffma2_rn(get2(v, o), two(-mx), u), get2(e, i)));
+                const float2 xh = __fmul2_rn(get2(v, o), two(r));
                 if (SMEM) {
-                    sums[c + e] = fmaf(d[e], v[n][e] * r, sums[c + e]);
-                    sums[p.C + c + e] += d[e];
+                    const float2 f = __fmul2_rn(get2(d, i), xh);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        if (g.has(o + k)) {
+                            const int c = g.at((o + k) / E) + (o + k) % E;
+                            sums[c] += k ? f.y : f.x;
+                            sums[p.C + c] += d[i + k];
+                        }
                 } else {
-                    aw[n][e] = fmaf(d[e], v[n][e] * r, aw[n][e]);
-                    ab[n][e] += d[e];
+                    put2(aw, o, __ffma2_rn(get2(d, i), xh, get2(aw, o)));
+                    put2(ab, o, __fadd2_rn(get2(ab, o), get2(d, i)));
                 }
             }
-            Piece<io_t, E>::store(static_cast<io_t *>(p.dx) + at + c, s);
+            Pieces<io_t, E, Q, KIND>(g, n).store(out, e);
         }
+        fetch_d(s, row + S * step);
+        s = s + 1 >= S ? 0 : s + 1;
     }
     if (!p.columns) return;
     if (!SMEM) {
-        for (int g = 0; g < groups; ++g) {
-            if (g == group) {
+        for (int o = 0; o < groups; ++o) {
+            if (o == group) {
 #pragma unroll
-                for (int n = 0; n < N; ++n) {
-                    const int c = (n * width + tid) * E;
-                    if (c >= p.C) continue;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        sums[c + e] += aw[n][e];
-                        sums[p.C + c + e] += ab[n][e];
+                for (int i = 0; i < M; ++i)
+                    if (g.has(i)) {
+                        const int c = g.at(i / E) + i % E;
+                        sums[c] += aw[i];
+                        sums[p.C + c] += ab[i];
                     }
-                }
             }
             __syncthreads();
         }
@@ -330,55 +473,52 @@ int sm_count() {
     return n;
 }
 
-// Channels a piece: 16 bytes where every row starts on such a boundary, else a word where it starts on
-// one, else an element.
+// Channels a piece: 16 bytes where every row starts on such a boundary, else a word.
 int piece(int io, int C) {
     const int e = io == OSDN_F32 ? 4 : 2;
-    return C * e % 16 == 0 ? 16 / e : C * e % 4 == 0 ? 4 / e : 1;
+    return C * e % 16 == 0 ? 16 / e : 4 / e;
 }
 constexpr int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-// f(E tag, N tag) for M = N E values a thread
+// f(E tag, N tag, KIND tag) for M = N E values a thread
 template <int X>
 using Int = std::integral_constant<int, X>;
 template <typename io_t, int M, typename F>
-void with_pieces(int E, const F &f) {
-    constexpr int wide = 16 / (int)sizeof(io_t);
-    if (E == wide) f(Int<wide>(), Int<M / wide>());
-    else if (sizeof(io_t) == 2 && E == 2) f(Int<sizeof(io_t) == 2 ? 2 : 1>(), Int<sizeof(io_t) == 2 ? M / 2 : M>());
-    else f(Int<1>(), Int<M>());
+void with_pieces(int C, int E, int threads, const F &f) {
+    constexpr int wide = 16 / (int)sizeof(io_t), word = 4 / (int)sizeof(io_t);
+    if (E == wide && C == threads * M) f(Int<wide>(), Int<M / wide>(), Int<kFull>());
+    else if (E == wide) f(Int<wide>(), Int<M / wide>(), Int<kTail>());
+    else if (sizeof(io_t) == 4 || C % 2 == 0) f(Int<word>(), Int<M / word>(), Int<kTail>());
+    else f(Int<word>(), Int<M / word>(), Int<sizeof(io_t) == 2 ? kOdd : kTail>());
 }
 
 template <typename io_t, int M>
 cudaError_t forward(Params p, int E, cudaStream_t stream) {
-    p.warps = ceil_div(p.C, 32 * M);
+    p.warps = ceil_div(p.C + (p.C & 1), 32 * M);   // an odd row may begin inside a word
     const int groups = p.warps == 1 ? 4 : 1;
     const dim3 grid((unsigned)((p.rows + groups - 1) / groups));
-    with_pieces<io_t, M>(E, [&](auto e, auto n) {
-        constexpr int EE = decltype(e)::value, NN = decltype(n)::value;
-        if (p.residual) norm_kernel<io_t, EE, NN, true><<<grid, groups * p.warps * 32, 0, stream>>>(p);
-        else norm_kernel<io_t, EE, NN, false><<<grid, groups * p.warps * 32, 0, stream>>>(p);
+    with_pieces<io_t, M>(p.C, E, p.warps * 32, [&](auto e, auto n, auto kind) {
+        constexpr int EE = decltype(e)::value, NN = decltype(n)::value, K = decltype(kind)::value;
+        if (p.residual) norm_kernel<io_t, EE, NN, K, true><<<grid, groups * p.warps * 32, 0, stream>>>(p);
+        else norm_kernel<io_t, EE, NN, K, false><<<grid, groups * p.warps * 32, 0, stream>>>(p);
     });
     return cudaGetLastError();
 }
 template <typename io_t>
 cudaError_t forward_any(const Params &p, int E, cudaStream_t stream) {
     // few rows: more threads a row, so that each waits less
-    const bool few = p.rows <= 1024;
-    if (p.C <= 256 || (few && p.C <= 8192)) return forward<io_t, 8>(p, E, stream);
-    if (p.C <= 512 || few) return forward<io_t, 16>(p, E, stream);
+    if (p.C < 256 || (p.rows <= 1024 && p.C < 8192)) return forward<io_t, 8>(p, E, stream);
+    if (p.C < 512) return forward<io_t, 16>(p, E, stream);
     return forward<io_t, 32>(p, E, stream);
 }
 
 struct Cut {
     int M, warps, groups, ctas;
-    bool smem;
 };
-Cut cut(long long rows, int C) {
+Cut cut(int io, long long rows, int C) {
     Cut k;
-    k.M = C <= 256 ? 8 : C <= 8192 ? 16 : 32;
-    k.smem = k.M == 32;
-    k.warps = ceil_div(C, 32 * k.M);
+    k.M = C < (io == OSDN_F32 ? 4096 : 512) ? 8 : C <= 8192 - (C & 1) ? 16 : 32;
+    k.warps = ceil_div(C + (C & 1), 32 * k.M);
     k.groups = 16 / k.warps;
     k.ctas = (int)std::min<long long>(sm_count(), (rows + k.groups - 1) / k.groups);
     return k;
@@ -387,12 +527,14 @@ Cut cut(long long rows, int C) {
 template <typename io_t, int M>
 cudaError_t backward(const Params &p, const Cut &k, int E, cudaStream_t stream) {
     cudaError_t r = cudaSuccess;
-    with_pieces<io_t, M>(E, [&](auto e, auto n) {
-        auto *kernel = backward_kernel<io_t, decltype(e)::value, decltype(n)::value, M == 32>;
+    with_pieces<io_t, M>(p.C, E, p.warps * 32, [&](auto e, auto n, auto kind) {
+        auto *kernel = backward_kernel<io_t, decltype(e)::value, decltype(n)::value, decltype(kind)::value>;
         static std::atomic<unsigned long long> done{0};
-        r = smem_attr_once(reinterpret_cast<const void *>(kernel), 2 * 16384 * 4, done);
+        r = smem_attr_once(reinterpret_cast<const void *>(kernel),
+                           Ahead<io_t, M>::bytes(512) + (M == 32 ? 16384 : M == 16 || sizeof(io_t) == 2 ? 8192 : 4096) * 8, done);
         if (r == cudaSuccess) {
-            kernel<<<k.ctas, k.groups * k.warps * 32, (size_t)p.C * 8, stream>>>(p);
+            const int threads = k.groups * k.warps * 32;
+            kernel<<<k.ctas, threads, Ahead<io_t, M>::bytes(threads) + (size_t)p.C * 8, stream>>>(p);
             r = cudaGetLastError();
         }
     });
@@ -401,7 +543,9 @@ cudaError_t backward(const Params &p, const Cut &k, int E, cudaStream_t stream) 
 
 }  // namespace
 
-size_t backward_scratch_bytes(long long rows, int C) { return (size_t)cut(rows, C).ctas * C * 8; }
+size_t backward_scratch_bytes(long long rows, int C) {   // (the shares of either I/O type)
+    return (size_t)std::max(cut(OSDN_F32, rows, C).ctas, cut(OSDN_BF16, rows, C).ctas) * C * 8;
+}
 
 cudaError_t norm_launch(int io, long long rows, int C, const void *x, const void *residual, const float *weight,
                         const float *bias, float eps, void *y, void *sum, cudaStream_t stream) {
@@ -417,7 +561,7 @@ cudaError_t backward_launch(int io, long long rows, int C, const void *x, const 
                             const void *ds, float eps, void *dx, float *dweight, float *dbias, void *scratch,
                             cudaStream_t stream) {
     Params p = {};
-    const Cut k = cut(rows, C);
+    const Cut k = cut(io, rows, C);
     p.rows = rows; p.C = C; p.eps = eps; p.warps = k.warps;
     p.x = x; p.dy = dy; p.ds = ds; p.weight = weight;
     p.dx = dx;
