@@ -190,26 +190,28 @@ __device__ __forceinline__ float row_sum(float v, int warps, int warp, float *pa
     for (int w = 0; w < warps; ++w) v += part[w];
     return v;
 }
-// Three at once: the first two exchanges halve what a lane carries (of four, one zero), so that six
-// shuffles do instead of fifteen; lanes 0 to 3 then hold one sum each.
-__device__ __forceinline__ float3 row_sum(float3 v, int warps, int warp, float4 *part, int bar) {
+// Four at once: the first two exchanges halve what a lane carries, so that six shuffles do instead of
+// twenty; lanes 0 to 3 then hold one sum each.
+__device__ __forceinline__ float4 row_sum(float4 v, int warps, int warp, float4 *part, int bar) {
     const int lane = threadIdx.x & 31;
     const bool a = lane & 1, b = lane & 2;
-    const float x = a ? v.y : v.x, gx = a ? v.x : v.y, y = a ? 0.0f : v.z, gy = a ? v.z : 0.0f;
-    const float p = x + __shfl_xor_sync(kFullMask, gx, 1), q = y + __shfl_xor_sync(kFullMask, gy, 1);
-    float s = (b ? q : p) + __shfl_xor_sync(kFullMask, b ? p : q, 2);   // lane 0: x, 1: y, 2: z
+    const float p = (a ? v.y : v.x) + __shfl_xor_sync(kFullMask, a ? v.x : v.y, 1);
+    const float q = (a ? v.w : v.z) + __shfl_xor_sync(kFullMask, a ? v.z : v.w, 1);
+    float s = (b ? q : p) + __shfl_xor_sync(kFullMask, b ? p : q, 2);   // lane 0: x, 1: y, 2: z, 3: w
 #pragma unroll
     for (int m = 4; m < 32; m <<= 1) s += __shfl_xor_sync(kFullMask, s, m);
     if (warps == 1)
-        return make_float3(__shfl_sync(kFullMask, s, 0), __shfl_sync(kFullMask, s, 1), __shfl_sync(kFullMask, s, 2));
+        return make_float4(__shfl_sync(kFullMask, s, 0), __shfl_sync(kFullMask, s, 1), __shfl_sync(kFullMask, s, 2),
+                           __shfl_sync(kFullMask, s, 3));
     if (lane < 4) reinterpret_cast<float *>(part + warp)[lane] = s;
     ptx::named_bar(bar, warps * 32);
-    float3 t = make_float3(0.0f, 0.0f, 0.0f);
+    float2 t = two(0.0f), u = two(0.0f);
     for (int w = 0; w < warps; ++w) {
-        const float4 u = part[w];
-        t = make_float3(t.x + u.x, t.y + u.y, t.z + u.z);
+        const float4 o = part[w];
+        t = __fadd2_rn(t, make_float2(o.x, o.y));
+        u = __fadd2_rn(u, make_float2(o.z, o.w));
     }
-    return t;
+    return make_float4(t.x, t.y, u.x, u.y);
 }
 
 struct Params {
@@ -295,8 +297,7 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
     constexpr bool ODD = P::ODD, SMEM = Ahead<io_t, M>::kSmem;
     constexpr int Q = E == 1 ? 2 : 1, EE = Q * E;   // pieces and values at a time
     extern __shared__ __align__(16) char sm[];      // [S][3][N][threads] pieces, [2][C] sums
-    __shared__ float part0[16];
-    __shared__ float4 part1[16];
+    __shared__ float4 part[2][16];   // (one for even and one for odd rows of a group)
     const int width = p.warps * 32, groups = blockDim.x / width;
     const int group = threadIdx.x / width, tid = threadIdx.x % width, warp = tid / 32;
     const float inv = 1.0f / (float)p.C;
@@ -309,30 +310,33 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
     float *const sums = reinterpret_cast<float *>(sm + Ahead<io_t, M>::bytes(blockDim.x));
     // tensor k (x, dy, ds) of a row into its place of stage s
     const auto place = [&](int s, int k, int n) { return slot + ((s * 3 + k) * N + n) * (int)blockDim.x; };
-    const auto fetch = [&](const void *base, int s, int k, long long row) {
-        const io_t *q = static_cast<const io_t *>(base) + (size_t)row * p.C + g.first;
+    const io_t *const x = static_cast<const io_t *>(p.x) + g.first, *const dy = static_cast<const io_t *>(p.dy) + g.first;
+    const io_t *const ds = p.ds ? static_cast<const io_t *>(p.ds) + g.first : nullptr;
+    const auto fetch = [&](const io_t *base, int s, int k, size_t at) {
+        const uint32_t to = ptx::smem_u32(place(s, k, 0));
 #pragma unroll
         for (int n = 0; n < N; ++n) {
             const int bytes = P::FULL || n < g.last ? (int)sizeof(raw_t) : ODD && n < g.count ? 2 : 0;
-            copy_async<sizeof(raw_t)>(ptx::smem_u32(place(s, k, n)), bytes ? q + n * g.step : base, bytes);
+            const io_t *q = base + at + n * g.step;
+            if (!P::FULL && !bytes) q = base - g.first;
+            copy_async<sizeof(raw_t)>(to + n * (unsigned)(blockDim.x * sizeof(raw_t)), q, bytes);
         }
     };
-    const auto fetch_x = [&](int s, long long row) {
-        if (S && row < rows) fetch(p.x, s, 0, row);
+    const size_t far = (size_t)step * p.C;   // elements from a group's row to its next
+    size_t at = (size_t)first * p.C;
+    const auto fetch_row = [&](int s, long long row, size_t from) {
+        if (S && row < rows) {
+            fetch(x, s, 0, from);
+            fetch(dy, s, 1, from);
+            if (ds) fetch(ds, s, 2, from);
+        }
         copies_commit();   // (a group even of nothing, so that waiting counts them)
     };
-    const auto fetch_d = [&](int s, long long row) {
-        if (S && row < rows) {
-            fetch(p.dy, s, 1, row);
-            if (p.ds) fetch(p.ds, s, 2, row);
-        }
-        copies_commit();
-    };
-    const auto read = [&](int s, int k, int n, long long row, float (&v)[EE]) {
+    const auto read = [&](int s, int k, int n, float (&v)[EE]) {
         raw_t u[Q];
         if constexpr (S == 0) {
             const void *base = k == 0 ? p.x : k == 1 ? p.dy : p.ds;
-            Pieces<io_t, E, Q, KIND>(g, n).load(static_cast<const io_t *>(base) + (size_t)row * p.C, u);
+            Pieces<io_t, E, Q, KIND>(g, n).load(static_cast<const io_t *>(base) + at, u);
         } else {
 #pragma unroll
             for (int i = 0; i < Q; ++i) u[i] = *place(s, k, n + i);
@@ -341,74 +345,97 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
         }
         Pieces<io_t, E, Q, KIND>::wide(u, v);
     };
+    // a row's first value: of the row in stage s, which the group's first thread has copied, or from `from`
+    const auto pivot = [&](int s, long long row, size_t from) {
+        if (row >= rows) return 0.0f;
+        if constexpr (S <= 1) return to_f32(static_cast<const io_t *>(p.x)[from]);
+        const raw_t *q = place(s, 0, 0) - tid;
+        return to_f32(reinterpret_cast<const io_t *>(q)[ODD ? (int)(from & 1) : 0]);
+    };
     float aw[M], ab[M], w[M];
 #pragma unroll
     for (int i = 0; i < M; ++i) aw[i] = ab[i] = 0.0f;
     if (!SMEM) g.affine(p.weight, 1.0f, w);
     for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) sums[c] = 0.0f;
     __syncthreads();
-    float x0 = first < rows ? to_f32(static_cast<const io_t *>(p.x)[(size_t)first * p.C]) : 0.0f;
+    float x0 = first < rows ? to_f32(static_cast<const io_t *>(p.x)[at]) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        fetch_x(i, first + i * step);
-        fetch_d(i, first + i * step);
-    }
-    int s = 0;
-    for (long long row = first; row < rows; row += step) {
+    for (int i = 0; i < S; ++i) fetch_row(i, first + i * step, at + i * far);
+    int s = 0, odd = 0;
+    for (long long row = first; row < rows; row += step, at += far, odd ^= 1) {
+        const int next = s + 1 >= S ? 0 : s + 1;
         float v[M];
-        float2 sum = two(0.0f);
-        copies_wait<S ? 2 * S - 1 : 0>();
+        float2 q[4] = {two(0.0f), two(0.0f), two(0.0f), two(0.0f)};   // sums of v, v^2, u and u v
+        copies_wait<(S > 1 ? S - 2 : 0)>();   // this row's and the next one's (for its pivot)
 #pragma unroll
         for (int n = 0; n < N; n += Q) {
-            float t[EE];
-            read(s, 0, n, row, t);
+            float t[EE], d[EE];
+            read(s, 0, n, t);
+            read(s, 1, n, d);
+            if (SMEM) Pieces<io_t, E, Q, KIND>(g, n).affine(p.weight, 1.0f, reinterpret_cast<float (&)[EE]>(w[n * E]));
 #pragma unroll
             for (int i = 0; i < EE; i += 2) {
                 const int o = n * E + i;
                 put2(v, o, __fadd2_rn(get2(t, i), make_float2(g.pick(o, -x0), g.pick(o + 1, -x0))));
-                sum = __fadd2_rn(sum, get2(v, o));
-            }
-        }
-        fetch_x(s, row + S * step);
-        if (row + step < rows) x0 = to_f32(static_cast<const io_t *>(p.x)[(size_t)(row + step) * p.C]);
-        const float m = row_sum(sum.x + sum.y, p.warps, warp, part0 + group * p.warps, 1 + group) * inv;
-        copies_wait<S ? 2 * S - 1 : 0>();
-        float2 q[3] = {two(0.0f), two(0.0f), two(0.0f)};   // sums of v^2, u and u v
-#pragma unroll
-        for (int n = 0; n < N; n += Q) {
-            float d[EE];
-            read(s, 1, n, row, d);
-            if (SMEM) Pieces<io_t, E, Q, KIND>(g, n).affine(p.weight, 1.0f, reinterpret_cast<float (&)[EE]>(w[n * E]));
-#pragma unroll
-            for (int i = 0; i < EE; i += 2) {
-                const int o = n * E + i;
-                put2(v, o, __fadd2_rn(get2(v, o), make_float2(g.pick(o, -m), g.pick(o + 1, -m))));
                 const float2 u = __fmul2_rn(get2(d, i), get2(w, o));
-                q[0] = __ffma2_rn(get2(v, o), get2(v, o), q[0]);
-                q[1] = __fadd2_rn(q[1], u);
-                q[2] = __ffma2_rn(u, get2(v, o), q[2]);
+                q[0] = __fadd2_rn(q[0], get2(v, o));
+                q[1] = __ffma2_rn(get2(v, o), get2(v, o), q[1]);
+                q[2] = __fadd2_rn(q[2], u);
+                q[3] = __ffma2_rn(u, get2(v, o), q[3]);
             }
         }
-        const float3 t = row_sum(make_float3(q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y), p.warps, warp,
-                                 part1 + group * p.warps, 1 + group);
-        const float r = rsqrtf(fmaf(t.x, inv, p.eps)), mu = t.y * inv, mx = t.z * inv * r * r;
-        io_t *out = static_cast<io_t *>(p.dx) + (size_t)row * p.C;
+        float4 t = row_sum(make_float4(q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y, q[3].x + q[3].y), p.warps,
+                           warp, part[odd] + group * p.warps, 1 + group);
+        const float m = t.x * inv, mu = t.z * inv;
+        float var = fmaf(-m, m, t.y * inv), uv = fmaf(-m, t.z, t.w) * inv;
+        if (!(m * m <= 16.0f * var)) {
+            // the first value lies far outside the others: the differences above have lost digits, so the
+            // sums are taken again about the mean (by the whole group, which sees the same sums)
+            float2 z[2] = {two(0.0f), two(0.0f)};
+#pragma unroll
+            for (int n = 0; n < N; n += Q) {
+                float d[EE];
+                read(s, 1, n, d);
+#pragma unroll
+                for (int i = 0; i < EE; i += 2) {
+                    const int o = n * E + i;
+                    const float2 c = __fadd2_rn(get2(v, o), make_float2(g.pick(o, -m), g.pick(o + 1, -m)));
+                    z[0] = __ffma2_rn(c, c, z[0]);
+                    z[1] = __ffma2_rn(__fmul2_rn(get2(d, i), get2(w, o)), c, z[1]);
+                }
+            }
+            if (p.warps > 1) ptx::named_bar(1 + group, width);   // all have read the sums above
+            t = row_sum(make_float4(z[0].x + z[0].y, z[1].x + z[1].y, 0.0f, 0.0f), p.warps, warp,
+                        part[odd] + group * p.warps, 1 + group);
+            var = t.x * inv;
+            uv = t.y * inv;
+        }
+        if (S > 1) {
+            if (p.warps == 1) __syncwarp();
+            x0 = pivot(next, row + step, at + far);   // (past a barrier that the copying thread has passed)
+        } else {
+            x0 = pivot(0, row + step, at + far);
+        }
+        // x^ = r v - r m,  dx = r u + k v + k0
+        const float r = rsqrtf(var + p.eps), rm = -r * m, kx = -uv * r * r * r, k0 = fmaf(-kx, m, -r * mu);
+        io_t *out = static_cast<io_t *>(p.dx) + at;
 #pragma unroll
         for (int n = 0; n < N; n += Q) {
             float d[EE], e[EE];
-            read(s, 1, n, row, d);
-#pragma unroll
-            for (int i = 0; i < EE; ++i) e[i] = 0.0f;
-            if (p.ds) read(s, 2, n, row, e);
+            read(s, 1, n, d);
+            if (ds) read(s, 2, n, e);
             if (SMEM) Pieces<io_t, E, Q, KIND>(g, n).affine(p.weight, 1.0f, reinterpret_cast<float (&)[EE]>(w[n * E]));
 #pragma unroll
             for (int i = 0; i < EE; i += 2) {
                 const int o = n * E + i;
-                const float2 u = __fadd2_rn(__fmul2_rn(get2(d, i), get2(w, o)), two(-mu));
-                put2(e, i, __ffma2_rn(two(r), __ffma2_rn(get2(v, o), two(-mx), u), get2(e, i)));
-                const float2 xh = __fmul2_rn(get2(v, o), two(r));
+                const float2 u = __fmul2_rn(get2(d, i), get2(w, o));
+                float2 f = __ffma2_rn(get2(v, o), two(kx), two(k0));
+                f = __ffma2_rn(u, two(r), f);
+                if (ds) f = __fadd2_rn(f, get2(e, i));
+                put2(e, i, f);
+                const float2 xh = __ffma2_rn(get2(v, o), two(r), two(rm));
                 if (SMEM) {
-                    const float2 f = __fmul2_rn(get2(d, i), xh);
+                    f = __fmul2_rn(get2(d, i), xh);
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         if (g.has(o + k)) {
@@ -423,8 +450,8 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
             }
             Pieces<io_t, E, Q, KIND>(g, n).store(out, e);
         }
-        fetch_d(s, row + S * step);
-        s = s + 1 >= S ? 0 : s + 1;
+        fetch_row(s, row + S * step, at + S * far);
+        s = next;
     }
     if (!p.columns) return;
     if (!SMEM) {
