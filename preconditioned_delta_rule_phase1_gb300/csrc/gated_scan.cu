@@ -172,19 +172,27 @@ struct Join {
 };
 // From every thread's (A, E) and the state s that enters the step: the state before the thread's
 // first token.  s becomes the state after the step.  `place`: the warp's turn in the recurrence;
-// `zeros`: whether a factor of this warp may be exactly zero.
-template <int V>
+// `zeros`: whether a factor of this warp may be exactly zero.  `meanwhile()` runs while the cluster's
+// CTAs wait for one another.
+template <int V, typename F>
 __device__ __forceinline__ Vec<V> join(Join<V> &j, int set, int n, int rank, int place, bool zeros, const Pair<V> &own,
-                                       Vec<V> &s) {
+                                       Vec<V> &s, const F &meanwhile) {
     const int lane = threadIdx.x & 31;
     j.warp[set][place][lane] = own;
     const bool any = __syncthreads_or(zeros);
+    // what lies before this warp in the CTA, and what the CTA does in all
+    Pair<V> before = {fill<V>(1.0f), fill<V>(0.0f)}, total = before;
+    const auto fold = [&](auto z) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == place) before = total;
+            total.template then<decltype(z)::value>(j.warp[set][w][lane]);
+        }
+    };
+    if (any) fold(std::true_type()); else fold(std::false_type());
+    Vec<V> mine = s;
     if (n > 1) {
         if (place == kWarps - 1) {   // the CTA's total, to every CTA of the cluster
-            Pair<V> total = j.warp[set][0][lane];
-#pragma unroll
-            for (int w = 1; w < kWarps - 1; ++w) total.template then<true>(j.warp[set][w][lane]);
-            total.template then<true>(own);
             for (int r = 0; r < n; ++r) {
                 const uint32_t at = ptx::cluster_map(&j.total[set][rank][lane], r);
                 if constexpr (V == 2)
@@ -193,28 +201,23 @@ __device__ __forceinline__ Vec<V> join(Join<V> &j, int set, int n, int rank, int
                     ptx::cluster_store(at, make_float2(total.A.v[0], total.E.v[0]));
             }
         }
-        ptx::cluster_arrive();
+        // Only the last warp has written for the others.  What every warp has read of an earlier step
+        // comes before it, by the barrier of the CTA.
+        __syncwarp();
+        if (place == kWarps - 1) ptx::cluster_arrive(); else ptx::cluster_arrive_relaxed();
+        meanwhile();
         ptx::cluster_wait();
-    }
-    Vec<V> mine = s;
-    if (n > 1) {
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r)
             if (r < n) {
                 if (r == rank) mine = s;
                 j.total[set][r][lane].template apply<true>(s);
             }
+    } else {
+        meanwhile();
+        total.template apply<true>(s);
     }
-    Vec<V> q = mine;
-    const auto fold = [&](auto z) {
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == place) mine = q;
-            j.warp[set][w][lane].template apply<decltype(z)::value>(q);
-        }
-    };
-    if (any) fold(std::true_type()); else fold(std::false_type());
-    if (n == 1) s = q;
+    before.template apply<true>(mine);
     return mine;
 }
 
@@ -331,8 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
             }
         }
         __syncwarp();   // the stage is read
-        fetch(step, kStages);
-        Vec<V> q = join<V>(j, step & 1, k.n, k.rank, k.warp, !usual, Pair<V>{A, E}, s);
+        Vec<V> q = join<V>(j, step & 1, k.n, k.rank, k.warp, !usual, Pair<V>{A, E}, s, [&] { fetch(step, kStages); });
         char *out = reinterpret_cast<char *>(static_cast<io_t *>(p.out) + k.at + k.lane * V);
         const auto run = [&](auto z) {
             constexpr bool Z = decltype(z)::value;
@@ -458,9 +460,10 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
             }
         }
         __syncwarp();
-        fetch(step, kStages);
-        row = before(k.t0 - k.stride, k.at - far);
-        Vec<V> q = join<V>(j, step & 1, k.n, k.rank, kWarps - 1 - k.warp, !usual, Pair<V>{A, E}, s);
+        Vec<V> q = join<V>(j, step & 1, k.n, k.rank, kWarps - 1 - k.warp, !usual, Pair<V>{A, E}, s, [&] {
+            fetch(step, kStages);
+            row = before(k.t0 - k.stride, k.at - far);
+        });
         char *dx = reinterpret_cast<char *>(static_cast<io_t *>(p.out) + k.at + k.lane * V);
         char *dg = reinterpret_cast<char *>(static_cast<io_t *>(p.dgate) + k.at + k.lane * V);
         const auto run = [&](auto z) {
