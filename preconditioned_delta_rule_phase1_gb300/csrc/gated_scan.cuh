@@ -132,27 +132,30 @@ __device__ __forceinline__ float weighted(float c, float x) {
     if (Z && passes(c)) return 0.0f;
     return weight<MIX>(c) * x;
 }
-// With v the state before a token: the factors that turn R into the gradients, w for x and
-// a b v + w' x = a b (v - k x) for g, where k is 0, 1 or a / w.  (w' = -a / w times a b, and k a b =
-// a^2 sqrt((1 - a) / (1 + a)) goes to zero where w does.)
+// With v the state before a token: the factor that turns R into the gradient of g, a b v + w' x =
+// a b (v - k x), where k is 0, 1 or a / w.  (w' = -a / w times a b, and k a b = a^2 sqrt((1 - a) /
+// (1 + a)) goes to zero where w does.)
 template <int MIX, bool Z>
-__device__ __forceinline__ void slopes(float c, float v, float x, float &w, float &slope) {
+__device__ __forceinline__ float slope_of(float c, float v, float x) {
     const float s = fabsf(c), ab = fmaf(-s, s, s);
-    w = weight<MIX>(c);
     if (MIX == OSDN_MIX_MEAN) v -= x;
     if (MIX == OSDN_MIX_UNIT)
         v = fmaf(-(keeps(c) ? 1.0f + c : c) * rsqrt_fast(fmaxf(unit_square(c), 1e-37f)), x, v);
-    slope = Z && ab == 0.0f ? 0.0f : ab * v;
+    return Z && ab == 0.0f ? 0.0f : ab * v;
 }
 
 // ------------------------------------------------------------- the short form
 constexpr float kPlainGate = 80.0f;   // e^80 and its reciprocal are normal numbers
-// a and b = 1 - a
+// e^-g, and from it a and b = 1 - a
 template <int V>
-__device__ __forceinline__ void sigmoids(const Vec<V> &g, Vec<V> &a, Vec<V> &b) {
+__device__ __forceinline__ Vec<V> exponentials(const Vec<V> &g) {
     Vec<V> e = mul(g, fill<V>(-kLog2e));
 #pragma unroll
     for (int i = 0; i < V; ++i) e.v[i] = exp2_fast(e.v[i]);
+    return e;
+}
+template <int V>
+__device__ __forceinline__ void sigmoids(const Vec<V> &e, Vec<V> &a, Vec<V> &b) {
     a = add(e, fill<V>(1.0f));
 #pragma unroll
     for (int i = 0; i < V; ++i) a.v[i] = rcp_fast(a.v[i]);
@@ -167,25 +170,27 @@ __device__ __forceinline__ Vec<V> weight(const Vec<V> &a, const Vec<V> &b) {
     for (int i = 0; i < V; ++i) w.v[i] = sqrt_fast(w.v[i]);
     return w;
 }
+// The same factor; v becomes the state after the token.
 template <int MIX, int V>
-__device__ __forceinline__ void slopes(const Vec<V> &a, const Vec<V> &b, const Vec<V> &v, const Vec<V> &x, Vec<V> &w,
-                                       Vec<V> &slope) {
+__device__ __forceinline__ Vec<V> slope_and_next(const Vec<V> &a, const Vec<V> &b, const Vec<V> &x, Vec<V> &v) {
     const Vec<V> ab = mul(a, b);
+    Vec<V> slope;
     if (MIX == OSDN_MIX_SUM) {
-        w = fill<V>(1.0f);
         slope = mul(ab, v);
+        v = fma(v, a, x);
     } else if (MIX == OSDN_MIX_MEAN) {
-        w = b;
         slope = mul(ab, fma(x, fill<V>(-1.0f), v));
+        v = fma(v, a, mul(b, x));
     } else {
-        const Vec<V> q = add(ab, b);
+        const Vec<V> q = add(ab, b);   // w^2
         Vec<V> k;
 #pragma unroll
         for (int i = 0; i < V; ++i) k.v[i] = rsqrt_fast(q.v[i]);
-        w = mul(q, k);
-        k = mul(mul(a, k), x);
-        slope = mul(ab, fma(k, fill<V>(-1.0f), v));
+        const Vec<V> xk = mul(k, x);
+        slope = mul(ab, fma(mul(a, xk), fill<V>(-1.0f), v));
+        v = fma(v, a, mul(q, xk));
     }
+    return slope;
 }
 
 }  // namespace gs

@@ -1,0 +1,187 @@
+// gated_scan_backward.cu -- the gradients of the gated recurrence; gated_scan.cu
+// has the formulas and the design.
+#include "gated_scan_walk.cuh"
+
+namespace osdn {
+namespace gs {
+
+namespace {
+
+// Backwards in time: steps, CTAs, warps and tokens from the last to the first.  The states are
+// recomputed from the row of h in front of the warp's tokens, so that one row in R of h is read.  A
+// thread's own (A, E) is gathered on the same way forwards: Q before its tokens is A Q + E with A the
+// product of their a and E the sum of their dh, each times the product of the a up to it.
+template <typename io_t, int MIX, int R, int W>
+__global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
+    typedef typename Raw<io_t>::type raw_t;
+    constexpr int V = 2;
+    constexpr bool kShort = sizeof(io_t) == 2;
+    extern __shared__ __align__(16) char sm[];
+    __shared__ Join j;
+    Walk<io_t, R, W, 3> k(p, sm, true);
+    typedef Rows<io_t, R, W> rows;
+    const size_t state = (size_t)k.b * p.C + k.c;
+    if (k.n > 1) ptx::cluster_arrive();   // every CTA of the cluster has started once all have arrived
+    Vec<V> s = fill<V>(0.0f);
+    if (p.first && k.live)
+#pragma unroll
+        for (int v = 0; v < V; ++v) s.v[v] = p.first[state + v];
+    const size_t far = (size_t)k.stride * p.C;
+    const auto fetch = [&](int step, int ahead) {
+        if (step + ahead < p.steps) {
+            const size_t from = k.at - ahead * far;
+            const int tokens = p.T - k.t0 + ahead * k.stride;
+            k.fetch((step + ahead) % kStages, 0, p.gate, from, tokens);
+            k.fetch((step + ahead) % kStages, 1, p.x, from, tokens);
+            k.fetch((step + ahead) % kStages, 2, p.dh, from, tokens);
+        }
+        copies_commit();
+    };
+    // the state before token t, where that is one of this lane's
+    const auto before = [&](int t, size_t at) {
+        raw_t u = raw_t();
+        if (k.live && t > 0 && t < p.T) {
+            const io_t *q = static_cast<const io_t *>(p.h) + at - p.C + k.lane * 2;
+            if constexpr (rows::kPaired) {
+                u = *reinterpret_cast<const raw_t *>(q);
+            } else if constexpr (sizeof(io_t) == 4) {
+                u.x = reinterpret_cast<const unsigned *>(q)[0];
+                if (k.second) u.y = reinterpret_cast<const unsigned *>(q)[1];
+            } else {
+                u = reinterpret_cast<const unsigned short *>(q)[0];
+                if (k.second) u |= (unsigned)reinterpret_cast<const unsigned short *>(q)[1] << 16;
+            }
+        }
+        return u;
+    };
+    raw_t row = before(k.t0, k.at);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch(0, i);
+    if (k.n > 1) ptx::cluster_wait();
+    for (int step = 0; step < p.steps; ++step) {
+        copies_wait<kStages - 1>();
+        __syncwarp();
+        const int tokens = p.T - k.t0, odd = k.odd(p.gate), oddx = k.odd(p.x), oddd = k.odd(p.dh);
+        const char *gate = k.tile(step % kStages, 0), *xs = k.tile(step % kStages, 1), *ds = k.tile(step % kStages, 2);
+        float most = 0.0f;
+        raw_t rg[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            rg[i] = rows::get(gate, i, odd);
+            const Vec<V> g = wide(rg[i]);
+#pragma unroll
+            for (int v = 0; v < V; ++v) most = fmaxf(most, fabsf(g.v[v]));
+        }
+        const bool usual = __all_sync(kFullMask, tokens >= R && (most <= kPlainGate || !k.live));
+        Vec<V> h = wide(row);
+        if (k.t0 == 0) h = k.load_state(p, p.h0);
+        Vec<V> co[R], slope[R];   // (co: c, or e^-g in the short form)
+        raw_t d[R];
+        Vec<V> A = fill<V>(1.0f), E = fill<V>(0.0f);
+        const auto exact = [&](auto z) {
+            constexpr bool Z = decltype(z)::value;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const Vec<V> g = wide(rg[i]), x = wide(rows::get(xs, i, oddx));
+                d[i] = rows::get(ds, i, oddd);
+                const Vec<V> di = wide(d[i]);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    co[i].v[v] = !Z || i < tokens ? gate_coefficient(g.v[v]) : -0.0f;
+                    slope[i].v[v] = slope_of<MIX, Z>(co[i].v[v], h.v[v], x.v[v]);
+                    h.v[v] = decay<Z>(co[i].v[v], h.v[v]) + (!Z || i < tokens ? weighted<MIX, Z>(co[i].v[v], x.v[v]) : 0.0f);
+                    A.v[v] = decay<Z>(co[i].v[v], A.v[v]);
+                    E.v[v] = Z && A.v[v] == 0.0f ? E.v[v] : fmaf(A.v[v], di.v[v], E.v[v]);
+                }
+            }
+        };
+        if (!usual) {
+            exact(std::true_type());
+        } else if constexpr (!kShort) {
+            exact(std::false_type());
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                Vec<V> a, f;
+                const Vec<V> x = wide(rows::get(xs, i, oddx));
+                co[i] = exponentials(wide(rg[i]));
+                sigmoids(co[i], a, f);
+                slope[i] = slope_and_next<MIX>(a, f, x, h);
+                d[i] = rows::get(ds, i, oddd);
+                A = mul(A, a);
+                E = fma(A, wide(d[i]), E);
+            }
+        }
+        __syncwarp();
+        Vec<V> q = join(j, step & 1, k.n, k.rank, kWarps - 1 - k.warp, !usual, Pair{A, E}, s, [&] {
+            fetch(step, kStages);
+            row = before(k.t0 - k.stride, k.at - far);
+        });
+        char *dx = reinterpret_cast<char *>(static_cast<io_t *>(p.out) + k.at + k.lane * V);
+        char *dg = reinterpret_cast<char *>(static_cast<io_t *>(p.dgate) + k.at + k.lane * V);
+        unsigned pitch = k.pitch;
+        asm volatile("" : "+r"(pitch));
+        const auto run = [&](auto z) {
+            constexpr bool Z = decltype(z)::value;
+#pragma unroll
+            for (int i = R - 1; i >= 0; --i) {
+                const Vec<V> r = add(wide(d[i]), q);
+                Vec<V> w;
+                // a and w again, rather than kept from above: registers for more tokens are worth more
+#pragma unroll
+                for (int v = 0; v < V; ++v) asm volatile("" : "+f"(co[i].v[v]));
+                if (!Z && kShort) {
+                    Vec<V> a, f;
+                    sigmoids(co[i], a, f);
+                    w = weight<MIX>(a, f);
+                    q = mul(r, a);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        w.v[v] = weight<MIX>(co[i].v[v]);
+                        q.v[v] = decay<Z>(co[i].v[v], r.v[v]);
+                    }
+                }
+                if (k.live && (!Z || i < tokens)) {
+                    put<rows::kPaired>(reinterpret_cast<io_t *>(dx + (size_t)i * pitch), MIX == OSDN_MIX_SUM ? r : mul(w, r), k.second);
+                    put<rows::kPaired>(reinterpret_cast<io_t *>(dg + (size_t)i * pitch), mul(slope[i], r), k.second);
+                }
+            }
+        };
+        if (!usual) run(std::true_type()); else run(std::false_type());
+        k.t0 -= k.stride;
+        k.at -= far;
+    }
+    if (k.rank == 0 && k.warp == 0) k.store_state(p, p.last, s);
+}
+
+}  // namespace
+
+cudaError_t backward_launch(int io, int B, int T, int C, int mix, const void *x, const void *gate, const void *h,
+                            const float *h0, const void *dh, const float *dhT, void *dx, void *dgate, float *dh0,
+                            cudaStream_t stream) {
+    Params p = {};
+    p.T = T; p.C = C;
+    p.x = x; p.gate = gate; p.h = h; p.dh = dh;
+    p.h0 = h0;
+    p.first = dhT;
+    p.out = dx; p.dgate = dgate;
+    p.last = dh0;
+    return with_types(io, mix, [&](auto t, auto m) {
+        using io_t = decltype(t);
+        // 16 tokens of OSDN_MIX_MEAN do not find room in 128 registers (2x8192x2048: 91 us either way,
+        // 16x1024x2048: 87 us, with 8 tokens 79 us); the others' do (16: 84 and 68 us, 8: 99 and 93 us)
+        constexpr int M = decltype(m)::value, most = sizeof(io_t) == 4 || M == OSDN_MIX_MEAN ? 8 : 16;
+        const Plan pl = plan(io, most, B, T, C);
+        p.per_seq = pl.per_seq;
+        p.steps = pl.steps;
+        return with_rows<io_t, most>(pl, [&](auto r, auto w) {
+            constexpr int R = decltype(r)::value, W = decltype(w)::value;
+            static std::atomic<unsigned long long> done{0};
+            return launch_as<io_t, R, W, 3>(backward_kernel<io_t, M, R, W>, done, pl, p, stream);
+        });
+    });
+}
+
+}  // namespace gs
+}  // namespace osdn

@@ -1,0 +1,327 @@
+// gated_scan_walk.cuh -- what the recurrence (gated_scan.cu) and its gradients
+// (gated_scan_backward.cu) share: the walk of a cluster over its strip of
+// channels, the copies ahead into shared memory and the join of what threads,
+// warps and CTAs have folded.  gated_scan.cu describes the whole.
+#pragma once
+
+#include <algorithm>
+#include <type_traits>
+
+#include "gated_scan.cuh"
+#include "ptx.cuh"
+
+namespace osdn {
+namespace gs {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxCluster = 8;
+
+struct Params {
+    int T, C, per_seq;      // per_seq: strips of 64 channels a sequence
+    int steps;              // of n kWarps R tokens
+    const void *x, *gate, *h, *dh;
+    const float *h0;        // (gradients)
+    const float *first;     // the state that enters: h0, or dhT
+    void *out, *dgate;      // h, or dx and dgate
+    float *last;            // the state that leaves: hT, or dh0
+};
+
+// A lane's two neighbouring channels as they lie in memory.
+template <typename io_t>
+struct Raw {
+    typedef typename std::conditional<sizeof(io_t) == 4, uint2, unsigned>::type type;
+};
+__device__ __forceinline__ Vec<2> wide(uint2 u) { return {{__uint_as_float(u.x), __uint_as_float(u.y)}}; }
+__device__ __forceinline__ Vec<2> wide(unsigned u) {
+    return {{__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)}};
+}
+// PAIRED: rows keep the boundaries of two channels; else `second`: whether the second one exists
+template <bool PAIRED, typename io_t>
+__device__ __forceinline__ void put(io_t *p, const Vec<2> &x, bool second) {
+    if constexpr (PAIRED) {
+        store2(p, x.v);
+    } else {
+        from_f32(p[0], x.v[0]);
+        if (second) from_f32(p[1], x.v[1]);
+    }
+}
+
+// `bytes` of the W bytes at src (the rest: zeros) into shared memory, asynchronously.
+template <int W>
+__device__ __forceinline__ void copy_async(uint32_t dst, const char *src, int bytes) {
+    if constexpr (W == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(W) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {   // all but the last N groups
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// R rows (tokens) of a strip of 64 channels in shared memory, and how a warp gets them.  W: 16, 8 or 4
+// bytes a copy, or 2: rows of an odd number of bf16, of which every other starts inside a word; the
+// words around it are copied, and a row begins 0 or 2 bytes into its place.
+template <typename io_t, int R, int W>
+struct Rows {
+    typedef typename Raw<io_t>::type raw_t;
+    static constexpr bool kPaired = W >= 2 * (int)sizeof(io_t);
+    static constexpr int kRow = 64 * (int)sizeof(io_t);          // bytes a row
+    static constexpr int kPitch = W == 2 ? kRow + 16 : kRow;     // in shared memory
+    static constexpr int kBytes = R * kPitch;
+    // rows 0 .. n - 1 from `src`, `pitch` bytes apart, the first `valid` bytes of each; zeros for the rest
+    __device__ __forceinline__ static void fetch(uint32_t dst, const char *src, unsigned pitch, int n, int valid) {
+        const int lane = threadIdx.x & 31;
+        if constexpr (W == 2) {
+            const char *const even = src - (reinterpret_cast<uintptr_t>(src) & 2);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const char *row = src + (size_t)r * pitch;
+                const int in = (int)(reinterpret_cast<uintptr_t>(row) & 2);   // bytes into its word
+                const int left = r < n ? in + valid - 4 * lane : 0;           // 33 words: lane 0 takes the last too
+                copy_async<4>(dst + r * kPitch + 4 * lane, left > 0 ? row - in + 4 * lane : even, max(0, min(4, left)));
+                if (lane == 0)
+                    copy_async<4>(dst + r * kPitch + 128, left > 128 ? row - in + 128 : even, max(0, min(4, left - 128)));
+            }
+        } else {
+            constexpr int per = kRow / W;                 // copies a row
+            constexpr int many = per < 32 ? 32 / per : 1; // rows a warp at once
+            constexpr int turns = per < 32 ? 1 : per / 32;
+            const int r0 = lane / per, q = lane % per * W;
+            const char *p = src + (size_t)r0 * pitch + q;
+            if (n >= R && valid == kRow) {
+#pragma unroll
+                for (int r = 0; r < R; r += many)
+#pragma unroll
+                    for (int t = 0; t < turns; ++t)
+                        copy_async<W>(dst + (r + r0) * kPitch + q + t * 32 * W, p + (size_t)r * pitch + t * 32 * W, W);
+            } else {
+#pragma unroll
+                for (int r = 0; r < R; r += many)
+#pragma unroll
+                    for (int t = 0; t < turns; ++t) {
+                        const bool there = r + r0 < n && q + t * 32 * W < valid;
+                        copy_async<W>(dst + (r + r0) * kPitch + q + t * 32 * W,
+                                      there ? p + (size_t)r * pitch + t * 32 * W : src, there ? W : 0);
+                    }
+            }
+        }
+    }
+    // this lane's channels of row r; `odd`: whether row 0 began inside a word
+    __device__ __forceinline__ static raw_t get(const char *p, int r, int odd) {
+        const char *at = p + r * kPitch + (threadIdx.x & 31) * sizeof(raw_t);
+        if constexpr (W == 2) {
+            const unsigned short *q = reinterpret_cast<const unsigned short *>(at + ((odd + r) & 1) * 2);
+            return (unsigned)q[0] | (unsigned)q[1] << 16;
+        } else {
+            return *reinterpret_cast<const raw_t *>(at);
+        }
+    }
+};
+
+// (A, E) pairs of a lane's channels: s <- A s + E.
+struct alignas(16) Pair {
+    Vec<2> A, E;
+    // Z: an A that is exactly zero hides s.  (Without an exactly shut gate anywhere an A of zero is an
+    // underflow, and takes nothing from a finite s.)
+    template <bool Z>
+    __device__ __forceinline__ void apply(Vec<2> &s) const {
+        const Vec<2> r = fma(A, s, E);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) s.v[i] = Z && A.v[i] == 0.0f ? E.v[i] : r.v[i];
+    }
+    template <bool Z>
+    __device__ __forceinline__ void then(const Pair &b) {   // this one first, then b
+        b.template apply<Z>(E);
+        A = mul(A, b.A);
+    }
+};
+
+// Where a step's pairs meet; one set for even and one for odd steps, so that a step's barriers are
+// enough: who writes a set again has passed the barriers of the step between.
+struct Join {
+    Pair warp[2][kWarps][32];
+    Pair total[2][kMaxCluster][32];
+};
+// From every thread's (A, E) and the state s that enters the step: the state before the thread's
+// first token.  s becomes the state after the step.  `place`: the warp's turn in the recurrence;
+// `zeros`: whether a factor of this warp may be exactly zero.  `meanwhile()` runs while the cluster's
+// CTAs wait for one another.
+template <typename F>
+__device__ __forceinline__ Vec<2> join(Join &j, int set, int n, int rank, int place, bool zeros, const Pair &own,
+                                       Vec<2> &s, const F &meanwhile) {
+    const int lane = threadIdx.x & 31;
+    j.warp[set][place][lane] = own;
+    const bool any = __syncthreads_or(zeros);
+    // what lies before this warp in the CTA, and what the CTA does in all
+    Pair before = {fill<2>(1.0f), fill<2>(0.0f)}, total = before;
+    const auto fold = [&](auto z) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == place) before = total;
+            if (w % 2 == 0) asm volatile("" ::: "memory");   // not all pairs into registers at once
+            total.template then<decltype(z)::value>(j.warp[set][w][lane]);
+        }
+    };
+    if (any) fold(std::true_type()); else fold(std::false_type());
+    Vec<2> mine = s;
+    if (n > 1) {
+        if (place == kWarps - 1) {   // the CTA's total, to every CTA of the cluster
+            for (int r = 0; r < n; ++r) {
+                const uint32_t at = ptx::cluster_map(&j.total[set][rank][lane], r);
+                ptx::cluster_store(at, make_float4(total.A.v[0], total.A.v[1], total.E.v[0], total.E.v[1]));
+            }
+        }
+        // Only the last warp has written for the others.  What every warp has read of an earlier step
+        // comes before it, by the barrier of the CTA.
+        __syncwarp();
+        if (place == kWarps - 1) ptx::cluster_arrive(); else ptx::cluster_arrive_relaxed();
+        meanwhile();
+        ptx::cluster_wait();
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+            if (r < n) {
+                if (r == rank) mine = s;
+                j.total[set][r][lane].template apply<true>(s);
+            }
+    } else {
+        meanwhile();
+        total.template apply<true>(s);
+    }
+    before.template apply<true>(mine);
+    return mine;
+}
+
+constexpr int kStages = 2;   // steps on their way into shared memory
+
+// What the two kernels share: the place of a thread, and the copies of K tensors.
+template <typename io_t, int R, int W, int K>
+struct Walk {
+    typedef Rows<io_t, R, W> rows;
+    int n, rank, lane, warp, b, c0, c, stride, t0;
+    bool live, second;   // whether this lane's two channels exist
+    unsigned pitch;
+    int valid;           // bytes of the strip's channels
+    size_t at;           // of row t0, channel c0
+    uint32_t smem;       // this warp's place
+    const char *mine;
+    __device__ __forceinline__ Walk(const Params &p, char *sm, bool backward) {
+        n = ptx::cluster_size();
+        rank = ptx::cluster_rank();
+        lane = threadIdx.x & 31;
+        warp = threadIdx.x >> 5;
+        const int strip = blockIdx.x / n;
+        b = strip / p.per_seq;
+        c0 = (strip - b * p.per_seq) * 64;
+        c = c0 + lane * 2;
+        live = c < p.C;
+        second = c + 1 < p.C;
+        pitch = p.C * (unsigned)sizeof(io_t);
+        valid = min(64, p.C - c0) * (int)sizeof(io_t);
+        stride = n * (kWarps * R);                 // tokens a step; T is at most 2^30
+        t0 = (backward ? p.steps * n - 1 - rank : rank) * (kWarps * R) + warp * R;
+        at = ((size_t)b * p.T + t0) * p.C + c0;
+        mine = sm + warp * (kStages * K * rows::kBytes);
+        smem = ptx::smem_u32(mine);
+    }
+    __device__ __forceinline__ void fetch(int stage, int k, const void *base, size_t from, int tokens) const {
+        // (computed where it is needed: kept over the steps, rows' offsets would take the tokens' registers)
+        unsigned pitch = this->pitch;
+        asm volatile("" : "+r"(pitch));
+        rows::fetch(smem + (stage * K + k) * rows::kBytes,
+                    reinterpret_cast<const char *>(static_cast<const io_t *>(base) + from), pitch, tokens, valid);
+    }
+    __device__ __forceinline__ const char *tile(int stage, int k) const { return mine + (stage * K + k) * rows::kBytes; }
+    __device__ __forceinline__ int odd(const void *base) const {
+        return W == 2 ? (int)((reinterpret_cast<uintptr_t>(base) >> 1) + at) & 1 : 0;
+    }
+    // a state [B][C] fp32 (zeros without one)
+    __device__ __forceinline__ Vec<2> load_state(const Params &p, const float *s) const {
+        Vec<2> v = fill<2>(0.0f);
+        if (s && live) v.v[0] = s[(size_t)b * p.C + c];
+        if (s && second) v.v[1] = s[(size_t)b * p.C + c + 1];
+        return v;
+    }
+    __device__ __forceinline__ void store_state(const Params &p, float *s, const Vec<2> &v) const {
+        if (s && live) s[(size_t)b * p.C + c] = v.v[0];
+        if (s && second) s[(size_t)b * p.C + c + 1] = v.v[1];
+    }
+};
+
+// f(type tag, mix tag) for the call's type and mix
+template <typename F>
+cudaError_t with_types(int io, int mix, const F &f) {
+    const auto by_mix = [&](auto t) {
+        if (mix == OSDN_MIX_SUM) return f(t, Mix<OSDN_MIX_SUM>());
+        if (mix == OSDN_MIX_MEAN) return f(t, Mix<OSDN_MIX_MEAN>());
+        return f(t, Mix<OSDN_MIX_UNIT>());
+    };
+    return io == OSDN_F32 ? by_mix(float()) : by_mix(__nv_bfloat16());
+}
+
+// How a call is cut: clusters of n CTAs a strip of 64 channels, R tokens a warp.
+struct Plan {
+    int R, W, n, steps, per_seq;
+    long long strips;
+};
+// `most`: the most tokens a warp holds in registers (4 at least, in powers of two).
+inline Plan plan(int io, int most, int B, int T, int C) {
+    Plan best = {};
+    const int row = C * (io == OSDN_F32 ? 4 : 2);
+    Plan p = {};
+    p.W = C % (io == OSDN_F32 ? 4 : 8) == 0 ? 16 : row % 8 == 0 && io == OSDN_F32 ? 8 : row % 4 == 0 ? 4 : 2;
+    p.per_seq = (C + 63) / 64;
+    p.strips = (long long)B * p.per_seq;
+    for (p.R = 4; p.R <= most; p.R *= 2) {
+        const int chunks = (T + kWarps * p.R - 1) / (kWarps * p.R);
+        // two CTAs an SM, in clusters of up to eight, are about 256
+        p.n = 1;
+        while (p.n < kMaxCluster && 2 * p.n * p.strips <= 288 && p.n < chunks) p.n *= 2;
+        p.steps = (chunks + p.n - 1) / p.n;
+        // a step takes its tokens and a join that is worth about four
+        if (!best.R || (long long)p.steps * (p.R + 4) <= (long long)best.steps * (best.R + 4)) best = p;
+    }
+    return best;
+}
+
+// K: the tensors that the kernel copies.
+template <typename io_t, int R, int W, int K>
+cudaError_t launch_as(void (*kernel)(Params), std::atomic<unsigned long long> &done, const Plan &pl, const Params &p,
+                      cudaStream_t stream) {
+    constexpr int smem = kWarps * kStages * K * Rows<io_t, R, W>::kBytes;
+    const cudaError_t e = smem_attr_once(reinterpret_cast<const void *>(kernel), smem, done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((unsigned)(pl.strips * pl.n));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = pl.n;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.attrs = &at;
+    c.numAttrs = pl.n > 1;
+    return cudaLaunchKernelEx(&c, kernel, p);
+}
+template <int X>
+using Int = std::integral_constant<int, X>;
+// f(R tag, W tag) for the plan; MOST as in plan()
+template <typename io_t, int MOST, typename F>
+cudaError_t with_rows(const Plan &pl, const F &f) {
+    const auto by_copy = [&](auto r) {
+        if (pl.W == 16) return f(r, Int<16>());
+        if (sizeof(io_t) == 4) return pl.W == 8 ? f(r, Int<sizeof(io_t) == 4 ? 8 : 4>()) : f(r, Int<4>());
+        return pl.W == 4 ? f(r, Int<4>()) : f(r, Int<sizeof(io_t) == 4 ? 4 : 2>());
+    };
+    return pl.R == 4 ? by_copy(Int<4>()) : pl.R == 8 ? by_copy(Int<8>()) : by_copy(Int<MOST>());
+}
+
+}  // namespace
+
+}  // namespace gs
+}  // namespace osdn
