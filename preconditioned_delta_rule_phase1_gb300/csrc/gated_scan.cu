@@ -54,13 +54,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
     for (int step = 0; step < p.steps; ++step) {
         copies_wait<kStages - 1>();
         __syncwarp();
-        const int tokens = p.T - k.t0, odd = k.odd(p.gate), oddx = k.odd(p.x);
+        const int tokens = p.T - k.t0, in = k.in(p.gate), inx = k.in(p.x);
         const char *gate = k.tile(step % kStages, 0), *xs = k.tile(step % kStages, 1);
         float most = 0.0f;
         raw_t rg[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            rg[i] = rows::get(gate, i, odd);
+            rg[i] = rows::get(gate, i, in, k.pitch);
             const Vec<V> g = wide(rg[i]);
 #pragma unroll
             for (int v = 0; v < V; ++v) most = fmaxf(most, fabsf(g.v[v]));
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
             constexpr bool Z = decltype(z)::value;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const Vec<V> g = wide(rg[i]), x = wide(rows::get(xs, i, oddx));
+                const Vec<V> g = wide(rg[i]), x = wide(rows::get(xs, i, inx, k.pitch));
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     // tokens past the end leave everything as it is
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 Vec<V> f;
-                const Vec<V> x = wide(rows::get(xs, i, oddx));
+                const Vec<V> x = wide(rows::get(xs, i, inx, k.pitch));
                 sigmoids(exponentials(wide(rg[i])), co[i], f);
                 wx[i] = MIX == OSDN_MIX_SUM ? x : mul(weight<MIX>(co[i], f), x);
                 A = mul(A, co[i]);
@@ -180,7 +180,7 @@ cudaError_t scan_launch(int io, int B, int T, int C, int mix, const void *x, con
         const Plan pl = plan(io, most, B, T, C);
         p.per_seq = pl.per_seq;
         p.steps = pl.steps;
-        return with_rows<io_t, most>(pl, [&](auto r, auto w) {
+        return with_rows<io_t, most, most>(pl, [&](auto r, auto w) {
             constexpr int R = decltype(r)::value, W = decltype(w)::value;
             static std::atomic<unsigned long long> done{0};
             return launch_as<io_t, R, W, 2>(scan_kernel<io_t, M, R, W>, done, pl, p, stream);

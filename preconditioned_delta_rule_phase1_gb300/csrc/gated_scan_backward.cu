@@ -61,13 +61,13 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
     for (int step = 0; step < p.steps; ++step) {
         copies_wait<kStages - 1>();
         __syncwarp();
-        const int tokens = p.T - k.t0, odd = k.odd(p.gate), oddx = k.odd(p.x), oddd = k.odd(p.dh);
+        const int tokens = p.T - k.t0, in = k.in(p.gate), inx = k.in(p.x), ind = k.in(p.dh);
         const char *gate = k.tile(step % kStages, 0), *xs = k.tile(step % kStages, 1), *ds = k.tile(step % kStages, 2);
         float most = 0.0f;
         raw_t rg[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            rg[i] = rows::get(gate, i, odd);
+            rg[i] = rows::get(gate, i, in, k.pitch);
             const Vec<V> g = wide(rg[i]);
 #pragma unroll
             for (int v = 0; v < V; ++v) most = fmaxf(most, fabsf(g.v[v]));
@@ -82,8 +82,8 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
             constexpr bool Z = decltype(z)::value;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const Vec<V> g = wide(rg[i]), x = wide(rows::get(xs, i, oddx));
-                d[i] = rows::get(ds, i, oddd);
+                const Vec<V> g = wide(rg[i]), x = wide(rows::get(xs, i, inx, k.pitch));
+                d[i] = rows::get(ds, i, ind, k.pitch);
                 const Vec<V> di = wide(d[i]);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
@@ -103,11 +103,11 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 Vec<V> a, f;
-                const Vec<V> x = wide(rows::get(xs, i, oddx));
+                const Vec<V> x = wide(rows::get(xs, i, inx, k.pitch));
                 co[i] = exponentials(wide(rg[i]));
                 sigmoids(co[i], a, f);
                 slope[i] = slope_and_next<MIX>(a, f, x, h);
-                d[i] = rows::get(ds, i, oddd);
+                d[i] = rows::get(ds, i, ind, k.pitch);
                 A = mul(A, a);
                 E = fma(A, wide(d[i]), E);
             }
@@ -170,12 +170,14 @@ cudaError_t backward_launch(int io, int B, int T, int C, int mix, const void *x,
     return with_types(io, mix, [&](auto t, auto m) {
         using io_t = decltype(t);
         // 16 tokens of OSDN_MIX_MEAN do not find room in 128 registers (2x8192x2048: 91 us either way,
-        // 16x1024x2048: 87 us, with 8 tokens 79 us); the others' do (16: 84 and 68 us, 8: 99 and 93 us)
+        // 16x1024x2048: 87 us, with 8 tokens 79 us), nor do those of rows of odd bf16 (2x8192x2047, sum:
+        // 160 us, with 8 tokens 128 us); the others do (2x8192x2048, unit and sum: 84 and 68 us, with 8
+        // tokens 99 and 93 us)
         constexpr int M = decltype(m)::value, most = sizeof(io_t) == 4 || M == OSDN_MIX_MEAN ? 8 : 16;
-        const Plan pl = plan(io, most, B, T, C);
+        const Plan pl = plan(io, C % 2 ? 8 : most, B, T, C);
         p.per_seq = pl.per_seq;
         p.steps = pl.steps;
-        return with_rows<io_t, most>(pl, [&](auto r, auto w) {
+        return with_rows<io_t, most, 8>(pl, [&](auto r, auto w) {
             constexpr int R = decltype(r)::value, W = decltype(w)::value;
             static std::atomic<unsigned long long> done{0};
             return launch_as<io_t, R, W, 3>(backward_kernel<io_t, M, R, W>, done, pl, p, stream);

@@ -64,8 +64,8 @@ __device__ __forceinline__ void copies_wait() {   // all but the last N groups
 }
 
 // R rows (tokens) of a strip of 64 channels in shared memory, and how a warp gets them.  W: 16, 8 or 4
-// bytes a copy, or 2: rows of an odd number of bf16, of which every other starts inside a word; the
-// words around it are copied, and a row begins 0 or 2 bytes into its place.
+// bytes a copy, or 2: rows of an odd number of bf16, which start anywhere; the nine 16-byte pieces around
+// a row are copied, and it begins `in` bytes into its place.
 template <typename io_t, int R, int W>
 struct Rows {
     typedef typename Raw<io_t>::type raw_t;
@@ -77,15 +77,15 @@ struct Rows {
     __device__ __forceinline__ static void fetch(uint32_t dst, const char *src, unsigned pitch, int n, int valid) {
         const int lane = threadIdx.x & 31;
         if constexpr (W == 2) {
-            const char *const even = src - (reinterpret_cast<uintptr_t>(src) & 2);
+            const char *const start = src - (reinterpret_cast<uintptr_t>(src) & 15);
+            const int r0 = lane / 9, q = lane % 9 * 16;   // three rows a warp at once
 #pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const char *row = src + (size_t)r * pitch;
-                const int in = (int)(reinterpret_cast<uintptr_t>(row) & 2);   // bytes into its word
-                const int left = r < n ? in + valid - 4 * lane : 0;           // 33 words: lane 0 takes the last too
-                copy_async<4>(dst + r * kPitch + 4 * lane, left > 0 ? row - in + 4 * lane : even, max(0, min(4, left)));
-                if (lane == 0)
-                    copy_async<4>(dst + r * kPitch + 128, left > 128 ? row - in + 128 : even, max(0, min(4, left - 128)));
+            for (int r = 0; r < R; r += 3) {
+                const char *row = src + (size_t)(r + r0) * pitch;
+                const int in = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+                const int left = r + r0 < n ? in + valid - q : 0;
+                if (lane < 27 && r + r0 < R)
+                    copy_async<16>(dst + (r + r0) * kPitch + q, left > 0 ? row - in + q : start, max(0, min(16, left)));
             }
         } else {
             constexpr int per = kRow / W;                 // copies a row
@@ -111,11 +111,11 @@ struct Rows {
             }
         }
     }
-    // this lane's channels of row r; `odd`: whether row 0 began inside a word
-    __device__ __forceinline__ static raw_t get(const char *p, int r, int odd) {
+    // this lane's channels of row r; `in`: where row 0 begins in its place
+    __device__ __forceinline__ static raw_t get(const char *p, int r, int in, unsigned pitch) {
         const char *at = p + r * kPitch + (threadIdx.x & 31) * sizeof(raw_t);
         if constexpr (W == 2) {
-            const unsigned short *q = reinterpret_cast<const unsigned short *>(at + ((odd + r) & 1) * 2);
+            const unsigned short *q = reinterpret_cast<const unsigned short *>(at + ((in + r * pitch) & 15));
             return (unsigned)q[0] | (unsigned)q[1] << 16;
         } else {
             return *reinterpret_cast<const raw_t *>(at);
@@ -236,8 +236,8 @@ struct Walk {
                     reinterpret_cast<const char *>(static_cast<const io_t *>(base) + from), pitch, tokens, valid);
     }
     __device__ __forceinline__ const char *tile(int stage, int k) const { return mine + (stage * K + k) * rows::kBytes; }
-    __device__ __forceinline__ int odd(const void *base) const {
-        return W == 2 ? (int)((reinterpret_cast<uintptr_t>(base) >> 1) + at) & 1 : 0;
+    __device__ __forceinline__ int in(const void *base) const {   // where row t0 begins in its place
+        return W == 2 ? (int)((reinterpret_cast<uintptr_t>(base) + at * 2) & 15) : 0;
     }
     // a state [B][C] fp32 (zeros without one)
     __device__ __forceinline__ Vec<2> load_state(const Params &p, const float *s) const {
@@ -310,13 +310,15 @@ cudaError_t launch_as(void (*kernel)(Params), std::atomic<unsigned long long> &d
 }
 template <int X>
 using Int = std::integral_constant<int, X>;
-// f(R tag, W tag) for the plan; MOST as in plan()
-template <typename io_t, int MOST, typename F>
+// f(R tag, W tag) for a plan of at most MOST tokens a warp, of rows of odd bf16 at most ODD
+template <typename io_t, int MOST, int ODD, typename F>
 cudaError_t with_rows(const Plan &pl, const F &f) {
     const auto by_copy = [&](auto r) {
+        constexpr bool f32 = sizeof(io_t) == 4, odd = !f32 && decltype(r)::value <= ODD;
         if (pl.W == 16) return f(r, Int<16>());
-        if (sizeof(io_t) == 4) return pl.W == 8 ? f(r, Int<sizeof(io_t) == 4 ? 8 : 4>()) : f(r, Int<4>());
-        return pl.W == 4 ? f(r, Int<4>()) : f(r, Int<sizeof(io_t) == 4 ? 4 : 2>());
+        if (f32 && pl.W == 8) return f(r, Int<f32 ? 8 : 4>());
+        if (odd && pl.W == 2) return f(r, Int<odd ? 2 : 4>());
+        return f(r, Int<4>());
     };
     return pl.R == 4 ? by_copy(Int<4>()) : pl.R == 8 ? by_copy(Int<8>()) : by_copy(Int<MOST>());
 }
