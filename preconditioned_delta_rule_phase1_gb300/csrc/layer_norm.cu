@@ -454,6 +454,7 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
         s = next;
     }
     if (!p.columns) return;
+    da::dependents_may_start();
     if (!SMEM) {
         for (int o = 0; o < groups; ++o) {
             if (o == group) {
@@ -472,19 +473,24 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
     for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) p.part[(size_t)blockIdx.x * 2 * p.C + c] = sums[c];
 }
 
-// dweight and dbias from the CTAs' shares: eight warps take shares 0, 8, ..; 1, 9, ..; of 32 columns.
-__global__ void __launch_bounds__(256) columns_kernel(int ctas, int C, const float *part, float *dweight, float *dbias) {
-    __shared__ float s[8][32];
+// dweight and dbias from the CTAs' shares, 32 columns a CTA: its 32 warps take shares 0, 32, ..; 1, 33, ..
+// (all at once: at most five each), and the first adds up what they have.
+constexpr int kColumnWarps = 32;
+__global__ void __launch_bounds__(kColumnWarps * 32) columns_kernel(int ctas, int C, const float *part, float *dweight,
+                                                                   float *dbias) {
+    __shared__ float s[kColumnWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const long long c = (long long)blockIdx.x * 32 + lane;
+    const int c = blockIdx.x * 32 + lane;   // C is at most 16384
+    da::dependency_wait();
     float v = 0.0f;
     if (c < 2 * C)
-        for (int i = warp; i < ctas; i += 8) v += part[(size_t)i * 2 * C + c];
+#pragma unroll 5
+        for (int i = warp; i < ctas; i += kColumnWarps) v += part[(size_t)i * 2 * C + c];
     s[warp][lane] = v;
     __syncthreads();
     if (warp || c >= 2 * C) return;
 #pragma unroll
-    for (int w = 1; w < 8; ++w) v += s[w][lane];
+    for (int w = 1; w < kColumnWarps; ++w) v += s[w][lane];
     if (c < C) {
         if (dweight) dweight[c] = v;
     } else if (dbias) {
@@ -544,7 +550,9 @@ struct Cut {
 };
 Cut cut(int io, long long rows, int C) {
     Cut k;
-    k.M = C < (io == OSDN_F32 ? 4096 : 512) ? 8 : C <= 8192 - (C & 1) ? 16 : 32;
+    // 16 values a thread halve what a row costs beside them, eight fill more threads (bf16, 8193 rows of
+    // 1024: 31 and 27 us; 16384 rows of 2048: 68 and 72 us); fp32 has no room for three rows of 16
+    k.M = C < (io == OSDN_F32 ? 4096 : 1536) ? 8 : C <= 8192 - (C & 1) ? 16 : 32;
     k.warps = ceil_div(C + (C & 1), 32 * k.M);
     k.groups = 16 / k.warps;
     k.ctas = (int)std::min<long long>(sm_count(), (rows + k.groups - 1) / k.groups);
@@ -604,9 +612,9 @@ cudaError_t backward_launch(int io, long long rows, int C, const void *x, const 
         const cudaError_t r = io == OSDN_F32 ? by_size(float()) : by_size(__nv_bfloat16());
         if (r != cudaSuccess) return r;
     }
-    if (p.columns)
-        columns_kernel<<<(2 * C + 31) / 32, 256, 0, stream>>>(k.ctas, C, p.part, dweight, dbias);
-    return cudaGetLastError();
+    if (!p.columns) return cudaSuccess;
+    return da::launch_overlapped(rows > 0, columns_kernel, dim3((2 * C + 31) / 32), kColumnWarps * 32, 0, stream, k.ctas,
+                                 C, static_cast<const float *>(p.part), dweight, dbias);
 }
 
 }  // namespace ln
