@@ -288,6 +288,7 @@ struct Ahead {
     static constexpr bool kSmem = M == 32;
     static constexpr int S = sizeof(io_t) * M <= 32 ? 3 : sizeof(io_t) * M <= 64 ? 1 : 0;
     static constexpr int bytes(int threads) { return threads * M * (int)sizeof(io_t) * 3 * S; }   // of copies
+    static constexpr int sum_bytes(int threads, int C) { return kSmem ? threads * M * 8 : C * 8; }
 };
 template <typename io_t, int E, int N, int KIND>
 __global__ void __launch_bounds__(512) backward_kernel(Params p) {
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
     constexpr int M = P::M, S = Ahead<io_t, M>::S;
     constexpr bool ODD = P::ODD, SMEM = Ahead<io_t, M>::kSmem;
     constexpr int Q = E == 1 ? 2 : 1, EE = Q * E;   // pieces and values at a time
-    extern __shared__ __align__(16) char sm[];      // [S][3][N][threads] pieces, [2][C] sums
+    extern __shared__ __align__(16) char sm[];      // [S][3][N][threads] pieces, sums
     __shared__ float4 part[2][16];   // (one for even and one for odd rows of a group)
     const int width = p.warps * 32, groups = blockDim.x / width;
     const int group = threadIdx.x / width, tid = threadIdx.x % width, warp = tid / 32;
@@ -356,7 +357,14 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
 #pragma unroll
     for (int i = 0; i < M; ++i) aw[i] = ab[i] = 0.0f;
     if (!SMEM) g.affine(p.weight, 1.0f, w);
-    for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) sums[c] = 0.0f;
+    // (SMEM: a thread's own sums, two at a time side by side over the threads)
+    float2 *const own = reinterpret_cast<float2 *>(sums) + threadIdx.x;
+    if (SMEM) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) own[i * (int)blockDim.x] = two(0.0f);
+    } else {
+        for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) sums[c] = 0.0f;
+    }
     __syncthreads();
     float x0 = first < rows ? to_f32(static_cast<const io_t *>(p.x)[at]) : 0.0f;
 #pragma unroll
@@ -435,14 +443,9 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
                 put2(e, i, f);
                 const float2 xh = __ffma2_rn(get2(v, o), two(r), two(rm));
                 if (SMEM) {
-                    f = __fmul2_rn(get2(d, i), xh);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if (g.has(o + k)) {
-                            const int c = g.at((o + k) / E) + (o + k) % E;
-                            sums[c] += k ? f.y : f.x;
-                            sums[p.C + c] += d[i + k];
-                        }
+                    float2 &sw = own[(o / 2) * (int)blockDim.x], &sb = own[(M / 2 + o / 2) * (int)blockDim.x];
+                    sw = __ffma2_rn(get2(d, i), xh, sw);
+                    sb = __fadd2_rn(sb, get2(d, i));
                 } else {
                     put2(aw, o, __ffma2_rn(get2(d, i), xh, get2(aw, o)));
                     put2(ab, o, __fadd2_rn(get2(ab, o), get2(d, i)));
@@ -455,22 +458,31 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
     }
     if (!p.columns) return;
     da::dependents_may_start();
-    if (!SMEM) {
-        for (int o = 0; o < groups; ++o) {
-            if (o == group) {
+    float *const share = p.part + (size_t)blockIdx.x * 2 * p.C;
+    if (SMEM) {   // one group
 #pragma unroll
-                for (int i = 0; i < M; ++i)
-                    if (g.has(i)) {
-                        const int c = g.at(i / E) + i % E;
-                        sums[c] += aw[i];
-                        sums[p.C + c] += ab[i];
-                    }
+        for (int i = 0; i < M; ++i)
+            if (g.has(i)) {
+                const int c = g.at(i / E) + i % E;
+                const float2 sw = own[(i / 2) * (int)blockDim.x], sb = own[(M / 2 + i / 2) * (int)blockDim.x];
+                share[c] = i % 2 ? sw.y : sw.x;
+                share[p.C + c] = i % 2 ? sb.y : sb.x;
             }
-            __syncthreads();
-        }
+        return;
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) p.part[(size_t)blockIdx.x * 2 * p.C + c] = sums[c];
+    for (int o = 0; o < groups; ++o) {
+        if (o == group) {
+#pragma unroll
+            for (int i = 0; i < M; ++i)
+                if (g.has(i)) {
+                    const int c = g.at(i / E) + i % E;
+                    sums[c] += aw[i];
+                    sums[p.C + c] += ab[i];
+                }
+        }
+        __syncthreads();
+    }
+    for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) share[c] = sums[c];
 }
 
 // dweight and dbias from the CTAs' shares, 32 columns a CTA: its 32 warps take shares 0, 32, ..; 1, 33, ..
@@ -566,10 +578,10 @@ cudaError_t backward(const Params &p, const Cut &k, int E, cudaStream_t stream) 
         auto *kernel = backward_kernel<io_t, decltype(e)::value, decltype(n)::value, decltype(kind)::value>;
         static std::atomic<unsigned long long> done{0};
         r = smem_attr_once(reinterpret_cast<const void *>(kernel),
-                           Ahead<io_t, M>::bytes(512) + (M == 32 ? 16384 : M == 16 || sizeof(io_t) == 2 ? 8192 : 4096) * 8, done);
+                           Ahead<io_t, M>::bytes(512) + Ahead<io_t, M>::sum_bytes(512, sizeof(io_t) == 2 || M == 16 ? 8192 : 4096), done);
         if (r == cudaSuccess) {
             const int threads = k.groups * k.warps * 32;
-            kernel<<<k.ctas, threads, Ahead<io_t, M>::bytes(threads) + (size_t)p.C * 8, stream>>>(p);
+            kernel<<<k.ctas, threads, Ahead<io_t, M>::bytes(threads) + Ahead<io_t, M>::sum_bytes(threads, p.C), stream>>>(p);
             r = cudaGetLastError();
         }
     });
