@@ -629,8 +629,7 @@ int osdn_gated_scan_step(int io, int B, int C, int mix, const void *x, const voi
  * -a^2 sqrt((1 - a) / (1 + a)) by mix.  Factors that are zero hide as above
  * (d_h is read at every token: a padded place has to hold zeros).
  *   h    in  [B][T][C] io: what osdn_gated_scan wrote for these inputs.  The
- *            states are recomputed in fp32 from rows of it some tens to
- *            hundreds of tokens apart
+ *            states are recomputed in fp32 from rows of it some tokens apart
  *   d_h  in  [B][T][C] io       d_hT in [B][C] fp32, or NULL (zeros)
  *   dx, dgate out [B][T][C] io  dh0 out [B][C] fp32, or NULL (not written)
  * The rest, and the limits, as osdn_gated_scan; with T == 0 the call writes
@@ -650,7 +649,8 @@ int osdn_gated_scan_backward(int io, int B, int T, int C, int mix, const void *x
  *   weight, bias in [C] fp32, each or both NULL (ones, zeros)
  *   y        out [rows][C] io
  *   sum      out [rows][C] io: s; given exactly if residual is
- * C is from 1 to 16384, rows below 2^31; eps > 0 and finite.
+ * C is from 1 to 16384, rows below 2^31; eps > 0 and finite.  The squares of
+ * the differences to the row's first value have to fit fp32.
  */
 int osdn_layer_norm(int io, long long rows, int C, const void *x, const void *residual, const float *weight,
                     const float *bias, float eps, void *y, void *sum, void *stream);

@@ -10,11 +10,11 @@
 // the same sign at every token of a constant gate).  g = -inf is c = +0, g =
 // +inf is c = -0; a factor that is exactly zero hides what it multiplies.
 //
-// The short one, for bf16 I/O and |g| <= kPlainGate, holds a rounded to fp32:
-// a bf16 gate knows its own 1 - a to 2^-9 g of itself, far less than that
-// rounding takes away (at g = 7, 1 - a = 9e-4 to 1.4%, and 2^-25 is 0.003% of
-// it), and instructions are what bounds bf16.  1 - a is e^-g a, and keeps its
-// digits in both forms.
+// The short one, for bf16 I/O and |g| <= kPlainGate, multiplies with a rounded
+// to fp32: a bf16 gate knows its own 1 - a to 2^-8 g of itself, which is far
+// more than that rounding takes away (at g = 7, 1 - a = 9e-4 to 2.7%, and 2^-25
+// is 0.003% of it), and instructions are what bounds bf16.  The weight of x
+// reads 1 - a as e^-g a, with its digits, in both forms.
 #pragma once
 
 #include "osdn_device.cuh"
@@ -99,9 +99,6 @@ __device__ __forceinline__ float rsqrt_fast(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// c v, where a factor that is exactly zero hides v whatever it holds.
-__device__ __forceinline__ float hide(float c, float v) { return c == 0.0f ? 0.0f : c * v; }
-
 // ------------------------------------------------------------- the exact form
 __device__ __forceinline__ float gate_coefficient(float g) {
     const float e = exp2_fast(fabsf(g) * -kLog2e);
@@ -138,10 +135,12 @@ __device__ __forceinline__ float weighted(float c, float x) {
 template <int MIX, bool Z>
 __device__ __forceinline__ float slope_of(float c, float v, float x) {
     const float s = fabsf(c), ab = fmaf(-s, s, s);
-    if (MIX == OSDN_MIX_MEAN) v -= x;
-    if (MIX == OSDN_MIX_UNIT)
-        v = fmaf(-(keeps(c) ? 1.0f + c : c) * rsqrt_fast(fmaxf(unit_square(c), 1e-37f)), x, v);
-    return Z && ab == 0.0f ? 0.0f : ab * v;
+    if (Z && ab == 0.0f) return 0.0f;
+    if (MIX == OSDN_MIX_SUM) return ab * v;
+    if (MIX == OSDN_MIX_MEAN) return ab * (v - x);
+    // (k a b first: k alone can be large, and with a large x leave fp32)
+    const float kab = (keeps(c) ? 1.0f + c : c) * (ab * rsqrt_fast(fmaxf(unit_square(c), 1e-37f)));
+    return fmaf(ab, v, -kab * x);
 }
 
 // ------------------------------------------------------------- the short form
@@ -186,9 +185,10 @@ __device__ __forceinline__ Vec<V> slope_and_next(const Vec<V> &a, const Vec<V> &
         Vec<V> k;
 #pragma unroll
         for (int i = 0; i < V; ++i) k.v[i] = rsqrt_fast(q.v[i]);
-        const Vec<V> xk = mul(k, x);
-        slope = mul(ab, fma(mul(a, xk), fill<V>(-1.0f), v));
-        v = fma(v, a, mul(q, xk));
+        // (k a b and w first: 1 / w alone can be large, and with a large x leave fp32)
+        const Vec<V> kab = mul(mul(ab, k), a);
+        slope = fma(mul(kab, x), fill<V>(-1.0f), mul(ab, v));
+        v = fma(v, a, mul(mul(q, k), x));
     }
     return slope;
 }

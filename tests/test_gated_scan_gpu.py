@@ -238,6 +238,29 @@ def test_extreme_gates(T):
 
 @pytest.mark.parametrize("io", ["f32", "bf16"])
 @pytest.mark.parametrize("mix", MIXES)
+def test_large_and_small_values(io, mix):
+    """Nothing on the way leaves fp32 where the results do not: inputs of 1e30 behind gates up to 79 and
+    down to -79, and values of 1e-30."""
+    for size in (1e30, 1e-30):
+        t = inputs(1, 300, 66, io, seed=11)
+        t["gate"][:, :, 0::3] = 79.0
+        t["gate"][:, :, 1::3] = torch.where(torch.rand(1, 300, 22, device="cuda") < 0.5, 60.0, -79.0).to(DT[io])
+        for n in ("x", "h0"):
+            t[n] *= size
+        d = wide(t)
+        ref, _ = forward64(d["x"], d["gate"], d["h0"], mix)
+        h, hT = ops.gated_scan(t["x"], t["gate"], t["h0"], mix=mix)
+        close(h, ref, HALF[io], 1e-37, what=(mix, size))
+        dx, dg, dh0, lever = backward64(d["x"], d["gate"], d["h0"], mix, d["dh"], d["dhT"])
+        g = ops.gated_scan_backward(t["x"], t["gate"], h, t["h0"], dh=t["dh"], dhT=t["dhT"], mix=mix)
+        assert all(torch.isfinite(v).all() for v in g.values()), (mix, size)
+        # (values below fp32's normal range may be zero)
+        close(g["x"], dx, HALF[io], 1e-36, what=(mix, size))
+        close(g["gate"], dg, HALF[io], lever * ((HALF[io] + TOL32) * ref.abs().amax((0, 1))) + 1e-36, what=(mix, size))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("mix", MIXES)
 @pytest.mark.parametrize("B,C", [(1, 1), (1, 2048), (3, 33), (256, 130), (70001, 3)])
 def test_steps_follow_the_prompt(io, mix, B, C):
     t = inputs(B, 6, C, io, seed=B)
