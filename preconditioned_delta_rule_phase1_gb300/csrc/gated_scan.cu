@@ -24,8 +24,8 @@
 // Measured (bf16, mean): 42 us at 16x1024x2048, where a CTA walks a strip alone
 // (4.8 TB/s, 0.71 of the measured copy bandwidth), 50 us at 2x8192x2048 in
 // clusters of four (0.60) and 181 us at 1x65536x2048 in clusters of eight
-// (0.66); fp32 46 us at 2x4096x2048.  About 33 instructions a token and warp at
-// 16 warps an SM (128 registers) take 0.42 to 0.47 of the issue slots; the rest
+// (0.66); fp32 46 us at 2x4096x2048.  34 to 40 instructions a token and warp at
+// 16 warps an SM (128 registers) take 0.42 to 0.49 of the issue slots; the rest
 // is a step's latency, about 2 us in a cluster of eight that has its SMs to
 // itself.  Joining through a chain of clusters in global memory took 118 us at
 // 2x8192x2048, eight tokens a warp in place of 16 66 us.

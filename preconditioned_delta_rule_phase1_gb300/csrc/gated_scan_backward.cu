@@ -3,7 +3,7 @@
 //
 // Measured (bf16, 2x8192x2048, five tensors of 67 MB): sum 68, unit 85, mean 91
 // us (0.73, 0.58 and 0.54 of the measured copy bandwidth); fp32 64 us at
-// 2x4096x2048, mean.  Bound by instruction issue (0.46 of the slots at 16 warps
+// 2x4096x2048, mean.  Bound by instruction issue (0.45 of the slots at 16 warps
 // an SM) and a step's latency.  Only e^-g and the slope of the gate stay in
 // registers between the two passes over a thread's tokens; with a and w kept
 // too there is room for eight tokens in place of 16 (sum 93 us).

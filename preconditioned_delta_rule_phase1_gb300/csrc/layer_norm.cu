@@ -13,11 +13,11 @@
 // sums in one (see there).  All arithmetic is fp32.
 //
 // Measured (bf16): the norm 48 us at 16384 rows of 2048 with a residual (5.6
-// TB/s, 0.83 of the measured copy bandwidth; 45 us among other calls), 123 us
+// TB/s, 0.83 of the measured copy bandwidth; 45 us among other calls), 125 us
 // at rows of 2047 (instruction issue: words, and masks at both ends); its
 // gradients with ds 64 us at 16384x2048 (0.62), 26 us at 8193x1024, 77 us at
-// 1024x16384, bound by instruction issue (0.47 of the slots at 16 warps an SM,
-// about 450 instructions a warp and row of 2048).  Gradients with two
+// 1024x16384, bound by instruction issue (0.5 of the slots at 16 warps an SM,
+// 460 instructions a warp and row of 2048).  Gradients with two
 // reductions a row took 72 us, with the loads ahead in registers 88 us.
 #include <algorithm>
 #include <type_traits>
