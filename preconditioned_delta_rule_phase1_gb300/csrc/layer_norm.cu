@@ -18,7 +18,7 @@
 // gradients with ds 64 us at 16384x2048 (0.62), 26 us at 8193x1024, 77 us at
 // 1024x16384, bound by instruction issue (0.5 of the slots at 16 warps an SM,
 // 460 instructions a warp and row of 2048).  Gradients with two
-// reductions a row took 72 us, with the loads ahead in registers 88 us.
+// reductions a row took 72 us, without loads ahead 88 us.
 #include <algorithm>
 #include <type_traits>
 

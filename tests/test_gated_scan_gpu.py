@@ -403,3 +403,28 @@ def test_in_a_graph(io, T):
         want = run(torch.zeros(2, 66, device="cuda"))
         assert all(torch.equal(a, b) for a, b in zip(got, want)), i
     assert ws.status() == 0
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements a tensor: the last tokens are what they are alone, behind a restart, and
+    so are the first ones' gradients."""
+    T, C, part = 1100001, 1990, 3000
+    assert T * C > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, gate, dh = (torch.empty(1, T, C, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(3))
+    gate.add_(3.0)
+    gate[:, part] = gate[:, T - part] = -math.inf
+    h, hT = ops.gated_scan(x, gate, mix="mean")
+    tail = slice(T - part, T)
+    alone, aT = ops.gated_scan(x[:, tail].clone(), gate[:, tail].clone(), mix="mean")
+    # (runs begin elsewhere: fp32 rounding, and at times another bf16)
+    close(h[:, tail], alone.double(), 2 * HALF["bf16"])
+    close(hT, aT.double(), 2.0 ** -24, 2 * TOL32 * alone.double().abs().amax((0, 1)))
+    got = ops.gated_scan_backward(x, gate, h, dh=dh, mix="mean")
+    for part_of in (slice(0, part), tail):
+        a = [v[:, part_of].clone() for v in (x, gate, h, dh)]
+        want = ops.gated_scan_backward(a[0], a[1], a[2], dh=a[3], mix="mean")
+        size = 4 * HALF["bf16"] * a[2].double().abs().amax((0, 1))
+        close(got["x"][:, part_of], want["x"].double(), 2 * HALF["bf16"])
+        # (the states are recomputed from other rows of h)
+        close(got["gate"][:, part_of], want["gate"].double(), 2 * HALF["bf16"], size * want["x"].double().abs().amax((0, 1)))

@@ -229,3 +229,22 @@ def test_repeatable_elsewhere_and_in_a_graph(io, rows, C):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, run()))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements a tensor: the last rows are what they are alone."""
+    rows, C, part = 1100003, 1990, 300
+    assert rows * C > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, r, dy = (torch.empty(rows, C, dtype=torch.bfloat16, device="cuda").normal_(generator=g) for _ in range(3))
+    w = torch.randn(C, generator=g, device="cuda")
+    y, s = ops.layer_norm(x, w, residual=r)
+    dx = ops.layer_norm_backward(s, dy, w, ds=r)["x"]
+    tail = slice(rows - part, rows)
+    a = [v[tail].clone() for v in (x, r, s, dy)]
+    want, sw = ops.layer_norm(a[0], w, residual=a[1])
+    assert torch.equal(s[tail], sw)
+    # (rows are cut otherwise where they are few: fp32 rounding, and at times another bf16)
+    within(y[tail], want.double(), 2 * HALF["bf16"] * want.double().abs() + 1e-5 * row(want.double()))
+    want = ops.layer_norm_backward(a[2], a[3], w, ds=a[1])["x"]
+    within(dx[tail], want.double(), 2 * HALF["bf16"] * want.double().abs() + 1e-5 * row(want.double()))
