@@ -27,54 +27,30 @@ struct Mix {
     static constexpr int value = M;
 };
 
-// V channels of a thread; two go through packed instructions.
+// A thread's two channels; arithmetic goes through packed instructions.
 template <int V>
 struct Vec {
+    static_assert(V == 2, "two channels a thread");
     float v[V];
 };
 template <int V>
 __device__ __forceinline__ Vec<V> fill(float x) {
-    Vec<V> r;
-#pragma unroll
-    for (int i = 0; i < V; ++i) r.v[i] = x;
-    return r;
+    return {{x, x}};
 }
 template <int V>
 __device__ __forceinline__ Vec<V> mul(const Vec<V> &a, const Vec<V> &b) {
-    Vec<V> r;
-    if constexpr (V == 2) {
-        const float2 x = __fmul2_rn(make_float2(a.v[0], a.v[1]), make_float2(b.v[0], b.v[1]));
-        r.v[0] = x.x;
-        r.v[1] = x.y;
-    } else {
-        r.v[0] = a.v[0] * b.v[0];
-    }
-    return r;
+    const float2 x = __fmul2_rn(make_float2(a.v[0], a.v[1]), make_float2(b.v[0], b.v[1]));
+    return {{x.x, x.y}};
 }
 template <int V>
 __device__ __forceinline__ Vec<V> add(const Vec<V> &a, const Vec<V> &b) {
-    Vec<V> r;
-    if constexpr (V == 2) {
-        const float2 x = __fadd2_rn(make_float2(a.v[0], a.v[1]), make_float2(b.v[0], b.v[1]));
-        r.v[0] = x.x;
-        r.v[1] = x.y;
-    } else {
-        r.v[0] = a.v[0] + b.v[0];
-    }
-    return r;
+    const float2 x = __fadd2_rn(make_float2(a.v[0], a.v[1]), make_float2(b.v[0], b.v[1]));
+    return {{x.x, x.y}};
 }
 template <int V>
 __device__ __forceinline__ Vec<V> fma(const Vec<V> &a, const Vec<V> &b, const Vec<V> &c) {
-    Vec<V> r;
-    if constexpr (V == 2) {
-        const float2 x = __ffma2_rn(make_float2(a.v[0], a.v[1]), make_float2(b.v[0], b.v[1]),
-                                    make_float2(c.v[0], c.v[1]));
-        r.v[0] = x.x;
-        r.v[1] = x.y;
-    } else {
-        r.v[0] = fmaf(a.v[0], b.v[0], c.v[0]);
-    }
-    return r;
+    const float2 x = __ffma2_rn(make_float2(a.v[0], a.v[1]), make_float2(b.v[0], b.v[1]), make_float2(c.v[0], c.v[1]));
+    return {{x.x, x.y}};
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {   // the hardware's, 2 ulp, zero below 2^-126

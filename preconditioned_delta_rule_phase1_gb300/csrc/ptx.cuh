@@ -208,12 +208,10 @@ __device__ __forceinline__ uint32_t cluster_map(const void *p, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
 }
+// Into another CTA's shared memory, at an address of cluster_map.
 __device__ __forceinline__ void cluster_store(uint32_t a, float4 v) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
-}
-__device__ __forceinline__ void cluster_store(uint32_t a, float2 v) {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
 // ---------------------------------------------------------------- UMMA
