@@ -27,12 +27,8 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
     __shared__ Join j;
     Walk<io_t, R, W, 3> k(p, sm, true);
     typedef Rows<io_t, R, W> rows;
-    const size_t state = (size_t)k.b * p.C + k.c;
     if (k.n > 1) ptx::cluster_arrive();   // every CTA of the cluster has started once all have arrived
-    Vec<V> s = fill<V>(0.0f);
-    if (p.first && k.live)
-#pragma unroll
-        for (int v = 0; v < V; ++v) s.v[v] = p.first[state + v];
+    Vec<V> s = k.load_state(p, p.first);
     const size_t far = (size_t)k.stride * p.C;
     const auto fetch = [&](int step, int ahead) {
         if (step + ahead < p.steps) {
