@@ -74,8 +74,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
 #pragma unroll
             for (int v = 0; v < V; ++v) most = fmaxf(most, fabsf(g.v[v]));
         }
-        // all tokens there and no factor zero, for the whole warp
-        const bool usual = __all_sync(kFullMask, tokens >= R && (most <= kPlainGate || !k.live));
+        // all tokens there, no factor zero and nothing infinite, for the whole warp
+        bool usual = __all_sync(kFullMask, tokens >= R && (most <= kPlainGate || !k.live));
         Vec<V> co[R], wx[R];
         Vec<V> A = fill<V>(1.0f), E = fill<V>(0.0f);
         const auto exact = [&](auto z) {
@@ -93,10 +93,15 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
                 }
             }
         };
-        if (!usual) {
+        if constexpr (!kShort) {
+            if (usual) {
+                exact(std::false_type());
+                usual = __all_sync(kFullMask, finite(E));
+                if (!usual) A = fill<V>(1.0f), E = fill<V>(0.0f);
+            }
+            if (!usual) exact(std::true_type());
+        } else if (!usual) {
             exact(std::true_type());
-        } else if constexpr (!kShort) {
-            exact(std::false_type());
         } else {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
@@ -113,8 +118,10 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
         char *out = reinterpret_cast<char *>(static_cast<io_t *>(p.out) + k.at + k.lane * V);
         unsigned pitch = k.pitch;
         asm volatile("" : "+r"(pitch));
+        const Vec<V> before = q;
         const auto run = [&](auto z) {
             constexpr bool Z = decltype(z)::value;
+            q = before;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 if (!Z && kShort) {
@@ -126,7 +133,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
                 if (k.live && (!Z || i < tokens)) put<rows::kPaired>(reinterpret_cast<io_t *>(out + (size_t)i * pitch), q, k.second);
             }
         };
-        if (!usual) run(std::true_type()); else run(std::false_type());
+        if (usual) {
+            run(std::false_type());
+            if constexpr (!kShort) usual = finite(q);
+        }
+        if (!usual) run(std::true_type());
         k.t0 += k.stride;
         k.at += far;
     }

@@ -84,11 +84,18 @@ __device__ __forceinline__ bool keeps(float c) { return (int)__float_as_uint(c) 
 __device__ __forceinline__ bool forgets(float c) { return __float_as_uint(c) == 0u; }          // a = 0
 __device__ __forceinline__ bool passes(float c) { return __float_as_uint(c) == 0x80000000u; }  // 1 - a = 0
 
-// a v.  Z: the factor may be exactly zero (without Z the callers have looked that none is).
+// a v.  Z: any factor and any v: one that is exactly zero hides v, and v + c v of an infinite v is v.
+// Without Z no factor is zero (the callers have looked), and an infinite v becomes NaN, which the
+// recurrence then carries to its end: the callers look there, and do it again with Z.
 template <bool Z>
 __device__ __forceinline__ float decay(float c, float v) {
     if (Z && forgets(c)) return 0.0f;
+    if (Z && keeps(c) && fabsf(v) == INFINITY) return v;
     return fmaf(c, v, keeps(c) ? v : 0.0f);
+}
+template <int V>
+__device__ __forceinline__ bool finite(const Vec<V> &a) {
+    return fabsf(a.v[0]) < INFINITY && fabsf(a.v[1]) < INFINITY;
 }
 // w(a)^2 = 1 - a^2 = s (2 - s), or 1 - s^2
 __device__ __forceinline__ float unit_square(float c) { return fmaf(-c, c, keeps(c) ? -2.0f * c : 1.0f); }

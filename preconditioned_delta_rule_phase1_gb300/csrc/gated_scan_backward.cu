@@ -75,9 +75,10 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
 #pragma unroll
             for (int v = 0; v < V; ++v) most = fmaxf(most, fabsf(g.v[v]));
         }
-        const bool usual = __all_sync(kFullMask, tokens >= R && (most <= kPlainGate || !k.live));
+        bool usual = __all_sync(kFullMask, tokens >= R && (most <= kPlainGate || !k.live));
         Vec<V> h = wide(row);
         if (k.t0 == 0) h = k.load_state(p, p.h0);
+        const Vec<V> first = h;
         Vec<V> co[R], slope[R];   // (co: c, or e^-g in the short form)
         raw_t d[R];
         Vec<V> A = fill<V>(1.0f), E = fill<V>(0.0f);
@@ -98,10 +99,15 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
                 }
             }
         };
-        if (!usual) {
+        if constexpr (!kShort) {
+            if (usual) {
+                exact(std::false_type());
+                usual = __all_sync(kFullMask, finite(h) && finite(E));
+                if (!usual) h = first, A = fill<V>(1.0f), E = fill<V>(0.0f);
+            }
+            if (!usual) exact(std::true_type());
+        } else if (!usual) {
             exact(std::true_type());
-        } else if constexpr (!kShort) {
-            exact(std::false_type());
         } else {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
@@ -124,8 +130,10 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
         char *dg = reinterpret_cast<char *>(static_cast<io_t *>(p.dgate) + k.at + k.lane * V);
         unsigned pitch = k.pitch;
         asm volatile("" : "+r"(pitch));
+        const Vec<V> behind = q;
         const auto run = [&](auto z) {
             constexpr bool Z = decltype(z)::value;
+            q = behind;
 #pragma unroll
             for (int i = R - 1; i >= 0; --i) {
                 const Vec<V> r = add(wide(d[i]), q);
@@ -145,13 +153,25 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
                         q.v[v] = decay<Z>(co[i].v[v], r.v[v]);
                     }
                 }
+                Vec<V> gx = MIX == OSDN_MIX_SUM ? r : mul(w, r), gg = mul(slope[i], r);
+                if constexpr (Z) {   // w and a (1 - a) that are exactly zero hide r
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        if (MIX != OSDN_MIX_SUM && passes(co[i].v[v])) gx.v[v] = 0.0f;
+                        if (passes(co[i].v[v]) || forgets(co[i].v[v])) gg.v[v] = 0.0f;
+                    }
+                }
                 if (k.live && (!Z || i < tokens)) {
-                    put<rows::kPaired>(reinterpret_cast<io_t *>(dx + (size_t)i * pitch), MIX == OSDN_MIX_SUM ? r : mul(w, r), k.second);
-                    put<rows::kPaired>(reinterpret_cast<io_t *>(dg + (size_t)i * pitch), mul(slope[i], r), k.second);
+                    put<rows::kPaired>(reinterpret_cast<io_t *>(dx + (size_t)i * pitch), gx, k.second);
+                    put<rows::kPaired>(reinterpret_cast<io_t *>(dg + (size_t)i * pitch), gg, k.second);
                 }
             }
         };
-        if (!usual) run(std::true_type()); else run(std::false_type());
+        if (usual) {
+            run(std::false_type());
+            if constexpr (!kShort) usual = finite(q);
+        }
+        if (!usual) run(std::true_type());
         k.t0 -= k.stride;
         k.at -= far;
     }
