@@ -601,11 +601,12 @@ int osdn_clip_grad_norm(int n, const void *const *grads, void *const *outs,
  * padded batch: hT is then the state after the last token that counts).
  * Otherwise an infinity or NaN reaches the later tokens of its channel, at
  * least until the product of the gates behind it leaves fp32's range.
- * The state is carried in fp32 and only rounded where it is stored in h.  With
- * fp32 I/O 1 - a enters the state with all its digits; with bf16 I/O a is
- * rounded to fp32 (the gate's own rounding to bf16 moves 1 - a far more).  The
+ * The state is carried in fp32 and only rounded where it is stored in h.  The
  * time axis is cut into runs that are worked on side by side and joined in a
- * fixed order: results are the same on every run.  The call needs no workspace.
+ * fixed order: results are the same on every run.  However near 1 the gates are,
+ * a run's decay reaches the state to within about 1e-5 of that decay, in either
+ * I/O type; the state itself is an fp32 sum with a term for every 32 tokens at
+ * least.  The call needs no workspace.
  * With T == 0 it writes hT = h0 and nothing else.  C is any number of channels
  * up to 2^24; T may be at most 1,073,741,760 and B ceil(C/32) ceil(T/16) below
  * 2^31.  Outputs must not overlap inputs or each other (OSDN_ERR_ALIAS).

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
         // all tokens there, no factor zero and nothing infinite, for the whole warp
         bool usual = __all_sync(kFullMask, tokens >= R && (most <= kPlainGate || !k.live));
         Vec<V> co[R], wx[R];
-        Vec<V> A = fill<V>(1.0f), E = fill<V>(0.0f);
+        Vec<V> A = fill<V>(1.0f), D = fill<V>(0.0f), E = D;   // (D: 1 - A)
         const auto exact = [&](auto z) {
             constexpr bool Z = decltype(z)::value;
 #pragma unroll
@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
                     // tokens past the end leave everything as it is
                     co[i].v[v] = !Z || i < tokens ? gate_coefficient(g.v[v]) : -0.0f;
                     wx[i].v[v] = !Z || i < tokens ? weighted<MIX, Z>(co[i].v[v], x.v[v]) : 0.0f;
+                    D.v[v] = decay_rest(co[i].v[v], A.v[v], D.v[v]);
                     A.v[v] = decay<Z>(co[i].v[v], A.v[v]);
                     E.v[v] = decay<Z>(co[i].v[v], E.v[v]) + wx[i].v[v];
                 }
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
             if (usual) {
                 exact(std::false_type());
                 usual = __all_sync(kFullMask, finite(E));
-                if (!usual) A = fill<V>(1.0f), E = fill<V>(0.0f);
+                if (!usual) A = fill<V>(1.0f), D = E = fill<V>(0.0f);
             }
             if (!usual) exact(std::true_type());
         } else if (!usual) {
@@ -106,15 +107,20 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 Vec<V> f;
-                const Vec<V> x = wide(rows::get(xs, i, inx, k.pitch));
-                sigmoids(exponentials(wide(rg[i])), co[i], f);
+                const Vec<V> x = wide(rows::get(xs, i, inx, k.pitch)), e = exponentials(wide(rg[i]));
+                sigmoids(e, co[i], f);
                 wx[i] = MIX == OSDN_MIX_SUM ? x : mul(weight<MIX>(co[i], f), x);
-                A = mul(A, co[i]);
+                D = fma(D, e, add(D, e));   // the product of the 1 + e, less 1: 1 / A - 1
                 E = fma(E, co[i], wx[i]);
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                A.v[v] = rcp_fast(1.0f + D.v[v]);
+                D.v[v] = D.v[v] < 1.0f ? D.v[v] * A.v[v] : 1.0f;   // (own_run then takes A)
             }
         }
         __syncwarp();   // the stage is read
-        Vec<V> q = join(j, step & 1, k.n, k.rank, k.warp, !usual, Pair{A, E}, s, [&] { fetch(step, kStages); });
+        Vec<V> q = join(j, step & 1, k.n, k.rank, k.warp, own_run(A, D, E), s, [&] { fetch(step, kStages); });
         char *out = reinterpret_cast<char *>(static_cast<io_t *>(p.out) + k.at + k.lane * V);
         unsigned pitch = k.pitch;
         asm volatile("" : "+r"(pitch));
@@ -141,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
         k.t0 += k.stride;
         k.at += far;
     }
-    if (k.rank == 0 && k.warp == 0) k.store_state(p, p.last, s);
+    if (k.rank == 0 && k.warp == kWarps - 1) k.store_state(p, p.last, s);   // (the last in turn)
 }
 
 // One token: h and the I/O tensors are flat, four elements a thread.

@@ -5,16 +5,16 @@
 // dropped (g >= 0):
 //     g >= 0:  1 - a = s = -c,  a v = v + c v
 //     g <  0:      a = s =  c,  a v = c v
-// Both a and 1 - a then have all their digits: a itself, rounded to fp32, says
-// too little of 1 - a for memories of thousands of tokens (2^-25, an error of
-// the same sign at every token of a constant gate).  g = -inf is c = +0, g =
-// +inf is c = -0; a factor that is exactly zero hides what it multiplies.
+// Both a and 1 - a then have all their digits.  g = -inf is c = +0, g = +inf is
+// c = -0; a factor that is exactly zero hides what it multiplies.
 //
 // The short one, for bf16 I/O and |g| <= kPlainGate, multiplies with a rounded
-// to fp32: a bf16 gate knows its own 1 - a to 2^-8 g of itself, which is far
-// more than that rounding takes away (at g = 7, 1 - a = 9e-4 to 2.7%, and 2^-25
-// is 0.003% of it), and instructions are what bounds bf16.  The weight of x
-// reads 1 - a as e^-g a, with its digits, in both forms.
+// to fp32, within the run of at most 16 tokens that a thread holds: instructions
+// are what costs most there, and a state is off by 16 roundings (2^-23 of it each)
+// for that, whatever the gate.  How a state passes from run to run is taken from
+// 1 - A with its digits in both forms (gated_scan_walk.cuh): a rounded a, taken
+// 2^16 times, would be off by 1e-3 at a gate of 11, and keep all from a gate of 17
+// on.  The weight of x reads 1 - a as e^-g a, with its digits, in both forms.
 #pragma once
 
 #include "osdn_device.cuh"
@@ -93,6 +93,8 @@ __device__ __forceinline__ float decay(float c, float v) {
     if (Z && keeps(c) && fabsf(v) == INFINITY) return v;
     return fmaf(c, v, keeps(c) ? v : 0.0f);
 }
+// 1 - A, with its digits, as A becomes a A
+__device__ __forceinline__ float decay_rest(float c, float A, float D) { return fmaf(-c, A, keeps(c) ? D : 1.0f); }
 template <int V>
 __device__ __forceinline__ bool finite(const Vec<V> &a) {
     return fabsf(a.v[0]) < INFINITY && fabsf(a.v[1]) < INFINITY;

@@ -1,8 +1,8 @@
 // gated_scan_backward.cu -- the gradients of the gated recurrence; gated_scan.cu
 // has the formulas and the design.
 //
-// Measured (bf16, 2x8192x2048, five tensors of 67 MB): sum 68, unit 85, mean 91
-// us (0.73, 0.58 and 0.54 of the measured copy bandwidth); fp32 64 us at
+// Measured (bf16, 2x8192x2048, five tensors of 67 MB): sum 72, unit 91, mean 89
+// us (0.68, 0.54 and 0.56 of the measured copy bandwidth); fp32 66 us at
 // 2x4096x2048, mean.  Bound by instruction issue (0.45 of the slots at 16 warps
 // an SM) and a step's latency.  Only e^-g and the slope of the gate stay in
 // registers between the two passes over a thread's tokens; with a and w kept
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
         const Vec<V> first = h;
         Vec<V> co[R], slope[R];   // (co: c, or e^-g in the short form)
         raw_t d[R];
-        Vec<V> A = fill<V>(1.0f), E = fill<V>(0.0f);
+        Vec<V> A = fill<V>(1.0f), D = fill<V>(0.0f), E = D;   // (D: 1 - A)
         const auto exact = [&](auto z) {
             constexpr bool Z = decltype(z)::value;
 #pragma unroll
@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
                     co[i].v[v] = !Z || i < tokens ? gate_coefficient(g.v[v]) : -0.0f;
                     slope[i].v[v] = slope_of<MIX, Z>(co[i].v[v], h.v[v], x.v[v]);
                     h.v[v] = decay<Z>(co[i].v[v], h.v[v]) + (!Z || i < tokens ? weighted<MIX, Z>(co[i].v[v], x.v[v]) : 0.0f);
+                    D.v[v] = decay_rest(co[i].v[v], A.v[v], D.v[v]);
                     A.v[v] = decay<Z>(co[i].v[v], A.v[v]);
                     E.v[v] = Z && A.v[v] == 0.0f ? E.v[v] : fmaf(A.v[v], di.v[v], E.v[v]);
                 }
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
             if (usual) {
                 exact(std::false_type());
                 usual = __all_sync(kFullMask, finite(h) && finite(E));
-                if (!usual) h = first, A = fill<V>(1.0f), E = fill<V>(0.0f);
+                if (!usual) h = first, A = fill<V>(1.0f), D = E = fill<V>(0.0f);
             }
             if (!usual) exact(std::true_type());
         } else if (!usual) {
@@ -117,12 +118,13 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
                 sigmoids(co[i], a, f);
                 slope[i] = slope_and_next<MIX>(a, f, x, h);
                 d[i] = rows::get(ds, i, ind, k.pitch);
+                D = fma(f, A, D);
                 A = mul(A, a);
                 E = fma(A, wide(d[i]), E);
             }
         }
         __syncwarp();
-        Vec<V> q = join(j, step & 1, k.n, k.rank, kWarps - 1 - k.warp, !usual, Pair{A, E}, s, [&] {
+        Vec<V> q = join(j, step & 1, k.n, k.rank, kWarps - 1 - k.warp, own_run(A, D, E), s, [&] {
             fetch(step, kStages);
             row = before(k.t0 - k.stride, k.at - far);
         });
@@ -175,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
         k.t0 -= k.stride;
         k.at -= far;
     }
-    if (k.rank == 0 && k.warp == 0) k.store_state(p, p.last, s);
+    if (k.rank == 0 && k.warp == 0) k.store_state(p, p.last, s);   // (the last in turn)
 }
 
 }  // namespace
