@@ -599,6 +599,9 @@ int osdn_clip_grad_norm(int n, const void *const *grads, void *const *outs,
  * document in a packed sequence), and with OSDN_MIX_MEAN or OSDN_MIX_UNIT one
  * whose gate is +infinity leaves the state as it is and does not read x (a
  * padded batch: hT is then the state after the last token that counts).
+ * Factors are formed in fp32: of finite gates, a is zero from about -104 down,
+ * 1 - a from about 104 up and sqrt(1 - a^2) from about 208 up; on the way there
+ * from a gate of 88 (175) on they have fewer digits than elsewhere.
  * Otherwise an infinity or NaN reaches the later tokens of its channel, at
  * least until the product of the gates behind it leaves fp32's range.
  * The state is carried in fp32 and only rounded where it is stored in h.  The

@@ -86,9 +86,9 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
                     // tokens past the end leave everything as it is
-                    co[i].v[v] = !Z || i < tokens ? gate_coefficient(g.v[v]) : -0.0f;
+                    co[i].v[v] = !Z || i < tokens ? gate_coefficient<Z>(g.v[v]) : kPasses;
                     wx[i].v[v] = !Z || i < tokens ? weighted<MIX, Z>(co[i].v[v], x.v[v]) : 0.0f;
-                    D.v[v] = decay_rest(co[i].v[v], A.v[v], D.v[v]);
+                    D.v[v] = decay_rest<Z>(co[i].v[v], A.v[v], D.v[v]);
                     A.v[v] = decay<Z>(co[i].v[v], A.v[v]);
                     E.v[v] = decay<Z>(co[i].v[v], E.v[v]) + wx[i].v[v];
                 }
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(128) step_kernel(long long n, const io_t *x, c
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float c = gate_coefficient(gv[e]);
+        const float c = gate_coefficient<true>(gv[e]);
         hv[e] = decay<true>(c, hv[e]) + weighted<MIX, true>(c, xv[e]);
     }
     if (whole) {

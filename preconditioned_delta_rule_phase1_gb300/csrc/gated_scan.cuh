@@ -5,8 +5,7 @@
 // dropped (g >= 0):
 //     g >= 0:  1 - a = s = -c,  a v = v + c v
 //     g <  0:      a = s =  c,  a v = c v
-// Both a and 1 - a then have all their digits.  g = -inf is c = +0, g = +inf is
-// c = -0; a factor that is exactly zero hides what it multiplies.
+// Both a and 1 - a then have all their digits.
 //
 // The short one, for bf16 I/O and |g| <= kPlainGate, multiplies with a rounded
 // to fp32, within the run of at most 16 tokens that a thread holds: instructions
@@ -76,34 +75,52 @@ __device__ __forceinline__ float rsqrt_fast(float x) {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------- the exact form
+// In two kinds.  Without Z: no gate beyond kPlainGate, so that no factor leaves fp32's normal range, and
+// nothing infinite (an infinite v becomes NaN, which the recurrence then carries to its end: the callers look
+// there, and do it again with Z).  With Z: any gate, any v.  A factor may then be exactly zero, and hides what
+// it multiplies.  A gate g above kPlainGate is held as c = -g: 1 - a is less than 2^-115, nothing beside any v
+// of the same channel, and what is formed of it comes from e^-g or e^(-g / 2) as it is needed.
+constexpr float kPlainGate = 80.0f;   // e^80 and its reciprocal are normal numbers
+constexpr float kPasses = -INFINITY;  // c of a gate of +inf
+__device__ __forceinline__ float exp2_whole(float x) {   // with what lies below 2^-126
+    float e;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x));
+    return e;
+}
+template <bool Z>
 __device__ __forceinline__ float gate_coefficient(float g) {
-    const float e = exp2_fast(fabsf(g) * -kLog2e);
+    if (Z && g > kPlainGate) return -g;
+    const float t = fabsf(g) * -kLog2e, e = Z ? exp2_whole(t) : exp2_fast(t);
     return __uint_as_float(__float_as_uint(e * rcp_fast(1.0f + e)) | (~__float_as_uint(g) & 0x80000000u));
 }
 __device__ __forceinline__ bool keeps(float c) { return (int)__float_as_uint(c) < 0; }
-__device__ __forceinline__ bool forgets(float c) { return __float_as_uint(c) == 0u; }          // a = 0
-__device__ __forceinline__ bool passes(float c) { return __float_as_uint(c) == 0x80000000u; }  // 1 - a = 0
+__device__ __forceinline__ bool forgets(float c) { return __float_as_uint(c) == 0u; }   // a = 0
+__device__ __forceinline__ bool open(float c) { return c < -1.0f; }                      // c is minus the gate
 
-// a v.  Z: any factor and any v: one that is exactly zero hides v, and v + c v of an infinite v is v.
-// Without Z no factor is zero (the callers have looked), and an infinite v becomes NaN, which the
-// recurrence then carries to its end: the callers look there, and do it again with Z.
+// a v
 template <bool Z>
 __device__ __forceinline__ float decay(float c, float v) {
     if (Z && forgets(c)) return 0.0f;
-    if (Z && keeps(c) && fabsf(v) == INFINITY) return v;
+    if (Z && (open(c) || (keeps(c) && fabsf(v) == INFINITY))) return v;
     return fmaf(c, v, keeps(c) ? v : 0.0f);
 }
 // 1 - A, with its digits, as A becomes a A
-__device__ __forceinline__ float decay_rest(float c, float A, float D) { return fmaf(-c, A, keeps(c) ? D : 1.0f); }
+template <bool Z>
+__device__ __forceinline__ float decay_rest(float c, float A, float D) {
+    if (Z && open(c)) return D;
+    return fmaf(-c, A, keeps(c) ? D : 1.0f);
+}
 template <int V>
 __device__ __forceinline__ bool finite(const Vec<V> &a) {
     return fabsf(a.v[0]) < INFINITY && fabsf(a.v[1]) < INFINITY;
 }
 // w(a)^2 = 1 - a^2 = s (2 - s), or 1 - s^2
 __device__ __forceinline__ float unit_square(float c) { return fmaf(-c, c, keeps(c) ? -2.0f * c : 1.0f); }
-template <int MIX>
+template <int MIX, bool Z>
 __device__ __forceinline__ float weight(float c) {
     if (MIX == OSDN_MIX_SUM) return 1.0f;
+    if (Z && open(c))   // e^-g, or sqrt(2) e^(-g / 2)
+        return MIX == OSDN_MIX_MEAN ? exp2_whole(c * kLog2e) : 1.41421356f * exp2_whole(c * (0.5f * kLog2e));
     if (MIX == OSDN_MIX_MEAN) return keeps(c) ? -c : 1.0f - c;
     return sqrt_fast(unit_square(c));
 }
@@ -111,25 +128,47 @@ __device__ __forceinline__ float weight(float c) {
 template <int MIX, bool Z>
 __device__ __forceinline__ float weighted(float c, float x) {
     if (MIX == OSDN_MIX_SUM) return x;
-    if (Z && passes(c)) return 0.0f;
-    return weight<MIX>(c) * x;
+    const float w = weight<MIX, Z>(c);
+    return Z && w == 0.0f ? 0.0f : w * x;
 }
+// the gate from which on e^-g, or e^(-g / 2) where that counts, is zero in fp32
+template <int MIX>
+__device__ __forceinline__ constexpr float zero_from() { return MIX == OSDN_MIX_UNIT ? 208.0f : 104.0f; }
 // With v the state before a token: the factor that turns R into the gradient of g, a b v + w' x =
 // a b (v - k x), where k is 0, 1 or a / w.  (w' = -a / w times a b, and k a b = a^2 sqrt((1 - a) /
 // (1 + a)) goes to zero where w does.)
+// a b and k a b
+template <int MIX, bool Z>
+__device__ __forceinline__ void slope_factors(float c, float &ab, float &kab) {
+    const float s = fabsf(c);
+    if (Z && open(c)) {
+        ab = c > -104.0f ? exp2_whole(c * kLog2e) : 0.0f;
+        if (c <= -zero_from<MIX>()) { kab = 0.0f; return; }
+        kab = MIX == OSDN_MIX_UNIT ? 0.70710678f * exp2_whole(c * (0.5f * kLog2e)) : MIX == OSDN_MIX_MEAN ? ab : 0.0f;
+        return;
+    }
+    ab = fmaf(-s, s, s);
+    // (k a b first: k alone can be large, and with a large x leave fp32)
+    kab = MIX == OSDN_MIX_UNIT ? (keeps(c) ? 1.0f + c : c) * (ab * rsqrt_fast(unit_square(c)))
+                               : MIX == OSDN_MIX_MEAN ? ab : 0.0f;
+}
 template <int MIX, bool Z>
 __device__ __forceinline__ float slope_of(float c, float v, float x) {
-    const float s = fabsf(c), ab = fmaf(-s, s, s);
-    if (Z && ab == 0.0f) return 0.0f;
+    float ab, kab;
+    slope_factors<MIX, Z>(c, ab, kab);
+    if (Z) {
+        const float y = kab == 0.0f ? 0.0f : -kab * x;
+        return ab == 0.0f ? y : fmaf(ab, v, y);
+    }
     if (MIX == OSDN_MIX_SUM) return ab * v;
     if (MIX == OSDN_MIX_MEAN) return ab * (v - x);
-    // (k a b first: k alone can be large, and with a large x leave fp32)
-    const float kab = (keeps(c) ? 1.0f + c : c) * (ab * rsqrt_fast(fmaxf(unit_square(c), 1e-37f)));
     return fmaf(ab, v, -kab * x);
 }
+// whether the gradient of g is zero whatever R is
+template <int MIX>
+__device__ __forceinline__ bool no_slope(float c) { return forgets(c) || c <= -zero_from<MIX>(); }
 
 // ------------------------------------------------------------- the short form
-constexpr float kPlainGate = 80.0f;   // e^80 and its reciprocal are normal numbers
 // e^-g, and from it a and b = 1 - a
 template <int V>
 __device__ __forceinline__ Vec<V> exponentials(const Vec<V> &g) {

@@ -1,8 +1,8 @@
 // gated_scan_backward.cu -- the gradients of the gated recurrence; gated_scan.cu
 // has the formulas and the design.
 //
-// Measured (bf16, 2x8192x2048, five tensors of 67 MB): sum 72, unit 91, mean 89
-// us (0.68, 0.54 and 0.56 of the measured copy bandwidth); fp32 66 us at
+// Measured (bf16, 2x8192x2048, five tensors of 67 MB): sum 70, unit 87, mean 89
+// us (0.70, 0.57 and 0.56 of the measured copy bandwidth); fp32 66 us at
 // 2x4096x2048, mean.  Bound by instruction issue (0.45 of the slots at 16 warps
 // an SM) and a step's latency.  Only e^-g and the slope of the gate stay in
 // registers between the two passes over a thread's tokens; with a and w kept
@@ -91,10 +91,10 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
                 const Vec<V> di = wide(d[i]);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    co[i].v[v] = !Z || i < tokens ? gate_coefficient(g.v[v]) : -0.0f;
+                    co[i].v[v] = !Z || i < tokens ? gate_coefficient<Z>(g.v[v]) : kPasses;
                     slope[i].v[v] = slope_of<MIX, Z>(co[i].v[v], h.v[v], x.v[v]);
                     h.v[v] = decay<Z>(co[i].v[v], h.v[v]) + (!Z || i < tokens ? weighted<MIX, Z>(co[i].v[v], x.v[v]) : 0.0f);
-                    D.v[v] = decay_rest(co[i].v[v], A.v[v], D.v[v]);
+                    D.v[v] = decay_rest<Z>(co[i].v[v], A.v[v], D.v[v]);
                     A.v[v] = decay<Z>(co[i].v[v], A.v[v]);
                     E.v[v] = Z && A.v[v] == 0.0f ? E.v[v] : fmaf(A.v[v], di.v[v], E.v[v]);
                 }
@@ -151,16 +151,16 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
                 } else {
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        w.v[v] = weight<MIX>(co[i].v[v]);
+                        w.v[v] = weight<MIX, Z>(co[i].v[v]);
                         q.v[v] = decay<Z>(co[i].v[v], r.v[v]);
                     }
                 }
                 Vec<V> gx = MIX == OSDN_MIX_SUM ? r : mul(w, r), gg = mul(slope[i], r);
-                if constexpr (Z) {   // w and a (1 - a) that are exactly zero hide r
+                if constexpr (Z) {   // factors that are exactly zero hide r
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        if (MIX != OSDN_MIX_SUM && passes(co[i].v[v])) gx.v[v] = 0.0f;
-                        if (passes(co[i].v[v]) || forgets(co[i].v[v])) gg.v[v] = 0.0f;
+                        if (w.v[v] == 0.0f) gx.v[v] = 0.0f;
+                        if (no_slope<MIX>(co[i].v[v])) gg.v[v] = 0.0f;
                     }
                 }
                 if (k.live && (!Z || i < tokens)) {
