@@ -611,8 +611,8 @@ int osdn_clip_grad_norm(int n, const void *const *grads, void *const *outs,
  * I/O type; the state itself is an fp32 sum with a term for every 32 tokens at
  * least.  The call needs no workspace.
  * With T == 0 it writes hT = h0 and nothing else.  C is any number of channels
- * up to 2^24; T may be at most 1,073,741,760 and B ceil(C/32) ceil(T/16) below
- * 2^31.  Outputs must not overlap inputs or each other (OSDN_ERR_ALIAS).
+ * up to 2^24; T may be at most 1,073,741,760, B ceil(C/64) below 2^31 and
+ * B T C at most 2^39.  Outputs must not overlap inputs or each other (OSDN_ERR_ALIAS).
  */
 int osdn_gated_scan(int io, int B, int T, int C, int mix, const void *x, const void *gate, const float *h0,
                     void *h, float *hT, void *stream);

@@ -32,15 +32,16 @@ using namespace osdn::api;
 
 constexpr int kMaxWidth = 16384;   // layer norm: a row stays in one CTA's registers
 constexpr long long kMaxRows = 0x7fffffff;
-constexpr int kMaxChannels = 1 << 24;   // the recurrence: 16 rows are addressed in 32 bits
+constexpr int kMaxChannels = 1 << 24;   // the recurrence: a row's bytes, and 16 rows' of bf16, are counted in 32 bits
 
 bool mix_ok(int mix) { return mix >= OSDN_MIX_SUM && mix <= OSDN_MIX_UNIT; }
 
-// Tiles of the recurrence (at least 16 tokens of 32 channels of a sequence) are numbered in 31 bits.
+// A CTA, or a cluster, takes 64 channels of a sequence, and CTAs are numbered in 31 bits; the rest is
+// addressed in 64 bits (2^39 elements are a terabyte in bf16, more than any device holds).
 bool scan_dims_ok(int B, int T, int C) {
     if (B < 0 || T < 0 || C < 0 || T > kMaxTokens || C > kMaxChannels) return false;
-    const double strips = (double)B * (((double)C + 31) / 32), chunks = ((double)T + 15) / 16;
-    return strips <= 2147483647.0 && strips * chunks <= 2147483647.0;
+    const double strips = (double)B * (((double)C + 63) / 64);
+    return strips <= 2147483647.0 && (double)B * C * T <= 549755813888.0;
 }
 bool norm_dims_ok(long long rows, int C) { return rows >= 0 && rows <= kMaxRows && C >= 1 && C <= kMaxWidth; }
 bool eps_ok(float eps) { return eps > 0.0f && !std::isinf(eps); }
