@@ -40,7 +40,7 @@ bool mix_ok(int mix) { return mix >= OSDN_MIX_SUM && mix <= OSDN_MIX_UNIT; }
 // addressed in 64 bits (2^39 elements are a terabyte in bf16, more than any device holds).
 bool scan_dims_ok(int B, int T, int C) {
     if (B < 0 || T < 0 || C < 0 || T > kMaxTokens || C > kMaxChannels) return false;
-    const double strips = (double)B * (((double)C + 63) / 64);
+    const double strips = (double)B * ((C + 63) / 64);
     return strips <= 2147483647.0 && (double)B * C * T <= 549755813888.0;
 }
 bool norm_dims_ok(long long rows, int C) { return rows >= 0 && rows <= kMaxRows && C >= 1 && C <= kMaxWidth; }
