@@ -32,6 +32,7 @@ import torch
 from . import build as _build
 
 OSDN_F32, OSDN_BF16 = 0, 1
+OSDN_ERR_DIMS = -2
 ACTS = {"none": 0, "silu": 1, "sigmoid": 2}
 MIXES = {"sum": 0, "mean": 1, "unit": 2}
 STATUS_BYTES = 256
@@ -826,6 +827,12 @@ def layer_norm_backward_workspace_bytes(rows, C) -> int:
     return int(lib().osdn_layer_norm_backward_workspace_bytes(rows, C))
 
 
+def _fits(name, *sizes):
+    """The C calls take these sizes as ints, which ctypes would cut a larger one down to."""
+    if max(sizes) > 0x7fffffff:
+        raise OsdnError(OSDN_ERR_DIMS, name)
+
+
 def _mix(mix):
     if mix not in MIXES:
         raise ValueError("mix must be one of %s, got %r" % (sorted(MIXES), mix))
@@ -843,6 +850,7 @@ def gated_scan(x, gate, h0=None, mix="mean", h=None, hT=None, workspace=None, st
     needs none."""
     m = _mix(mix)
     B, T, C = x.shape
+    _fits("osdn_gated_scan", B, T, C)
     io, dt, dev = _io(x), x.dtype, x.device
     if h is None:
         h = torch.empty((B, T, C), dtype=dt, device=dev)
@@ -860,6 +868,7 @@ def gated_scan_step(x, gate, h, mix="mean", y=None, stream=None):
     token x, gate [B,C] (io); returns y [B,C] (io), the state rounded."""
     m = _mix(mix)
     B, C = x.shape
+    _fits("osdn_gated_scan_step", B, C)
     io, dt, dev = _io(x), x.dtype, x.device
     if y is None:
         y = torch.empty((B, C), dtype=dt, device=dev)
@@ -876,6 +885,7 @@ def gated_scan_backward(x, gate, h, h0=None, *, dh, dhT=None, mix="mean", worksp
     gate (io) and, if h0 is given, h0 (fp32).  `workspace` as in ``gated_scan``."""
     m = _mix(mix)
     B, T, C = x.shape
+    _fits("osdn_gated_scan_backward", B, T, C)
     io, dt, dev = _io(x), x.dtype, x.device
     full = (B, T, C)
     args = (io, B, T, C, m, _arg("x", x, full, dt, dev), _arg("gate", gate, full, dt, dev),
@@ -897,6 +907,7 @@ def layer_norm(x, weight=None, bias=None, residual=None, eps=1e-5, y=None, s=Non
     if x.dim() == 0:
         raise ValueError("x must have a last dimension to norm over")
     C = x.shape[-1]
+    _fits("osdn_layer_norm", C)
     rows = x.numel() // C if C else 0
     io, dt, dev = _io(x), x.dtype, x.device
     if s is not None and residual is None:
@@ -920,6 +931,7 @@ def layer_norm_backward(x, dy, weight=None, bias=None, ds=None, eps=1e-5, worksp
     if x.dim() == 0:
         raise ValueError("x must have a last dimension to norm over")
     C = x.shape[-1]
+    _fits("osdn_layer_norm_backward", C)
     rows = x.numel() // C if C else 0
     io, dt, dev = _io(x), x.dtype, x.device
     args = (io, rows, C, _arg("x", x, x.shape, dt, dev), _arg("dy", dy, x.shape, dt, dev),

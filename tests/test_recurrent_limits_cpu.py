@@ -1,6 +1,7 @@
 """The sizes that the gated recurrence's C entry points take and refuse (no GPU needed:
 a call that is not refused stops at the device check, before anything is enqueued)."""
 import pytest
+import torch
 
 from preconditioned_delta_rule_phase1_gb300 import build as osdn_build
 from preconditioned_delta_rule_phase1_gb300 import ops
@@ -38,3 +39,24 @@ def test_what_cannot_be_numbered_is_refused(L):
         for B, T, C in ((MANY, 1, 65), (1 << 25, 1, 1 << 13), (1, 1073741761, 1), (1, 1, (1 << 24) + 1),
                         (1 << 20, 1 << 20, 1), (1, 1073741760, 1024)):
             assert call(L, B, T, C) == -2, (call, B, T, C)
+
+
+BIG = (1 << 32) + 16   # cut down to 32 bits: 16
+
+
+def test_sizes_that_do_not_fit_the_c_calls_are_refused_by_the_binding(L):
+    """Not passed on as what is left of them in 32 bits."""
+    new = lambda *shape, dtype=torch.float32: torch.empty(*shape, dtype=dtype, device="meta")  # noqa: E731
+    calls = []
+    for shape in ((1, BIG, 1), (BIG, 1, 1), (1, 1, BIG)):
+        x = new(*shape)
+        calls += [lambda x=x: ops.gated_scan(x, x), lambda x=x: ops.gated_scan_backward(x, x, x, dh=x)]
+    for shape in ((BIG, 1), (1, BIG)):
+        x = new(*shape)
+        calls += [lambda x=x: ops.gated_scan_step(x, x, x)]
+    x = new(1, BIG)
+    calls += [lambda: ops.layer_norm(x), lambda: ops.layer_norm_backward(x, x)]
+    for call in calls:
+        with pytest.raises(ops.OsdnError) as e:
+            call()
+        assert e.value.code == -2
