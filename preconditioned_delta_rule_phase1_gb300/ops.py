@@ -846,12 +846,14 @@ def gated_scan(x, gate, h0=None, mix="mean", h=None, hT=None, workspace=None, st
     ("mean") or sqrt(1 - a^2) ("unit").  Returns (h [B,T,C] (io), hT [B,C] fp32).
 
     A gate of -inf forgets what was before the token; with "mean" and "unit" one of +inf passes over
-    the token, whatever x holds there.  `workspace` is taken as by the other layers' calls; this one
-    needs none."""
+    the token, whatever x holds there.  `workspace` is taken, and has to fit, as by the other layers'
+    calls; this one needs none and does not touch it."""
     m = _mix(mix)
     B, T, C = x.shape
     _fits("osdn_gated_scan", B, T, C)
     io, dt, dev = _io(x), x.dtype, x.device
+    if workspace is not None:
+        _workspace(workspace, dev)
     if h is None:
         h = torch.empty((B, T, C), dtype=dt, device=dev)
     if hT is None:
@@ -887,6 +889,8 @@ def gated_scan_backward(x, gate, h, h0=None, *, dh, dhT=None, mix="mean", worksp
     B, T, C = x.shape
     _fits("osdn_gated_scan_backward", B, T, C)
     io, dt, dev = _io(x), x.dtype, x.device
+    if workspace is not None:
+        _workspace(workspace, dev)
     full = (B, T, C)
     args = (io, B, T, C, m, _arg("x", x, full, dt, dev), _arg("gate", gate, full, dt, dev),
             _arg("h", h, full, dt, dev), _arg("h0", h0, (B, C), F32, dev), _arg("dh", dh, full, dt, dev),

@@ -1,5 +1,7 @@
-"""The sizes that the gated recurrence's C entry points take and refuse (no GPU needed:
+"""The sizes and workspaces that the recurrent layer's calls take and refuse (no GPU needed:
 a call that is not refused stops at the device check, before anything is enqueued)."""
+import types
+
 import pytest
 import torch
 
@@ -60,3 +62,17 @@ def test_sizes_that_do_not_fit_the_c_calls_are_refused_by_the_binding(L):
         with pytest.raises(ops.OsdnError) as e:
             call()
         assert e.value.code == -2
+
+
+def test_a_workspace_of_another_device_is_refused(L):
+    """By the calls that need none, too, as by those that do."""
+    x = torch.zeros(2, 5, 64)
+    elsewhere = types.SimpleNamespace(buf=torch.empty(256, dtype=torch.uint8, device="meta"))
+    here = types.SimpleNamespace(buf=torch.empty(256, dtype=torch.uint8))
+    for call in (lambda ws: ops.gated_scan(x, x, workspace=ws),
+                 lambda ws: ops.gated_scan_backward(x, x, x, dh=x, workspace=ws),
+                 lambda ws: ops.layer_norm_backward(x, x, workspace=ws)):
+        with pytest.raises(ValueError, match="workspace is on meta"):
+            call(elsewhere)
+        with pytest.raises(ValueError, match="CUDA tensors only"):   # no argument was refused
+            call(here)
