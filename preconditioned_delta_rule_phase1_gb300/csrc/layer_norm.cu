@@ -444,8 +444,9 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
         } else {
             x0 = pivot(0, row + step, at + far);
         }
-        // x^ = r v - r m,  dx = r u + k v + k0
-        const float r = rsqrtf(var + p.eps), rm = -r * m, kx = -uv * r * r * r, k0 = fmaf(-kx, m, -r * mu);
+        // x^ = r v - r m,  dx = r u + k x^ + k0  (in v, k would have a cube of r, which may leave fp32 where dx
+        // does not)
+        const float r = rsqrtf(var + p.eps), rm = -r * m, kx = -uv * r * r, k0 = -r * mu;
         io_t *out = static_cast<io_t *>(p.dx) + at;
 #pragma unroll
         for (int n = 0; n < N; n += Q) {
@@ -457,11 +458,11 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
             for (int i = 0; i < EE; i += 2) {
                 const int o = n * E + i;
                 const float2 u = __fmul2_rn(get2(d, i), get2(w, o));
-                float2 f = __ffma2_rn(get2(v, o), two(kx), two(k0));
+                const float2 xh = __ffma2_rn(get2(v, o), two(r), two(rm));
+                float2 f = __ffma2_rn(xh, two(kx), two(k0));
                 f = __ffma2_rn(u, two(r), f);
                 if (ds) f = __fadd2_rn(f, get2(e, i));
                 put2(e, i, f);
-                const float2 xh = __ffma2_rn(get2(v, o), two(r), two(rm));
                 if (SMEM) {
                     float2 &sw = own[(o / 2) * (int)blockDim.x], &sb = own[(M / 2 + o / 2) * (int)blockDim.x];
                     sw = __ffma2_rn(get2(d, i), xh, sw);
