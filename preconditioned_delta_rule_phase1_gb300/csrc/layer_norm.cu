@@ -10,7 +10,8 @@
 // short and by up to 32 otherwise.  Differences to the row's first value come
 // before any sum, so that a large mean costs no accuracy; the norm then takes
 // the mean and the variance about it, two reductions, the gradients all four
-// sums in one (see there).  All arithmetic is fp32.
+// sums in one.  A row whose first value is an outlier (kFarSquare) takes them
+// again about its mean.  All arithmetic is fp32.
 //
 // Measured (bf16): the norm 48 us at 16384 rows of 2048 with a residual (5.6
 // TB/s, 0.83 of the measured copy bandwidth; 45 us among other calls), 125 us
@@ -246,6 +247,9 @@ struct Params {
 };
 
 constexpr int kMaxWarps = 32;
+// A row's first value may lie this far (four standard deviations, squared) from the mean: differences to it
+// are then rounded by 2^-22 of one.
+constexpr float kFarSquare = 16.0f;
 
 // A row a group of p.warps warps; several groups a CTA where that is one warp.
 template <typename io_t, int E, int N, int KIND, bool RES>
@@ -279,14 +283,43 @@ __global__ void __launch_bounds__(N * E == 8 ? 1024 : N * E == 16 ? 128 : 512) n
         sum = __fadd2_rn(sum, get2(v, i));
     }
     const float inv = 1.0f / (float)p.C;
-    const float m = row_sum(sum.x + sum.y, p.warps, tid / 32, part[0], 1) * inv;
-    sum = two(0.0f);
+    // the mean of v off, and the variance
+    const auto centre = [&](const P &g, float s, float &m) {
+        m = row_sum(s, p.warps, tid / 32, part[0], 1) * inv;
+        float2 q = two(0.0f);
 #pragma unroll
-    for (int i = 0; i < M; i += 2) {
-        put2(v, i, __fadd2_rn(get2(v, i), make_float2(g.pick(i, -m), g.pick(i + 1, -m))));
-        sum = __ffma2_rn(get2(v, i), get2(v, i), sum);
+        for (int i = 0; i < M; i += 2) {
+            put2(v, i, __fadd2_rn(get2(v, i), make_float2(g.pick(i, -m), g.pick(i + 1, -m))));
+            q = __ffma2_rn(get2(v, i), get2(v, i), q);
+        }
+        return row_sum(q.x + q.y, p.warps, tid / 32, part[1], 1) * inv;
+    };
+    float m, var = centre(g, sum.x + sum.y, m);
+    if (!(m * m <= kFarSquare * var)) {
+        // The first value lies far outside the others: the differences to it have lost their digits.  Those
+        // to the mean have them all, and their mean is what that one was off by.  (The whole row sees the
+        // same sums.)
+        const float mean = x0 + m;
+        P h = g;   // (its masks computed again: kept over the reductions, rows on words take twice the time)
+        asm volatile("" : "+r"(h.first), "+r"(h.count), "+r"(h.last));
+        h.load(x, rx);
+        P::wide(rx, v);
+        if (RES) {
+            float b[M];
+            h.load(res, rr);
+            P::wide(rr, b);
+#pragma unroll
+            for (int i = 0; i < M; i += 2) put2(v, i, __fadd2_rn(get2(v, i), get2(b, i)));
+        }
+        sum = two(0.0f);
+#pragma unroll
+        for (int i = 0; i < M; i += 2) {
+            put2(v, i, __fadd2_rn(get2(v, i), make_float2(h.pick(i, -mean), h.pick(i + 1, -mean))));
+            sum = __fadd2_rn(sum, get2(v, i));
+        }
+        var = centre(h, sum.x + sum.y, m);
     }
-    const float r = rsqrtf(fmaf(row_sum(sum.x + sum.y, p.warps, tid / 32, part[1], 1), inv, p.eps));
+    const float r = rsqrtf(var + p.eps);
     float w[M], b[M];
     g.affine(p.weight, 1.0f, w);
     g.affine(p.bias, 0.0f, b);
@@ -414,29 +447,33 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
         }
         float4 t = row_sum(make_float4(q[0].x + q[0].y, q[1].x + q[1].y, q[2].x + q[2].y, q[3].x + q[3].y), p.warps,
                            warp, part[odd] + group * p.warps, 1 + group);
-        const float m = t.x * inv, mu = t.z * inv;
-        float var = fmaf(-m, m, t.y * inv), uv = fmaf(-m, t.z, t.w) * inv;
-        if (!(m * m <= 16.0f * var)) {
-            // the first value lies far outside the others: the differences above have lost digits, so the
-            // sums are taken again about the mean (by the whole group, which sees the same sums)
-            float2 z[2] = {two(0.0f), two(0.0f)};
+        const float mu = t.z * inv;
+        float m = t.x * inv, var = fmaf(-m, m, t.y * inv), uv = fmaf(-m, t.z, t.w) * inv;
+        if (!(m * m <= kFarSquare * var)) {
+            // the first value lies far outside the others: differences and sums are taken again, about the mean
+            // (by the whole group, which sees the same sums)
+            const float mean = x0 + m;
+            float2 z[3] = {two(0.0f), two(0.0f), two(0.0f)};
 #pragma unroll
             for (int n = 0; n < N; n += Q) {
-                float d[EE];
+                float c[EE], d[EE];
+                read(s, 0, n, c);
                 read(s, 1, n, d);
 #pragma unroll
                 for (int i = 0; i < EE; i += 2) {
                     const int o = n * E + i;
-                    const float2 c = __fadd2_rn(get2(v, o), make_float2(g.pick(o, -m), g.pick(o + 1, -m)));
-                    z[0] = __ffma2_rn(c, c, z[0]);
-                    z[1] = __ffma2_rn(__fmul2_rn(get2(d, i), get2(w, o)), c, z[1]);
+                    put2(v, o, __fadd2_rn(get2(c, i), make_float2(g.pick(o, -mean), g.pick(o + 1, -mean))));
+                    z[0] = __fadd2_rn(z[0], get2(v, o));
+                    z[1] = __ffma2_rn(get2(v, o), get2(v, o), z[1]);
+                    z[2] = __ffma2_rn(__fmul2_rn(get2(d, i), get2(w, o)), get2(v, o), z[2]);
                 }
             }
             if (p.warps > 1) ptx::named_bar(1 + group, width);   // all have read the sums above
-            t = row_sum(make_float4(z[0].x + z[0].y, z[1].x + z[1].y, 0.0f, 0.0f), p.warps, warp,
+            t = row_sum(make_float4(z[0].x + z[0].y, z[1].x + z[1].y, mu, z[2].x + z[2].y), p.warps, warp,
                         part[odd] + group * p.warps, 1 + group);
-            var = t.x * inv;
-            uv = t.y * inv;
+            m = t.x * inv;   // (what the mean was off by)
+            var = fmaf(-m, m, t.y * inv);
+            uv = fmaf(-m, mu, t.w * inv);
         }
         if (S > 1) {
             if (p.warps == 1) __syncwarp();

@@ -1,5 +1,6 @@
-"""Layer norm and its gradients at sizes where squares or cubes of what is formed on the
-way could leave fp32, element by element against the formula in 64 bits.
+"""Layer norm and its gradients at rows whose first value lies far from the others, and
+at sizes where squares or cubes of what is formed on the way could leave fp32, element
+by element against the formula in 64 bits.
 
 Tolerance.  A row's mean is a sum of at most 48 roundings one after the other (32 values
 of a thread in pairs, 5 exchanges, 16 warps, and those of the differences), so it is off
@@ -47,6 +48,34 @@ def check(x, dy, io, eps, what):
                + xh.abs() * (56 * U * mean((u * xh).abs()) + mean(u.abs() * off))) + 56 * U * dx.abs()
     bad = (got - dx).abs() - (HALF[io] * dx.abs() + tol)
     assert bool((bad <= 0).all()), ("dx", what, float((bad / tol).max()))
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [40, 255, 513, 1000, 2047, 2048, 5000, 8192, 16383, 16384])
+def test_the_others_keep_their_digits(io, C):
+    g = torch.Generator().manual_seed(C)
+    x, dy = torch.randn(10, C, generator=g), torch.randn(10, C, generator=g)
+    x += 0.3
+    for r, far in enumerate((0.0, 5.0, 30.0, -300.0, 3e3, -1e5, 1e6, -1e7, 1e4, 100.0)):
+        x[r, 0] += far
+    x[8, C // 2] = -1e4   # another one far out, where the sums do not begin
+    check(x.to(DT[io]).cuda(), dy.to(DT[io]).cuda(), io, 1e-5, C)
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,C", [(3, 2048), (1500, 2048), (1500, 690), (1500, 300)])
+def test_the_sum_with_a_residual(residual, rows, C):
+    """The same with what few and many rows choose, and for the sum's norm."""
+    g = torch.Generator().manual_seed(C)
+    x, res = torch.randn(rows, C, generator=g), torch.randn(rows, C, generator=g)
+    x[::3, 0] = 2e5
+    x, res = x.cuda(), res.cuda()
+    s = x + res if residual else x
+    d = s.double() - mean(s.double())
+    xh = d / (mean(d * d) + 1e-5).sqrt()
+    y = ops.layer_norm(x, residual=res)[0] if residual else ops.layer_norm(x)
+    tol = 48 * U * mean(xh.abs()) + 60 * U * xh.abs()
+    assert bool(((y.double() - xh).abs() <= tol).all())
 
 
 @pytest.mark.parametrize("C", [64, 1000, 2048, 5000, 16384])
