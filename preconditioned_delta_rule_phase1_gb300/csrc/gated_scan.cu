@@ -55,13 +55,13 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
             k.fetch((step + ahead) % kStages, 0, p.gate, from, tokens);
             k.fetch((step + ahead) % kStages, 1, p.x, from, tokens);
         }
-        copies_commit();   // (a group a step, so that waiting counts them)
+        ptx::copies_commit();   // (a group a step, so that waiting counts them)
     };
 #pragma unroll
     for (int i = 0; i < kStages; ++i) fetch(0, i);
     if (k.n > 1) ptx::cluster_wait();
     for (int step = 0; step < p.steps; ++step) {
-        copies_wait<kStages - 1>();
+        ptx::copies_wait<kStages - 1>();
         __syncwarp();
         const int tokens = p.T - k.t0, in = k.in(p.gate), inx = k.in(p.x);
         const char *gate = k.tile(step % kStages, 0), *xs = k.tile(step % kStages, 1);

@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
             k.fetch((step + ahead) % kStages, 1, p.x, from, tokens);
             k.fetch((step + ahead) % kStages, 2, p.dh, from, tokens);
         }
-        copies_commit();
+        ptx::copies_commit();
     };
     // the state before token t, where that is one of this lane's
     const auto before = [&](int t, size_t at) {
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
     for (int i = 0; i < kStages; ++i) fetch(0, i);
     if (k.n > 1) ptx::cluster_wait();
     for (int step = 0; step < p.steps; ++step) {
-        copies_wait<kStages - 1>();
+        ptx::copies_wait<kStages - 1>();
         __syncwarp();
         const int tokens = p.T - k.t0, in = k.in(p.gate), inx = k.in(p.x), ind = k.in(p.dh);
         const char *gate = k.tile(step % kStages, 0), *xs = k.tile(step % kStages, 1), *ds = k.tile(step % kStages, 2);

@@ -49,20 +49,6 @@ __device__ __forceinline__ void put(io_t *p, const Vec<2> &x, bool second) {
     }
 }
 
-// `bytes` of the W bytes at src (the rest: zeros) into shared memory, asynchronously.
-template <int W>
-__device__ __forceinline__ void copy_async(uint32_t dst, const char *src, int bytes) {
-    if constexpr (W == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(W) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {   // all but the last N groups
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // R rows (tokens) of a strip of 64 channels in shared memory, and how a warp gets them.  W: 16, 8 or 4
 // bytes a copy, or 2: rows of an odd number of bf16, which start anywhere; the nine 16-byte pieces around
 // a row are copied, and it begins `in` bytes into its place.
@@ -85,7 +71,7 @@ struct Rows {
                 const int in = (int)(reinterpret_cast<uintptr_t>(row) & 15);
                 const int left = r + r0 < n ? in + valid - q : 0;
                 if (lane < 27 && r + r0 < R)
-                    copy_async<16>(dst + (r + r0) * kPitch + q, left > 0 ? row - in + q : start, max(0, min(16, left)));
+                    ptx::copy_async<16>(dst + (r + r0) * kPitch + q, left > 0 ? row - in + q : start, max(0, min(16, left)));
             }
         } else {
             constexpr int per = kRow / W;                 // copies a row
@@ -98,14 +84,14 @@ struct Rows {
                 for (int r = 0; r < R; r += many)
 #pragma unroll
                     for (int t = 0; t < turns; ++t)
-                        copy_async<W>(dst + (r + r0) * kPitch + q + t * 32 * W, p + (size_t)r * pitch + t * 32 * W, W);
+                        ptx::copy_async<W>(dst + (r + r0) * kPitch + q + t * 32 * W, p + (size_t)r * pitch + t * 32 * W, W);
             } else {
 #pragma unroll
                 for (int r = 0; r < R; r += many)
 #pragma unroll
                     for (int t = 0; t < turns; ++t) {
                         const bool there = r + r0 < n && q + t * 32 * W < valid;
-                        copy_async<W>(dst + (r + r0) * kPitch + q + t * 32 * W,
+                        ptx::copy_async<W>(dst + (r + r0) * kPitch + q + t * 32 * W,
                                       there ? p + (size_t)r * pitch + t * 32 * W : src, there ? W : 0);
                     }
             }

@@ -172,20 +172,6 @@ struct Pieces {
     }
 };
 
-// `bytes` of the W bytes at src (the rest: zeros) into shared memory, asynchronously.
-template <int W>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int bytes) {
-    if constexpr (W == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {   // all but the last N groups
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Two values an instruction.
 __device__ __forceinline__ float2 two(float x) { return make_float2(x, x); }
 template <int M>
@@ -373,7 +359,7 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
             const int bytes = P::FULL || n < g.last ? (int)sizeof(raw_t) : ODD && n < g.count ? 2 : 0;
             const io_t *q = base + at + n * g.step;
             if (!P::FULL && !bytes) q = base - g.first;
-            copy_async<sizeof(raw_t)>(to + n * (unsigned)(blockDim.x * sizeof(raw_t)), q, bytes);
+            ptx::copy_async<sizeof(raw_t)>(to + n * (unsigned)(blockDim.x * sizeof(raw_t)), q, bytes);
         }
     };
     const size_t far = (size_t)step * p.C;   // elements from a group's row to its next
@@ -384,7 +370,7 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
             fetch(dy, s, 1, from);
             if (ds) fetch(ds, s, 2, from);
         }
-        copies_commit();   // (a group even of nothing, so that waiting counts them)
+        ptx::copies_commit();   // (a group even of nothing, so that waiting counts them)
     };
     const auto read = [&](int s, int k, int n, float (&v)[EE]) {
         raw_t u[Q];
@@ -427,7 +413,7 @@ __global__ void __launch_bounds__(512) backward_kernel(Params p) {
         const int next = s + 1 >= S ? 0 : s + 1;
         float v[M];
         float2 q[4] = {two(0.0f), two(0.0f), two(0.0f), two(0.0f)};   // sums of v, v^2, u and u v
-        copies_wait<(S > 1 ? S - 2 : 0)>();   // this row's and the next one's (for its pivot)
+        ptx::copies_wait<(S > 1 ? S - 2 : 0)>();   // this row's and the next one's (for its pivot)
 #pragma unroll
         for (int n = 0; n < N; n += Q) {
             float t[EE], d[EE];
