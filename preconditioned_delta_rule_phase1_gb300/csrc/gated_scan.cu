@@ -65,45 +65,41 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
         __syncwarp();
         const int tokens = p.T - k.t0, in = k.in(p.gate), inx = k.in(p.x);
         const char *gate = k.tile(step % kStages, 0), *xs = k.tile(step % kStages, 1);
-        float most = 0.0f;
         raw_t rg[R];
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            rg[i] = rows::get(gate, i, in, k.pitch);
-            const Vec<V> g = wide(rg[i]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) most = fmaxf(most, fabsf(g.v[v]));
-        }
-        // all tokens there, no factor zero and nothing infinite, for the whole warp
-        bool usual = __all_sync(kFullMask, tokens >= R && (most <= kPlainGate || !k.live));
+        for (int i = 0; i < R; ++i) rg[i] = rows::get(gate, i, in, k.pitch);
+        int kind = kind_of<R>(
+            [&](int i) { return wide(rg[i]); }, [&](int i) { return calm(wide(rows::get(xs, i, inx, k.pitch))); }, tokens, k.live);
         Vec<V> co[R], wx[R];
         Vec<V> A = fill<V>(1.0f), D = fill<V>(0.0f), E = D;   // (D: 1 - A)
-        const auto exact = [&](auto z) {
-            constexpr bool Z = decltype(z)::value;
+        const auto exact = [&](auto x_) {
+            constexpr int X = decltype(x_)::value;
+            if (X != kPlain) asm volatile("" ::: "memory");   // (the gates are read again, not kept)
+            A = fill<V>(1.0f), D = E = fill<V>(0.0f);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const Vec<V> g = wide(rg[i]), x = wide(rows::get(xs, i, inx, k.pitch));
+                const Vec<V> g = wide(X == kPlain ? rg[i] : rows::get(gate, i, in, k.pitch));
+                const Vec<V> x = wide(rows::get(xs, i, inx, k.pitch));
+                const bool there = X == kPlain || i < tokens;   // tokens past the end leave everything as it is
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    // tokens past the end leave everything as it is
-                    co[i].v[v] = !Z || i < tokens ? gate_coefficient<Z>(g.v[v]) : kPasses;
-                    wx[i].v[v] = !Z || i < tokens ? weighted<MIX, Z>(co[i].v[v], x.v[v]) : 0.0f;
-                    D.v[v] = decay_rest<Z>(co[i].v[v], A.v[v], D.v[v]);
-                    A.v[v] = decay<Z>(co[i].v[v], A.v[v]);
-                    E.v[v] = decay<Z>(co[i].v[v], E.v[v]) + wx[i].v[v];
+                    co[i].v[v] = there ? gate_coefficient<X>(g.v[v]) : X == kAny ? kPasses : -0.0f;
+                    wx[i].v[v] = there ? weighted<MIX, X>(co[i].v[v], x.v[v]) : 0.0f;
+                    D.v[v] = decay_rest<X>(co[i].v[v], A.v[v], D.v[v]);
+                    A.v[v] = decay<X>(co[i].v[v], A.v[v]);
+                    E.v[v] = decay<X>(co[i].v[v], E.v[v]) + wx[i].v[v];
                 }
             }
         };
-        if constexpr (!kShort) {
-            if (usual) {
-                exact(std::false_type());
-                usual = __all_sync(kFullMask, finite(E));
-                if (!usual) A = fill<V>(1.0f), D = E = fill<V>(0.0f);
-            }
-            if (!usual) exact(std::true_type());
-        } else if (!usual) {
-            exact(std::true_type());
-        } else {
+        if (!kShort && kind == kPlain) {
+            exact(Int<kPlain>());
+            if (!__all_sync(kFullMask, finite(E))) kind = kAny;
+        }
+        if (__builtin_expect(kind == kAny, 0)) {
+            exact(Int<kAny>());
+        } else if (__builtin_expect(kind == kEnds, 0)) {
+            exact(Int<kEnds>());
+        } else if (kShort) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 Vec<V> f;
@@ -125,25 +121,28 @@ __global__ void __launch_bounds__(kThreads, 2) scan_kernel(Params p) {
         unsigned pitch = k.pitch;
         asm volatile("" : "+r"(pitch));
         const Vec<V> before = q;
-        const auto run = [&](auto z) {
-            constexpr bool Z = decltype(z)::value;
-            q = before;
+        const auto run = [&](auto x_) {
+            constexpr int X = decltype(x_)::value;
+            if (!kShort) q = before;
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                if (!Z && kShort) {
+                if (kShort && X == kPlain) {
                     q = fma(q, co[i], wx[i]);
                 } else {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) q.v[v] = decay<Z>(co[i].v[v], q.v[v]) + wx[i].v[v];
+                    for (int v = 0; v < V; ++v) q.v[v] = decay<X>(co[i].v[v], q.v[v]) + wx[i].v[v];
                 }
-                if (k.live && (!Z || i < tokens)) put<rows::kPaired>(reinterpret_cast<io_t *>(out + (size_t)i * pitch), q, k.second);
+                if (k.live && (X == kPlain || i < tokens)) put<rows::kPaired>(reinterpret_cast<io_t *>(out + (size_t)i * pitch), q, k.second);
             }
         };
-        if (usual) {
-            run(std::false_type());
-            if constexpr (!kShort) usual = finite(q);
+        if (__builtin_expect(kind == kPlain, 1)) {
+            run(Int<kPlain>());
+            if (!kShort && !finite(q)) run(Int<kAny>());
+        } else if (kind == kEnds && calm(q)) {
+            run(Int<kEnds>());
+        } else {
+            run(Int<kAny>());
         }
-        if (!usual) run(std::true_type());
         k.t0 += k.stride;
         k.at += far;
     }
@@ -174,8 +173,8 @@ __global__ void __launch_bounds__(128) step_kernel(long long n, const io_t *x, c
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const float c = gate_coefficient<true>(gv[e]);
-        hv[e] = decay<true>(c, hv[e]) + weighted<MIX, true>(c, xv[e]);
+        const float c = gate_coefficient<kAny>(gv[e]);
+        hv[e] = decay<kAny>(c, hv[e]) + weighted<MIX, kAny>(c, xv[e]);
     }
     if (whole) {
         store4(h + i, hv);

@@ -75,11 +75,15 @@ __device__ __forceinline__ float rsqrt_fast(float x) {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------- the exact form
-// In two kinds.  Without Z: no gate beyond kPlainGate, so that no factor leaves fp32's normal range, and
-// nothing infinite (an infinite v becomes NaN, which the recurrence then carries to its end: the callers look
-// there, and do it again with Z).  With Z: any gate, any v.  A factor may then be exactly zero, and hides what
-// it multiplies.  A gate g above kPlainGate is held as c = -g: 1 - a is less than 2^-115, nothing beside any v
-// of the same channel, and what is formed of it comes from e^-g or e^(-g / 2) as it is needed.
+// In kinds, X, by what the callers have looked at:
+//   kPlain  no gate beyond kPlainGate, so that no factor leaves fp32's normal range;
+//   kEnds   or gates of -inf (c = +0) and +inf (c = -0): factors that are exactly zero;
+//   kAny    any gate.  One above kPlainGate is held as c = -g: 1 - a is less than 2^-115, nothing beside any v
+//           of the same channel, and what is formed of it comes from e^-g or e^(-g / 2) as it is needed.
+// A factor that is exactly zero hides what it multiplies.  Only kAny says so: where v is finite it makes no
+// difference, and an infinite v becomes NaN in the others, which the recurrence then carries to its end; the
+// callers look there, and do it again.
+enum { kPlain, kEnds, kAny };
 constexpr float kPlainGate = 80.0f;   // e^80 and its reciprocal are normal numbers
 constexpr float kPasses = -INFINITY;  // c of a gate of +inf
 __device__ __forceinline__ float exp2_whole(float x) {   // with what lies below 2^-126
@@ -87,10 +91,10 @@ __device__ __forceinline__ float exp2_whole(float x) {   // with what lies below
     asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(x));
     return e;
 }
-template <bool Z>
+template <int X>
 __device__ __forceinline__ float gate_coefficient(float g) {
-    if (Z && g > kPlainGate) return -g;
-    const float t = fabsf(g) * -kLog2e, e = Z ? exp2_whole(t) : exp2_fast(t);
+    if (X == kAny && g > kPlainGate) return -g;
+    const float t = fabsf(g) * -kLog2e, e = X == kAny ? exp2_whole(t) : exp2_fast(t);
     return __uint_as_float(__float_as_uint(e * rcp_fast(1.0f + e)) | (~__float_as_uint(g) & 0x80000000u));
 }
 __device__ __forceinline__ bool keeps(float c) { return (int)__float_as_uint(c) < 0; }
@@ -98,16 +102,16 @@ __device__ __forceinline__ bool forgets(float c) { return __float_as_uint(c) == 
 __device__ __forceinline__ bool open(float c) { return c < -1.0f; }                      // c is minus the gate
 
 // a v
-template <bool Z>
+template <int X>
 __device__ __forceinline__ float decay(float c, float v) {
-    if (Z && forgets(c)) return 0.0f;
-    if (Z && (open(c) || (keeps(c) && fabsf(v) == INFINITY))) return v;
+    if (X == kAny && forgets(c)) return 0.0f;
+    if (X == kAny && (open(c) || (keeps(c) && fabsf(v) == INFINITY))) return v;
     return fmaf(c, v, keeps(c) ? v : 0.0f);
 }
 // 1 - A, with its digits, as A becomes a A
-template <bool Z>
+template <int X>
 __device__ __forceinline__ float decay_rest(float c, float A, float D) {
-    if (Z && open(c)) return D;
+    if (X == kAny && open(c)) return D;
     return fmaf(-c, A, keeps(c) ? D : 1.0f);
 }
 template <int V>
@@ -116,20 +120,20 @@ __device__ __forceinline__ bool finite(const Vec<V> &a) {
 }
 // w(a)^2 = 1 - a^2 = s (2 - s), or 1 - s^2
 __device__ __forceinline__ float unit_square(float c) { return fmaf(-c, c, keeps(c) ? -2.0f * c : 1.0f); }
-template <int MIX, bool Z>
+template <int MIX, int X>
 __device__ __forceinline__ float weight(float c) {
     if (MIX == OSDN_MIX_SUM) return 1.0f;
-    if (Z && open(c))   // e^-g, or sqrt(2) e^(-g / 2)
+    if (X == kAny && open(c))   // e^-g, or sqrt(2) e^(-g / 2)
         return MIX == OSDN_MIX_MEAN ? exp2_whole(c * kLog2e) : 1.41421356f * exp2_whole(c * (0.5f * kLog2e));
     if (MIX == OSDN_MIX_MEAN) return keeps(c) ? -c : 1.0f - c;
     return sqrt_fast(unit_square(c));
 }
 // w(a) x
-template <int MIX, bool Z>
+template <int MIX, int X>
 __device__ __forceinline__ float weighted(float c, float x) {
     if (MIX == OSDN_MIX_SUM) return x;
-    const float w = weight<MIX, Z>(c);
-    return Z && w == 0.0f ? 0.0f : w * x;
+    const float w = weight<MIX, X>(c);
+    return X == kAny && w == 0.0f ? 0.0f : w * x;
 }
 // the gate from which on e^-g, or e^(-g / 2) where that counts, is zero in fp32
 template <int MIX>
@@ -138,10 +142,10 @@ __device__ __forceinline__ constexpr float zero_from() { return MIX == OSDN_MIX_
 // a b (v - k x), where k is 0, 1 or a / w.  (w' = -a / w times a b, and k a b = a^2 sqrt((1 - a) /
 // (1 + a)) goes to zero where w does.)
 // a b and k a b
-template <int MIX, bool Z>
+template <int MIX, int X>
 __device__ __forceinline__ void slope_factors(float c, float &ab, float &kab) {
     const float s = fabsf(c);
-    if (Z && open(c)) {
+    if (X == kAny && open(c)) {
         ab = c > -104.0f ? exp2_whole(c * kLog2e) : 0.0f;
         if (c <= -zero_from<MIX>()) { kab = 0.0f; return; }
         kab = MIX == OSDN_MIX_UNIT ? 0.70710678f * exp2_whole(c * (0.5f * kLog2e)) : MIX == OSDN_MIX_MEAN ? ab : 0.0f;
@@ -149,14 +153,14 @@ __device__ __forceinline__ void slope_factors(float c, float &ab, float &kab) {
     }
     ab = fmaf(-s, s, s);
     // (k a b first: k alone can be large, and with a large x leave fp32)
-    kab = MIX == OSDN_MIX_UNIT ? (keeps(c) ? 1.0f + c : c) * (ab * rsqrt_fast(unit_square(c)))
+    kab = MIX == OSDN_MIX_UNIT ? (keeps(c) ? 1.0f + c : c) * (ab * rsqrt_fast(X == kEnds ? fmaxf(unit_square(c), 1e-37f) : unit_square(c)))
                                : MIX == OSDN_MIX_MEAN ? ab : 0.0f;
 }
-template <int MIX, bool Z>
+template <int MIX, int X>
 __device__ __forceinline__ float slope_of(float c, float v, float x) {
     float ab, kab;
-    slope_factors<MIX, Z>(c, ab, kab);
-    if (Z) {
+    slope_factors<MIX, X>(c, ab, kab);
+    if (X == kAny) {
         const float y = kab == 0.0f ? 0.0f : -kab * x;
         return ab == 0.0f ? y : fmaf(ab, v, y);
     }
@@ -166,7 +170,7 @@ __device__ __forceinline__ float slope_of(float c, float v, float x) {
 }
 // whether the gradient of g is zero whatever R is
 template <int MIX>
-__device__ __forceinline__ bool no_slope(float c) { return forgets(c) || c <= -zero_from<MIX>(); }
+__device__ __forceinline__ bool no_slope(float c) { return c == 0.0f || c <= -zero_from<MIX>(); }
 
 // ------------------------------------------------------------- the short form
 // e^-g, and from it a and b = 1 - a

@@ -66,50 +66,50 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
         __syncwarp();
         const int tokens = p.T - k.t0, in = k.in(p.gate), inx = k.in(p.x), ind = k.in(p.dh);
         const char *gate = k.tile(step % kStages, 0), *xs = k.tile(step % kStages, 1), *ds = k.tile(step % kStages, 2);
-        float most = 0.0f;
         raw_t rg[R];
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            rg[i] = rows::get(gate, i, in, k.pitch);
-            const Vec<V> g = wide(rg[i]);
-#pragma unroll
-            for (int v = 0; v < V; ++v) most = fmaxf(most, fabsf(g.v[v]));
-        }
-        bool usual = __all_sync(kFullMask, tokens >= R && (most <= kPlainGate || !k.live));
-        Vec<V> h = wide(row);
-        if (k.t0 == 0) h = k.load_state(p, p.h0);
-        const Vec<V> first = h;
+        for (int i = 0; i < R; ++i) rg[i] = rows::get(gate, i, in, k.pitch);
+        const auto state_before = [&] { return k.t0 == 0 ? k.load_state(p, p.h0) : wide(row); };
+        Vec<V> h = state_before();
+        const bool calm_state = calm(h);
+        int kind = kind_of<R>(
+            [&](int i) { return wide(rg[i]); },
+            [&](int i) { return calm_state && calm(wide(rows::get(xs, i, inx, k.pitch))) && calm(wide(rows::get(ds, i, ind, k.pitch))); },
+            tokens, k.live);
         Vec<V> co[R], slope[R];   // (co: c, or e^-g in the short form)
         raw_t d[R];
         Vec<V> A = fill<V>(1.0f), D = fill<V>(0.0f), E = D;   // (D: 1 - A)
-        const auto exact = [&](auto z) {
-            constexpr bool Z = decltype(z)::value;
+        const auto exact = [&](auto x_) {
+            constexpr int X = decltype(x_)::value;
+            if (X != kPlain) asm volatile("" ::: "memory");   // (the gates are read again, not kept)
+            h = state_before(), A = fill<V>(1.0f), D = E = fill<V>(0.0f);
 #pragma unroll
             for (int i = 0; i < R; ++i) {
-                const Vec<V> g = wide(rg[i]), x = wide(rows::get(xs, i, inx, k.pitch));
+                const Vec<V> g = wide(X == kPlain ? rg[i] : rows::get(gate, i, in, k.pitch));
+                const Vec<V> x = wide(rows::get(xs, i, inx, k.pitch));
+                const bool there = X == kPlain || i < tokens;
                 d[i] = rows::get(ds, i, ind, k.pitch);
                 const Vec<V> di = wide(d[i]);
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    co[i].v[v] = !Z || i < tokens ? gate_coefficient<Z>(g.v[v]) : kPasses;
-                    slope[i].v[v] = slope_of<MIX, Z>(co[i].v[v], h.v[v], x.v[v]);
-                    h.v[v] = decay<Z>(co[i].v[v], h.v[v]) + (!Z || i < tokens ? weighted<MIX, Z>(co[i].v[v], x.v[v]) : 0.0f);
-                    D.v[v] = decay_rest<Z>(co[i].v[v], A.v[v], D.v[v]);
-                    A.v[v] = decay<Z>(co[i].v[v], A.v[v]);
-                    E.v[v] = Z && A.v[v] == 0.0f ? E.v[v] : fmaf(A.v[v], di.v[v], E.v[v]);
+                    co[i].v[v] = there ? gate_coefficient<X>(g.v[v]) : X == kAny ? kPasses : -0.0f;
+                    slope[i].v[v] = slope_of<MIX, X>(co[i].v[v], h.v[v], x.v[v]);
+                    h.v[v] = decay<X>(co[i].v[v], h.v[v]) + (there ? weighted<MIX, X>(co[i].v[v], x.v[v]) : 0.0f);
+                    D.v[v] = decay_rest<X>(co[i].v[v], A.v[v], D.v[v]);
+                    A.v[v] = decay<X>(co[i].v[v], A.v[v]);
+                    E.v[v] = X == kAny && A.v[v] == 0.0f ? E.v[v] : fmaf(A.v[v], di.v[v], E.v[v]);
                 }
             }
         };
-        if constexpr (!kShort) {
-            if (usual) {
-                exact(std::false_type());
-                usual = __all_sync(kFullMask, finite(h) && finite(E));
-                if (!usual) h = first, A = fill<V>(1.0f), D = E = fill<V>(0.0f);
-            }
-            if (!usual) exact(std::true_type());
-        } else if (!usual) {
-            exact(std::true_type());
-        } else {
+        if (!kShort && kind == kPlain) {
+            exact(Int<kPlain>());
+            if (!__all_sync(kFullMask, finite(h) && finite(E))) kind = kAny;
+        }
+        if (__builtin_expect(kind == kAny, 0)) {
+            exact(Int<kAny>());
+        } else if (__builtin_expect(kind == kEnds, 0)) {
+            exact(Int<kEnds>());
+        } else if (kShort) {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 Vec<V> a, f;
@@ -133,9 +133,9 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
         unsigned pitch = k.pitch;
         asm volatile("" : "+r"(pitch));
         const Vec<V> behind = q;
-        const auto run = [&](auto z) {
-            constexpr bool Z = decltype(z)::value;
-            q = behind;
+        const auto run = [&](auto x_) {
+            constexpr int X = decltype(x_)::value;
+            if (!kShort) q = behind;
 #pragma unroll
             for (int i = R - 1; i >= 0; --i) {
                 const Vec<V> r = add(wide(d[i]), q);
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
                 // a and w again, rather than kept from above: registers for more tokens are worth more
 #pragma unroll
                 for (int v = 0; v < V; ++v) asm volatile("" : "+f"(co[i].v[v]));
-                if (!Z && kShort) {
+                if (kShort && X == kPlain) {
                     Vec<V> a, f;
                     sigmoids(co[i], a, f);
                     w = weight<MIX>(a, f);
@@ -151,29 +151,32 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
                 } else {
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
-                        w.v[v] = weight<MIX, Z>(co[i].v[v]);
-                        q.v[v] = decay<Z>(co[i].v[v], r.v[v]);
+                        w.v[v] = weight<MIX, X>(co[i].v[v]);
+                        q.v[v] = decay<X>(co[i].v[v], r.v[v]);
                     }
                 }
                 Vec<V> gx = MIX == OSDN_MIX_SUM ? r : mul(w, r), gg = mul(slope[i], r);
-                if constexpr (Z) {   // factors that are exactly zero hide r
+                if constexpr (X == kAny) {   // factors that are exactly zero hide r
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
                         if (w.v[v] == 0.0f) gx.v[v] = 0.0f;
                         if (no_slope<MIX>(co[i].v[v])) gg.v[v] = 0.0f;
                     }
                 }
-                if (k.live && (!Z || i < tokens)) {
+                if (k.live && (X == kPlain || i < tokens)) {
                     put<rows::kPaired>(reinterpret_cast<io_t *>(dx + (size_t)i * pitch), gx, k.second);
                     put<rows::kPaired>(reinterpret_cast<io_t *>(dg + (size_t)i * pitch), gg, k.second);
                 }
             }
         };
-        if (usual) {
-            run(std::false_type());
-            if constexpr (!kShort) usual = finite(q);
+        if (__builtin_expect(kind == kPlain, 1)) {
+            run(Int<kPlain>());
+            if (!kShort && !finite(q)) run(Int<kAny>());
+        } else if (kind == kEnds && calm(q)) {
+            run(Int<kEnds>());
+        } else {
+            run(Int<kAny>());
         }
-        if (!usual) run(std::true_type());
         k.t0 -= k.stride;
         k.at -= far;
     }

@@ -135,7 +135,7 @@ __device__ __forceinline__ Vec<2> unit(const Vec<2> &c) { return {{c.v[0] < 0.0f
 // stays as it is.
 __device__ __forceinline__ Vec<2> through(const Pair &b, const Vec<2> &s) { return fma(b.c, s, fma(unit(b.c), s, b.E)); }
 __device__ __forceinline__ Vec<2> through_exact(const Pair &b, const Vec<2> &s) {
-    return {{decay<true>(b.c.v[0], s.v[0]) + b.E.v[0], decay<true>(b.c.v[1], s.v[1]) + b.E.v[1]}};
+    return {{decay<kAny>(b.c.v[0], s.v[0]) + b.E.v[0], decay<kAny>(b.c.v[1], s.v[1]) + b.E.v[1]}};
 }
 
 // Where a step's pairs meet; one set for even and one for odd steps, so that a step's barriers are
@@ -292,6 +292,35 @@ struct Walk {
     }
 };
 
+// Values of this size and less stay finite over a warp's tokens, whatever the gates.
+constexpr float kCalm = 1e36f;
+__device__ __forceinline__ bool calm(const Vec<2> &a) { return fabsf(a.v[0]) <= kCalm && fabsf(a.v[1]) <= kCalm; }
+// The arithmetic that a warp's tokens ask for (gated_scan.cuh): kPlain, by the gates alone; kEnds, where some
+// gates are infinite or some tokens past the end, and all values calm; else kAny.  (kAny is several times the
+// instructions, and one warp of it in a step holds up its cluster: 306 us at 1x65536x2048 with documents of 3000
+// tokens, with kEnds 210 us.)
+template <int R, typename F, typename G>
+__device__ __forceinline__ int kind_of(const F &gate, const G &values, int tokens, bool live) {
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const Vec<2> g = gate(i);
+        most = fmaxf(most, fmaxf(fabsf(g.v[0]), fabsf(g.v[1])));
+    }
+    if (__builtin_expect(__all_sync(kFullMask, tokens >= R && (most <= kPlainGate || !live)), 1)) return kPlain;
+    bool ends = true;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const Vec<2> g = gate(i);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) ends &= fabsf(g.v[v]) <= kPlainGate || fabsf(g.v[v]) == INFINITY;
+        ends &= values(i);
+    }
+    return __all_sync(kFullMask, ends || !live) ? kEnds : kAny;
+}
+template <int X>
+using Int = std::integral_constant<int, X>;
+
 // f(type tag, mix tag) for the call's type and mix
 template <typename F>
 cudaError_t with_types(int io, int mix, const F &f) {
@@ -348,8 +377,6 @@ cudaError_t launch_as(void (*kernel)(Params), std::atomic<unsigned long long> &d
     c.numAttrs = pl.n > 1;
     return cudaLaunchKernelEx(&c, kernel, p);
 }
-template <int X>
-using Int = std::integral_constant<int, X>;
 // f(R tag, W tag) for a plan of at most MOST tokens a warp, of rows of odd bf16 at most ODD
 template <typename io_t, int MOST, int ODD, typename F>
 cudaError_t with_rows(const Plan &pl, const F &f) {
