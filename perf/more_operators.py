@@ -237,8 +237,9 @@ def run(s):
         h, hT = ops.gated_scan(s["x"], s["gate"], s["h0"], mix=case["mix"], workspace=ws)
         return {"h": h, "hT": hT}
     if op == "scan_train":
-        return ops.gated_scan_backward(s["x"], s["gate"], s["h"], s["h0"], dh=s["dh"], dhT=s["dhT"],
-                                       mix=case["mix"], workspace=ws)
+        # (in fp32 the plain recurrence may leave h as a slice; the call reads it densely)
+        return ops.gated_scan_backward(s["x"], s["gate"], s["h"].contiguous(), s["h0"], dh=s["dh"],
+                                       dhT=s["dhT"], mix=case["mix"], workspace=ws)
     if op == "step":
         return {"y": ops.gated_scan_step(s["x"], s["gate"], s["h"], mix=case["mix"]), "h": s["h"]}
     if op == "norm":
