@@ -633,7 +633,11 @@ int osdn_gated_scan_step(int io, int B, int C, int mix, const void *x, const voi
  * -a^2 sqrt((1 - a) / (1 + a)) by mix.  Factors that are zero hide as above
  * (d_h is read at every token: a padded place has to hold zeros).
  *   h    in  [B][T][C] io: what osdn_gated_scan wrote for these inputs.  The
- *            states are recomputed in fp32 from rows of it some tokens apart
+ *            states are recomputed in fp32 from a row of it every 4, 8 or 16
+ *            tokens.  With bf16 I/O such a row is off by half a step of its own,
+ *            2^-9 to 2^-8 of it, and so is, at most and less with every token
+ *            behind it, the h_{t-1} of dgate: R a (1 - a) times that, about as
+ *            much as dgate's own rounding (dx and dh0 do not read states)
  *   d_h  in  [B][T][C] io       d_hT in [B][C] fp32, or NULL (zeros)
  *   dx, dgate out [B][T][C] io  dh0 out [B][C] fp32, or NULL (not written)
  * The rest, and the limits, as osdn_gated_scan; with T == 0 the call writes
@@ -654,7 +658,7 @@ int osdn_gated_scan_backward(int io, int B, int T, int C, int mix, const void *x
  *   y        out [rows][C] io
  *   sum      out [rows][C] io: s; given exactly if residual is
  * C is from 1 to 16384, rows below 2^31; eps > 0 and finite.  The squares of
- * the differences to the row's first value have to fit fp32.
+ * the differences to the row's first value, and their sum, have to fit fp32.
  */
 int osdn_layer_norm(int io, long long rows, int C, const void *x, const void *residual, const float *weight,
                     const float *bias, float eps, void *y, void *sum, void *stream);

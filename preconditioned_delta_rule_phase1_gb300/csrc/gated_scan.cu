@@ -5,8 +5,9 @@
 //     dx_t = w(a_t) R_t,   dgate_t = R_t (a_t (1 - a_t) h_{t-1} + w'_t x_t)
 //
 // Both directions are a recurrence s <- a s + e of every channel, and runs of
-// it compose: (A, E) after (A', E') is (A A', A E' + E).  The tensors are read
-// and written once, so HBM bounds them.  A warp holds R tokens of 32 lanes'
+// it compose: (A, E) after (A', E') is (A A', A E' + E), with A held so that 1 - A
+// keeps its digits (gated_scan_walk.cuh).  The tensors are read and written once,
+// so HBM is what they cannot do without.  A warp holds R tokens of 32 lanes'
 // channels (two a lane) in registers, a CTA kWarps warps one
 // behind the other in time.  A strip of channels belongs to a cluster of up to
 // eight CTAs, which walks the sequence, each step a run of tokens a CTA:
@@ -21,11 +22,11 @@
 // it copied itself.  Nothing leaves the cluster, so there is no workspace and
 // nothing to wait for but its own barrier.  Every fold is in a fixed order.
 //
-// Measured (bf16, mean): 42 us at 16x1024x2048, where a CTA walks a strip alone
-// (4.8 TB/s, 0.71 of the measured copy bandwidth), 50 us at 2x8192x2048 in
-// clusters of four (0.60) and 181 us at 1x65536x2048 in clusters of eight
-// (0.66); fp32 46 us at 2x4096x2048.  34 to 40 instructions a token and warp at
-// 16 warps an SM (128 registers) take 0.42 to 0.49 of the issue slots; the rest
+// Measured (bf16, mean): 43 us at 16x1024x2048, where a CTA walks a strip alone
+// (4.7 TB/s, 0.69 of the measured copy bandwidth), 52 us at 2x8192x2048 in
+// clusters of four (0.57) and 193 us at 1x65536x2048 in clusters of eight
+// (0.62); fp32 51 us at 2x4096x2048.  38 to 45 instructions a token and warp at
+// 16 warps an SM (128 registers) take 0.43 to 0.49 of the issue slots; the rest
 // is a step's latency, about 2 us in a cluster of eight that has its SMs to
 // itself.  Joining through a chain of clusters in global memory took 118 us at
 // 2x8192x2048, eight tokens a warp in place of 16 66 us.

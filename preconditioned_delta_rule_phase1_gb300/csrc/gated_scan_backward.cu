@@ -1,10 +1,11 @@
 // gated_scan_backward.cu -- the gradients of the gated recurrence; gated_scan.cu
 // has the formulas and the design.
 //
-// Measured (bf16, 2x8192x2048, five tensors of 67 MB): sum 70, unit 87, mean 89
-// us (0.70, 0.57 and 0.56 of the measured copy bandwidth); fp32 66 us at
-// 2x4096x2048, mean.  Bound by instruction issue (0.45 of the slots at 16 warps
-// an SM) and a step's latency.  Only e^-g and the slope of the gate stay in
+// Measured (bf16, 2x8192x2048, five tensors of 67 MB): sum 70, unit 89, mean 90
+// us (0.71, 0.56 and 0.55 of the measured copy bandwidth); fp32 67 us at
+// 2x4096x2048, mean.  Neither issue (0.46 of the slots at 16 warps an SM) nor HBM
+// (0.45) is full: a step's latency is what counts, its barriers first (2.2 warps
+// wait there for each one that issues).  Only e^-g and the slope of the gate stay in
 // registers between the two passes over a thread's tokens; with a and w kept
 // too there is room for eight tokens in place of 16 (sum 93 us).
 #include "gated_scan_walk.cuh"

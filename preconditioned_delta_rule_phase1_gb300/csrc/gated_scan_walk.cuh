@@ -112,8 +112,8 @@ struct Rows {
 // What a run of tokens does to a lane's channels, s <- A s + E.  A is held as one signed number c, as a gate
 // is (gated_scan.cuh): -(1 - A) where that is small, with its digits, else A.  An A near 1 that is rounded to
 // fp32 takes up to 2^-25 of the state with it, or adds as much, at every run, and to the same side where gates
-// are constant.  (Measured, 2x8192x2048 bf16: 50 us either way, gradients 89 us either way with mean, 70 for 68
-// us with sum and 87 for 85 us with unit.)
+// are constant.  (Measured, 2x8192x2048 bf16: 50 us either way, gradients 89 us either way with mean, 70
+// for 68 us with sum and 87 for 85 us with unit.)
 constexpr float kNear = 0.125f;   // (eight factors of 1 - kNear are still 0.34: see join)
 struct alignas(16) Pair {
     Vec<2> c, E;

@@ -13,13 +13,16 @@
 // sums in one.  A row whose first value is an outlier (kFarSquare) takes them
 // again about its mean.  All arithmetic is fp32.
 //
-// Measured (bf16): the norm 48 us at 16384 rows of 2048 with a residual (5.6
-// TB/s, 0.83 of the measured copy bandwidth; 45 us among other calls), 125 us
-// at rows of 2047 (instruction issue: words, and masks at both ends); its
-// gradients with ds 64 us at 16384x2048 (0.62), 26 us at 8193x1024, 77 us at
-// 1024x16384, bound by instruction issue (0.5 of the slots at 16 warps an SM,
-// 460 instructions a warp and row of 2048).  Gradients with two
-// reductions a row took 72 us, without loads ahead 88 us.
+// Measured (bf16): the norm 47 us at 16384 rows of 2048 with a residual (5.7
+// TB/s, 0.84 of the measured copy bandwidth; 45 us among other calls), 130 us
+// at rows of 2047 (words, and masks at both ends); its gradients with ds 56 us
+// at 16384x2048 (0.71), where nothing is full (0.54 of the issue slots at 16
+// warps an SM, 430 instructions a warp and row; 0.67 of HBM) and a row's way
+// through barrier, shared memory and arithmetic is what counts, 26 us at
+// 8193x1024 (0.38) and 78 us at 1024x16384 (0.25: one row ahead, sums in shared
+// memory, the weight read twice a row).  Gradients with two reductions a row
+// took 72 us, without loads ahead 88 us, where one reduction and three rows
+// ahead took 66.
 #include <algorithm>
 #include <type_traits>
 
@@ -316,12 +319,14 @@ __global__ void __launch_bounds__(N * E == 8 ? 1024 : N * E == 16 ? 128 : 512) n
 }
 
 // Groups of p.warps warps walk rows; the sums over rows stay with the threads that own the columns,
-// in registers or (SMEM, wide rows) in shared memory, and end as one share a CTA.  The next S rows are
-// on their way into shared memory meanwhile; a thread reads only what it copied itself.  With kOdd a
+// in registers or (SMEM, wide rows) in shared memory, and end as one share a CTA.  Rows come into shared
+// memory by asynchronous copies, S at a time; a thread reads only what it copied itself.  With kOdd a
 // group keeps to rows of one parity, which begin in the same place of a word, so that its columns stay
 // its own.
-// Rows ahead, by what 227 KB of shared memory hold beside the sums (none: 16384 channels of fp32, which
-// are read when they are needed).
+// S, by what 227 KB of shared memory hold beside the sums: three rows of up to 16 values a thread in bf16
+// and 8 in fp32, of which two are under way while one is worked on; one of 32 in bf16 and 16 in fp32, whose
+// copy begins when the row before it is done, so that every row waits for memory; none of 32 in fp32, which
+// are read when they are needed.
 template <typename io_t, int M>
 struct Ahead {
     static constexpr bool kSmem = M == 32;
