@@ -138,10 +138,9 @@ __device__ __forceinline__ float weighted(float c, float x) {
 // the gate from which on e^-g, or e^(-g / 2) where that counts, is zero in fp32
 template <int MIX>
 __device__ __forceinline__ constexpr float zero_from() { return MIX == OSDN_MIX_UNIT ? 208.0f : 104.0f; }
-// With v the state before a token: the factor that turns R into the gradient of g, a b v + w' x =
+// With v the state before a token, the factor that turns R into the gradient of g is a b v + w' x =
 // a b (v - k x), where k is 0, 1 or a / w.  (w' = -a / w times a b, and k a b = a^2 sqrt((1 - a) /
-// (1 + a)) goes to zero where w does.)
-// a b and k a b
+// (1 + a)) goes to zero where w does.)  Here a b and k a b:
 template <int MIX, int X>
 __device__ __forceinline__ void slope_factors(float c, float &ab, float &kab) {
     const float s = fabsf(c);
@@ -160,13 +159,12 @@ template <int MIX, int X>
 __device__ __forceinline__ float slope_of(float c, float v, float x) {
     float ab, kab;
     slope_factors<MIX, X>(c, ab, kab);
+    if (MIX == OSDN_MIX_MEAN) return X == kAny && ab == 0.0f ? 0.0f : ab * (v - x);
     if (X == kAny) {
         const float y = kab == 0.0f ? 0.0f : -kab * x;
         return ab == 0.0f ? y : fmaf(ab, v, y);
     }
-    if (MIX == OSDN_MIX_SUM) return ab * v;
-    if (MIX == OSDN_MIX_MEAN) return ab * (v - x);
-    return fmaf(ab, v, -kab * x);
+    return MIX == OSDN_MIX_SUM ? ab * v : fmaf(ab, v, -kab * x);
 }
 // whether the gradient of g is zero whatever R is
 template <int MIX>

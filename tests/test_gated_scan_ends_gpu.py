@@ -106,3 +106,18 @@ def test_what_a_finite_gate_does_not_hide(io, mix):
     assert bool((ops.gated_scan(x, gate, h0, mix=mix)[1] == float("inf")).all())
     ops.gated_scan_step(x[:, 0].clone(), gate[:, 0].clone(), h0, mix=mix)
     assert bool((h0 == float("inf")).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_a_far_gate_leaves_its_neighbours_as_they_are(io):
+    """A weighted mean of what the state is already does not move: dgate is zero, exactly, whatever form of
+    the arithmetic another channel's gate asks for."""
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(1, 1, 64, generator=g).to(DT[io]).cuda()
+    gate = torch.randn(1, 1, 64, generator=g).to(DT[io]).cuda()
+    h0 = x[:, 0].float()
+    for far in (0.0, float("inf"), 90.0, 150.0, -95.0):
+        gate[0, 0, 7] = far
+        h, _ = ops.gated_scan(x, gate, h0, mix="mean")
+        got = ops.gated_scan_backward(x, gate, h, h0, dh=torch.ones_like(x), mix="mean")
+        assert not got["gate"].any(), far
