@@ -191,9 +191,21 @@ __device__ __forceinline__ Vec<2> join(Join &j, int set, int n, int rank, int pl
             if (P.v[i] != 0.0f && -C.v[i] < kNear) sum.c.v[i] = near_one(-C.v[i]);
     }
     if (!finite(E) || (last && !finite(sum.E))) {
+        // exactly; an A of zero is zero before and behind a gate of NaN, too
         E = zero;
-        for (int w = 0; w < place; ++w) E = through_exact(j.warp[set][w][lane], E);
-        if (last) sum.E = through_exact(own, E);
+        for (int w = 0; w < place; ++w) {
+            const Pair b = j.warp[set][w][lane];
+            E = through_exact(b, E);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (forgets(b.c.v[i])) A.v[i] = sum.c.v[i] = 0.0f;
+        }
+        if (last) {
+            sum.E = through_exact(own, E);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (forgets(own.c.v[i])) sum.c.v[i] = 0.0f;
+        }
     }
     Vec<2> mine = s;
     if (n > 1) {

@@ -165,3 +165,36 @@ def test_infinite_cotangents_and_states_backwards(io, mix, kind, T):
     sure |= dg.isnan()
     assert torch.equal((got["gate"].double() == INF)[sure], (dg == INF)[sure])
     assert torch.equal(got["gate"].isnan()[sure], dg.isnan()[sure])
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("mix", MIXES)
+@pytest.mark.parametrize("T", [1, 6, 300, 2000])
+def test_a_gate_of_nan_reaches_its_channel_until_a_restart(io, mix, T):
+    C, at = 34, T // 3
+    g = torch.Generator().manual_seed(T)
+    x, dh = (torch.randn(2, T, C, generator=g).to(DT[io]).cuda() for _ in range(2))
+    h0, dhT = (torch.randn(2, C, generator=g).cuda() for _ in range(2))
+    gate = gates(2, T, C, io, "mixed")
+    gate[1, at, 5] = math.nan
+    if T > 5:
+        gate[:, at + 3] = -INF
+    ref, _ = forward64(x.double(), gate.double(), h0.double(), mix)
+    h, hT = ops.gated_scan(x, gate, h0, mix=mix)
+    assert torch.equal(h.isnan(), ref.isnan()) and int(h.isnan().sum()) == min(3, T - at)
+    same(h, ref, HALF[io], "h")
+    same(hT, ref[:, -1], 2.0 ** -24, "hT", among=ref)
+    got = ops.gated_scan_backward(x, gate, h, h0, dh=dh, dhT=dhT, mix=mix)
+    # R of the tokens before is NaN, w and the slope of the token itself are, and the slopes behind it
+    w = torch.ones(T, dtype=torch.bool, device="cuda")
+    before, after = w.clone(), w.clone()
+    before[at:], after[:at + 1], after[at + 3:] = False, False, False   # (the restart's own slope is zero)
+    want = torch.zeros(2, T, C, dtype=torch.bool, device="cuda")
+    want[1, :, 5] = before
+    if mix != "sum":
+        want[1, at, 5] = True
+    assert torch.equal(got["x"].isnan(), want)
+    want[1, at, 5] = True
+    want[1, :, 5] |= after
+    assert torch.equal(got["gate"].isnan(), want)
+    assert int(got["h0"].isnan().sum()) == 1 and bool(got["h0"][1, 5].isnan())
