@@ -105,7 +105,7 @@ __device__ __forceinline__ bool open(float c) { return c < -1.0f; }             
 template <int X>
 __device__ __forceinline__ float decay(float c, float v) {
     if (X == kAny && forgets(c)) return 0.0f;
-    if (X == kAny && (open(c) || (keeps(c) && fabsf(v) == INFINITY))) return v;
+    if (X == kAny && (open(c) || (c <= 0.0f && fabsf(v) == INFINITY))) return v;   // (a NaN is neither)
     return fmaf(c, v, keeps(c) ? v : 0.0f);
 }
 // 1 - A, with its digits, as A becomes a A

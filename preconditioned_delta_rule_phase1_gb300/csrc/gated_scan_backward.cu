@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads, 2) backward_kernel(Params p) {
                     slope[i].v[v] = slope_of<MIX, X>(co[i].v[v], h.v[v], x.v[v]);
                     h.v[v] = decay<X>(co[i].v[v], h.v[v]) + (there ? weighted<MIX, X>(co[i].v[v], x.v[v]) : 0.0f);
                     D.v[v] = decay_rest<X>(co[i].v[v], A.v[v], D.v[v]);
-                    A.v[v] = decay<X>(co[i].v[v], A.v[v]);
+                    if (X != kAny || A.v[v] != 0.0f) A.v[v] = decay<X>(co[i].v[v], A.v[v]);
                     E.v[v] = X == kAny && A.v[v] == 0.0f ? E.v[v] : fmaf(A.v[v], di.v[v], E.v[v]);
                 }
             }

@@ -198,3 +198,39 @@ def test_a_gate_of_nan_reaches_its_channel_until_a_restart(io, mix, T):
     want[1, :, 5] |= after
     assert torch.equal(got["gate"].isnan(), want)
     assert int(got["h0"].isnan().sum()) == 1 and bool(got["h0"][1, 5].isnan())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("mix", MIXES)
+@pytest.mark.parametrize("T,C,B", [(1, 33, 3), (4, 5, 180), (6, 33, 5), (16, 64, 4), (40, 130, 2), (100, 34, 3), (700, 20, 2)])
+def test_infinities_nan_and_restarts_together(io, mix, T, C, B):
+    """Gates of +-inf, NaN and 90 and infinite or NaN values, all over a call: the same ones come out, at the
+    same places.  (The gates between are open enough for their product to stay in fp32.)"""
+    for seed in range(4):
+        g = torch.Generator().manual_seed(seed * 1000 + T)
+        some = lambda p, *s: torch.rand(*s, generator=g) < p  # noqa: E731
+        gate = (1 if T < 200 else 4) + 4 * torch.rand(B, T, C, generator=g)
+        gate = torch.where(some(0.04, B, T, 1), -INF, gate)
+        if seed % 2:
+            gate = torch.where(some(0.1, B, T, 1), INF, gate)
+        gate = torch.where(some(0.01, B, T, C), math.nan, gate)
+        gate = torch.where(some(0.02, B, T, C), 90.0, gate)
+        x, dh = (torch.randn(B, T, C, generator=g) for _ in range(2))
+        h0, dhT = (torch.randn(B, C, generator=g) for _ in range(2))
+        for i, t in enumerate((x, dh, h0, dhT)):
+            for k, v in enumerate((INF, -INF, math.nan)):
+                if (seed + i + k) % 3 == 0:
+                    t[some(0.03, *t.shape)] = v
+        x, dh, gate, h0, dhT = x.to(DT[io]).cuda(), dh.to(DT[io]).cuda(), gate.to(DT[io]).cuda(), h0.cuda(), dhT.cuda()
+        ref, _ = forward64(x.double(), gate.double(), h0.double(), mix)
+        h, hT = ops.gated_scan(x, gate, h0, mix=mix)
+        same(h, ref, HALF[io], ("h", seed))
+        same(hT, ref[:, -1], 2.0 ** -24, ("hT", seed), among=ref)
+        got = ops.gated_scan_backward(x, gate, h, h0, dh=dh, dhT=dhT, mix=mix)
+        dx, dg, dh0, sure = backward64(x.double(), gate.double(), h0.double(), mix, dh.double(), dhT.double(), HALF[io])
+        for name, a, b in (("x", got["x"], dx), ("h0", got["h0"], dh0)):
+            assert torch.equal(a.isnan(), b.isnan()), (name, seed)
+            assert torch.equal(a.double() == INF, b == INF) and torch.equal(a.double() == -INF, b == -INF), (name, seed)
+        sure |= dg.isnan()
+        assert torch.equal(torch.isfinite(got["gate"])[sure], torch.isfinite(dg)[sure]), seed
+        assert torch.equal((got["gate"].double() == INF)[sure], (dg == INF)[sure]), seed
